@@ -61,6 +61,9 @@ SIGNATURES = {
                                                _i64, _c_int, _p]),
     "bsf_grouped_gemm_nvfp4_masked": (_c_int, [_p, _p, _i64, _c_int, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
                                                _i64, _c_int, _p]),
+    "bsf_gate": (_c_int, [_p, _c_int, _i64, _i64, _i64, _p, _i64, _i64, _i64, _c_int, ctypes.c_float, _p, _p, _p]),
+    "bsf_swiglu_quantise": (_c_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p]),
+    "bsf_dense_gemm": (_c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p]),
 }
 
 _LIB = None

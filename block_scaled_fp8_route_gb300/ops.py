@@ -423,3 +423,133 @@ def grouped_gemm_f32sf_masked(a, sfa, b, sfb, masked_m, max_m, d=None, expected_
         _ptr(a), _ptr(sfa), sfa.shape[1], _wptr(b, flags), _wptr(sfb, flags), _ptr(d), _ptr(masked_m), E, max_m, N, K, expected_m,
         flags, _stream(stream)), "grouped_gemm_f32sf_masked")
     return d
+
+
+# ----------------------------------------------------------------------------- around the expert path
+GATE_SIGMOID = 0x1
+GATE_GROUP_TOP2 = 0x2
+GATE_RENORMALISE = 0x4
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}       # BSF_TYPE_F32, BSF_TYPE_BF16
+
+
+def _dptr(t, dtype, what):
+    """Address of a CUDA tensor of the given type whose rows are contiguous."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
+    return t.data_ptr()
+
+
+def _row_stride(t, what):
+    """Row stride of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _whole(t, shape, what):
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, group_score="max", renormalise=True,
+         scale=1.0, topk_ids=None, topk_weights=None, stream=None):
+    """Router logits [T, E] (float32 or bf16, any row stride) -> (topk_ids int32 [T, kr], topk_weights
+    float32 [T, kr]) for ``route`` / ``dispatch`` / ``combine``.  ``score`` "softmax" or "sigmoid"; with
+    ``bias`` float32 [E] the choice goes by score + bias; of ``groups`` groups of experts only the
+    ``kept_groups`` best take part (``group_score`` "max" or "top2"); ids of -1 where too few experts can
+    be chosen (a logit of -inf or NaN masks its expert)."""
+    if logits.dtype not in _TYPES:
+        raise ValueError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
+    if score not in ("softmax", "sigmoid") or group_score not in ("max", "top2"):
+        raise ValueError(f"score {score!r} / group_score {group_score!r}: expected softmax or sigmoid / max or top2")
+    ld = _row_stride(logits, "logits")
+    T, E = logits.shape
+    if topk_ids is None:
+        topk_ids = torch.empty((T, kr), dtype=torch.int32, device=logits.device)
+    if topk_weights is None:
+        topk_weights = torch.empty((T, kr), dtype=torch.float32, device=logits.device)
+    _whole(topk_ids, (T, kr), "topk_ids")
+    _whole(topk_weights, (T, kr), "topk_weights")
+    if bias is not None:
+        _whole(bias, (E,), "bias")
+    flags = ((GATE_SIGMOID if score == "sigmoid" else 0) | (GATE_GROUP_TOP2 if group_score == "top2" else 0)
+             | (GATE_RENORMALISE if renormalise else 0))
+    _lib.check(_lib.load().bsf_gate(
+        _dptr(logits, logits.dtype, "logits"), _TYPES[logits.dtype], T, E, ld,
+        None if bias is None else _dptr(bias, torch.float32, "bias"), groups,
+        groups if kept_groups is None else kept_groups, kr, flags, scale, _dptr(topk_ids, torch.int32, "topk_ids"),
+        _dptr(topk_weights, torch.float32, "topk_weights"), _raw_stream(stream)), "gate")
+    return topk_ids, topk_weights
+
+
+def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
+    """y bf16 [T, 2 K] (gate columns, then up columns; any row stride that is a multiple of 8) ->
+    (q uint8 [T, Kp], sf int32 [ceil(Kp/512), >= T]) of silu(gate) * up, Kp = K rounded up to 128.
+    ``rows`` as in ``quantise_act``: only the routed rows of a packed operand."""
+    ld = _row_stride(y, "y")
+    T, K = y.shape[0], y.shape[1] // 2
+    if y.shape[1] % 2:
+        raise ValueError(f"y: expected an even number of columns, got {y.shape[1]}")
+    Kp = (K + 127) // 128 * 128
+    if q is None:
+        q = torch.empty((T, Kp), dtype=torch.uint8, device=y.device)
+    if sf is None:
+        sf = torch.empty((sf_words(Kp), sf_ld(T)), dtype=torch.int32, device=y.device)
+    _whole(q, (T, Kp), "q")
+    _whole(sf, (sf_words(Kp), sf.shape[1]), "sf")
+    token_of_row = rows_used = None
+    if rows is not None:
+        token_of_row, rows_used = rows
+        if token_of_row.numel() < T or rows_used.numel() < 1 or not token_of_row.is_contiguous():
+            raise ValueError("rows: expected token_of_row of at least T entries and rows_used of one")
+        token_of_row = _dptr(token_of_row, torch.int32, "token_of_row")
+        rows_used = _dptr(rows_used, torch.int32, "rows_used")
+    _lib.check(_lib.load().bsf_swiglu_quantise(
+        _dptr(y, torch.bfloat16, "y"), T, K, ld, token_of_row, rows_used, _dptr(q, torch.uint8, "q"),
+        _dptr(sf, torch.int32, "sf"), sf.shape[1], _raw_stream(stream)), "swiglu_quantise")
+    return q, sf
+
+
+def prepare_dense_weight(w):
+    """w bf16 [N, K] -> (b uint8 [Np, Kp] tiled, sfb int32 [ceil(Kp/512), Np]) for ``dense_gemm`` with
+    ``B_TILED``, on the current stream; N and K are rounded up to 128 with zero weights."""
+    N, K = w.shape
+    w = torch.nn.functional.pad(w, (0, -K % 128, 0, -N % 128))
+    q, sf128 = quantise_weight(w.unsqueeze(0))
+    sfb = prepare_weight_sf(sf128, w.shape[1])
+    return tile_weights(q)[0], sfb[0]
+
+
+def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, stream=None):
+    """a uint8 [M, K] with scales sfa, b uint8 [Np, K] with scales sfb (``prepare_dense_weight``) ->
+    d bf16 [M, N], N <= Np < N + 128 (default Np); ``addend`` bf16 [M, N] is added before the rounding."""
+    M, K = a.shape
+    Np = b.shape[0]
+    N = Np if N is None else N
+    if (N + 127) // 128 * 128 != Np:
+        raise ValueError(f"b: expected {(N + 127) // 128 * 128} rows for N = {N}, got {Np}")
+    _whole(a, (M, K), "a")
+    _whole(b, (Np, K), "b")
+    _whole(sfa, (sf_words(K), sfa.shape[1]), "sfa")
+    _whole(sfb, (sf_words(K), Np), "sfb")
+    if d is None:
+        d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    ldd = _row_stride(d, "d")
+    ldc, c = 0, None
+    if addend is not None:
+        ldc, c = _row_stride(addend, "addend"), _dptr(addend, torch.bfloat16, "addend")
+        if addend.shape != (M, N):
+            raise ValueError(f"addend: expected shape {(M, N)}, got {tuple(addend.shape)}")
+    if d.shape != (M, N):
+        raise ValueError(f"d: expected shape {(M, N)}, got {tuple(d.shape)}")
+    _lib.check(_lib.load().bsf_dense_gemm(
+        _dptr(a, torch.uint8, "a"), _dptr(sfa, torch.int32, "sfa"), sfa.shape[1], M, _dptr(b, torch.uint8, "b"),
+        _dptr(sfb, torch.int32, "sfb"), N, K, c, ldc, _dptr(d, torch.bfloat16, "d"), ldd, flags,
+        _raw_stream(stream)), "dense_gemm")
+    return d

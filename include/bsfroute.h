@@ -8,7 +8,10 @@
  * The same path on the pages' other operand formats, declared further down:
  *   NVFP4  (E2M1 + one UE4M3 scale per 16 values, *_nvfp4),
  *   BF16   (unquantised, *_bf16),
- *   FP8 with float32 scale factors (*_f32sf).
+ *   FP8 with float32 scale factors (*_f32sf);
+ * and the operators around the path in an MoE block, at the end:
+ *   gate (router logits -> topk ids and weights), swiglu_quantise (gate-up
+ *   product -> operand of the down product), dense_gemm (one weight matrix).
  *
  * Conventions of every entry point
  *   - Pointers are DEVICE pointers (CUDA global memory) unless a parameter says
@@ -518,6 +521,95 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
                                          const float* sfb, void* d, const int32_t* masked_m, int64_t E,
                                          int64_t max_m, int64_t N, int64_t K, int64_t expected_m, int flags,
                                          bsf_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of an MoE block around the expert path.  "GEMM 执行方式" §4.2 takes
+ * topk_ids and topk_weights as given and the pages define no activation
+ * between the gate-up and down products; these entry points supply both, and
+ * the product of an expert that every token takes.
+ */
+
+/* Element types of an argument that takes more than one. */
+#define BSF_TYPE_F32 0
+#define BSF_TYPE_BF16 1
+
+/* bsf_gate flags. */
+#define BSF_GATE_SIGMOID 0x1     /* score = sigmoid(logit); otherwise softmax over the usable experts */
+#define BSF_GATE_GROUP_TOP2 0x2  /* group score = sum of its two largest; otherwise its largest */
+#define BSF_GATE_RENORMALISE 0x4 /* weights divided by their sum over the chosen experts */
+
+/*
+ * bsf_gate — routing to experts: topk_ids and topk_weights of each token from
+ * its router logits.
+ *   logits        [T, E], row stride ld >= E elements; logits_type
+ *                 BSF_TYPE_F32 or BSF_TYPE_BF16.  An expert whose logit is NaN
+ *                 or -inf is not usable for that token; +inf counts as the
+ *                 largest finite float32.
+ *   score         s_e = 1 / (1 + exp(-l_e)), or exp(l_e - m) / sum exp(l_j - m)
+ *                 over the usable experts, in float32.
+ *   bias          fp32 [E] or NULL.  With a bias the choice goes by s_e + b_e
+ *                 (an expert for which that is NaN or -inf is never chosen);
+ *                 without one by the logit itself.
+ *   groups        number of groups of E / groups consecutive experts (E %
+ *                 groups == 0).  Only the kept_groups groups of the largest
+ *                 score take part: the largest of what the choice goes by, or
+ *                 with BSF_GATE_GROUP_TOP2 the sum of the two largest s_e (+ b_e).
+ *   topk_ids      int32 [T, kr] (output): the kr largest, in descending order.
+ *                 Ties, of experts and of groups, go to the lowest index.
+ *                 Where fewer can be chosen the rest is -1, which bsf_route
+ *                 and bsf_combine skip.
+ *   topk_weights  fp32 [T, kr] (output): s of the chosen (never the bias),
+ *                 divided by their sum with BSF_GATE_RENORMALISE (0 where the
+ *                 sum is 0), times scale; 0 for an id of -1.
+ * E <= 1024, groups <= 32, kr <= 32 (else BSF_ERR_UNSUPPORTED), kr <=
+ * kept_groups * E / groups, scale finite.  T == 0 is a no-op.  No workspace;
+ * asynchronous on stream.
+ */
+bsf_status bsf_gate(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ld, const float* bias,
+                    int64_t groups, int64_t kept_groups, int64_t kr, int flags, float scale, int32_t* topk_ids,
+                    float* topk_weights, bsf_stream_t stream);
+
+/*
+ * bsf_swiglu_quantise — h = silu(g) * u of a gate-up product, quantised as
+ * bsf_quantise_act into the operand of the down product, in one pass.
+ *   y     bf16 [T, 2 K], row stride ld >= 2 K elements, ld % 8 == 0: g in
+ *         columns 0 .. K - 1, u in columns K .. 2 K - 1.
+ *   token_of_row, rows_used  both NULL: every row; otherwise the row filter of
+ *         bsf_quantise_act_rows (rows without a token are not written).
+ *   q     e4m3 [T, Kp], Kp = K rounded up to 128 (output); columns K .. Kp - 1
+ *         are zero codes.
+ *   sf    int32 [ceil(Kp/512)][sf_ld] packed MN-major (output), sf_ld >= T, a
+ *         multiple of 4.
+ * h = (g / (1 + exp(-g))) * u in float32, each operation rounded once; block
+ * scales and codes as in bsf_quantise_act.  K % 8 == 0.  T == 0 is a no-op.
+ */
+bsf_status bsf_swiglu_quantise(const void* y, int64_t T, int64_t K, int64_t ld, const int32_t* token_of_row,
+                               const int32_t* rows_used, uint8_t* q, int32_t* sf, int64_t sf_ld,
+                               bsf_stream_t stream);
+
+/*
+ * bsf_dense_gemm — D[r, :] = BF16( dequant(A[r, :]) . dequant(B)^T (+ C[r, :]) )
+ * of one weight matrix, for every row r < M: the product of an expert that
+ * every token takes, or of a projection.
+ *   a, sfa   e4m3 [M, K], int32 [ceil(K/512)][sfa_ld] (1 x 128 scales), as from
+ *            bsf_quantise_act or bsf_swiglu_quantise.
+ *   b, sfb   e4m3 [Np, K], int32 [ceil(K/512)][Np] with Np = N rounded up to
+ *            128: bsf_quantise_weight and bsf_prepare_weight_sf with E = 1 of
+ *            the weights with zero rows up to Np (and zero columns up to a
+ *            multiple of 128).  BSF_B_TILED: b through bsf_tile_weights.
+ *   addend   bf16 [M, N], row stride ldc >= N, or NULL: added to the FP32 sum
+ *            before the one rounding (for instance the routed experts'
+ *            combine).  It may be d itself.
+ *   d        bf16 [M, N] (output), row stride ldd >= N; nothing else is written.
+ * FP32 accumulation on the tensor cores, a fixed order of sums (bit-identical
+ * from run to run), round-to-nearest-even to bf16.  K % 128 == 0; 16-byte
+ * aligned a, b, sfa, sfb; d and addend need only their element alignment (8
+ * bytes and row strides of 4 elements are faster).  flags: BSF_B_TILED.
+ * M == 0 is a no-op.  A wait that runs out sets BSF_DEVERR_TIMEOUT.
+ */
+bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, int64_t M, const uint8_t* b,
+                          const int32_t* sfb, int64_t N, int64_t K, const void* addend, int64_t ldc, void* d,
+                          int64_t ldd, int flags, bsf_stream_t stream);
 
 #ifdef __cplusplus
 }
