@@ -10,8 +10,9 @@
 // "GEMM 执行方式" (rainlin-net) §4.2 takes topk_ids / topk_weights as given;
 // these are the tensors bsf_route, bsf_dispatch and bsf_combine consume.
 //
-// One warp per token: lane l holds experts l, l + 32, ... in registers, so a
-// row of logits is read once.
+// One warp per token.  Lane l holds the VPL consecutive experts from l * VPL in registers, so a row of
+// logits is read once with wide loads, a group of E / G experts is a run of 32 / G lanes, and the lowest
+// lane among equals is the lowest expert.
 #include <cfloat>
 
 #include "common.cuh"
@@ -23,7 +24,8 @@ namespace {
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxGroups = 32;
 constexpr int kGateMaxKr = 32;
-constexpr int kGateWarps = 4;           // tokens per CTA
+constexpr int kGateWarps = 4;           // warps per CTA
+constexpr unsigned kAll = 0xffffffffu;
 
 struct GateArgs {
   const void* logits;
@@ -31,176 +33,292 @@ struct GateArgs {
   const float* bias;
   int64_t T;
   int E, G, kept, kr;
+  int kr_lanes;            // power of two >= kr
+  int lane_groups;         // a group is 32 / G whole lanes
+  int group_shift;         // log2(32 / G) of such groups
+  int wide;                // rows may be read with the widest loads (E = 32 VPL, aligned)
   uint32_t group_magic;    // e / (E / G) = (e * group_magic) >> 22 for e < 1024
+  int flags;
   float scale;
   int32_t* ids;
   float* weights;
 };
 
-// Unsigned image of a float that keeps its order (-0 and +0 the same); 0 = an expert that is not to
-// be chosen (no finite or +inf float maps to 0).
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+// 1 / x of x >= 1 to one unit in the last place (0 above 2**126, where the quotient would be subnormal).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sigmoid(float l) { return reciprocal(1.f + expf(-l)); }
+
+// The VPL logits of this lane: -inf where there is no usable expert (past E, -inf, NaN), +inf as the
+// largest finite float.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_row(const GateArgs& p, int64_t t, int lane, float (&l)[VPL]) {
+  const int e0 = lane * VPL;
+  if (BF16) {
+    const uint16_t* row = static_cast<const uint16_t*>(p.logits) + t * p.ld + e0;
+    constexpr int W = VPL % 8 == 0 ? 8 : VPL % 4 == 0 ? 4 : VPL % 2 == 0 ? 2 : 1;   // values per load
+    if (W > 1 && p.wide) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += W) {
+        uint32_t w[W >= 2 ? W / 2 : 1];
+        if constexpr (W == 8) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
+          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (W == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + i));
+          w[0] = v.x, w[1] = v.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + i));
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          if (i + j < VPL) l[i + j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        l[i] = e0 + i < p.E ? __uint_as_float(static_cast<uint32_t>(__ldg(row + i)) << 16) : -INFINITY;
+    }
+  } else {
+    const float* row = static_cast<const float*>(p.logits) + t * p.ld + e0;
+    constexpr int W = VPL % 4 == 0 ? 4 : VPL % 2 == 0 ? 2 : 1;
+    if (W > 1 && p.wide) {
+#pragma unroll
+      for (int i = 0; i < VPL; i += W) {
+        if constexpr (W == 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
+          l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+        } else if constexpr (W == 2) {
+          const float2 v = __ldg(reinterpret_cast<const float2*>(row + i));
+          l[i] = v.x, l[i + 1] = v.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = e0 + i < p.E ? __ldg(row + i) : -INFINITY;
+    }
+  }
 }
 
-template <int VPL, bool BF16, bool SIGMOID, bool TOP2, bool RENORM>
+// What bounds it: a row is 4 E bytes, but choosing takes a fixed chain of warp operations, so short
+// batches are bound by that chain's latency and long ones by issue slots.  A row's keys are sorted once
+// within each lane (VPL <= 8; a stable exchange of neighbours, about 2.5 VPL^2 slots) so that a round of
+// the choice looks at one key per lane: one reduction, one ballot, and a shift in the lane that gave.
+// Wider lanes (VPL > 8) look through all their keys in each round instead, 5 VPL slots a round, which
+// is less than the sort for the kr of such routers.
+// Scores are computed only where they decide: with no bias the choice goes by the logits, and only the
+// kr chosen get an exp (plus the sum of a softmax that is not renormalised).
+template <int VPL, bool BF16>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p) {
   pdl_launch_dependents();
   __shared__ float s_val[kGateWarps][VPL * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
-  if (t >= p.T) return;
   const int E = p.E;
-  float s[VPL];
-  uint32_t key[VPL];
-  float m = -INFINITY;
+  const bool sig = p.flags & BSF_GATE_SIGMOID, top2 = p.flags & BSF_GATE_GROUP_TOP2;
+  const bool renorm = p.flags & BSF_GATE_RENORMALISE, biased = p.bias != nullptr;
+  const bool need_max = !sig && (biased || !renorm || (top2 && p.G > 1));
+  const bool need_sum = !sig && (biased || !renorm);
+  float bias[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
+  for (int i = 0; i < VPL; ++i) bias[i] = biased && lane * VPL + i < E ? __ldg(p.bias + lane * VPL + i) : 0.f;
+
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGateWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
+  if (t >= p.T) return;
+  float next[VPL];
+  load_row<VPL, BF16>(p, t, lane, next);
+  for (; t < p.T; t += step) {
+    float key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = next[i] > -INFINITY ? fminf(next[i], FLT_MAX) : -INFINITY;
+    if (t + step < p.T) load_row<VPL, BF16>(p, t + step, lane, next);
+
+    float m = 0.f, inv = 1.f;
+    if (need_max) {
+      m = key[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = fmaxf(m, key[i]);
+      m = fmaxf(warp_max(m), -FLT_MAX);            // (finite also where nothing is usable)
+    }
+    if (need_sum) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += expf(key[i] - m);          // exp(-inf) = 0
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      inv = sum > 0.f ? reciprocal(sum) : 0.f;        // (the largest term is 1)
+    }
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float v = (sig ? sigmoid(key[i]) : expf(key[i] - m) * inv) + bias[i];
+        key[i] = key[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;
+      }
+    }
+    // what a group's two largest keys count for in its score (scores rise with the logits)
+    auto counts = [&](float k) { return biased || !top2 ? k : sig ? sigmoid(k) : expf(k - m); };
+
+    bool open = true;                               // this lane's experts take part
+    if (p.G > 1 && p.lane_groups) {
+      const int mine = lane >> p.group_shift;
+      float a = key[0], b = -INFINITY;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) {
+        b = fmaxf(b, fminf(a, key[i]));
+        a = fmaxf(a, key[i]);
+      }
+      for (int o = 1; o < 1 << p.group_shift; o <<= 1) {
+        const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+        a = fmaxf(a, a2);
+      }
+      float gs = -INFINITY;
+      if (a > -INFINITY) gs = counts(a) + (top2 && b > -INFINITY ? counts(b) : 0.f);
+      open = false;
+      for (int r = 0; r < p.kept; ++r) {
+        const float v = open ? -INFINITY : gs;
+        const float best = warp_max(v);
+        if (best == -INFINITY) break;
+        open |= mine == (__ffs(__ballot_sync(kAll, v == best)) - 1) >> p.group_shift;
+      }
+    } else if (p.G > 1) {
+      // groups that end inside a lane: lane g reduces group g from shared memory
+      float* val = s_val[warp];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) val[lane * VPL + i] = key[i];
+      __syncwarp();
+      const int per = E / p.G;
+      float gs = -INFINITY;
+      if (lane < p.G) {
+        float a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < per; ++i) {
+          const float v = val[lane * per + i];
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
+        }
+        if (a > -INFINITY) gs = counts(a) + (top2 && b > -INFINITY ? counts(b) : 0.f);
+      }
+      __syncwarp();
+      uint32_t keep = 0;
+      for (int r = 0; r < p.kept; ++r) {
+        const float best = warp_max(gs);
+        if (best == -INFINITY) break;
+        const int g = __ffs(__ballot_sync(kAll, gs == best)) - 1;
+        keep |= 1u << g;
+        if (lane == g) gs = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const uint32_t g = (static_cast<uint32_t>(lane * VPL + i) * p.group_magic) >> 22;
+        if (!((keep >> (g & 31)) & 1u)) key[i] = -INFINITY;
+      }
+    }
+
+    int my_id = -1;
+    if constexpr (VPL <= 8) {
+      uint32_t order = 0x76543210u;                 // nibble j: position of the j-th largest key
+      int idx[VPL];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) idx[i] = i;
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) {
+#pragma unroll
+        for (int j = i; j > 0; --j) {
+          const bool up = key[j] > key[j - 1];
+          const float hi = fmaxf(key[j], key[j - 1]), lo = fminf(key[j], key[j - 1]);
+          const int ih = up ? idx[j] : idx[j - 1], il = up ? idx[j - 1] : idx[j];
+          key[j] = lo, key[j - 1] = hi;
+          idx[j] = il, idx[j - 1] = ih;
+        }
+      }
+      if constexpr (VPL > 1) {
+        order = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) order |= static_cast<uint32_t>(idx[i]) << (4 * i);
+      }
+      if (!open) key[0] = -INFINITY;                // a lane that never gives
+      for (int r = 0; r < p.kr; ++r) {
+        const float best = warp_max(key[0]);
+        if (best == -INFINITY) break;
+        const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+        const int e = __shfl_sync(kAll, lane * VPL + static_cast<int>(order & 15u), from);
+        if (lane == r) my_id = e;
+        if (lane == from) {
+#pragma unroll
+          for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
+          key[VPL - 1] = -INFINITY;
+          order >>= 4;
+        }
+      }
+    } else {
+      if (!open) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
+      }
+      for (int r = 0; r < p.kr; ++r) {
+        float head = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) head = fmaxf(head, key[i]);
+        const float best = warp_max(head);
+        if (best == -INFINITY) break;
+        const int from = __ffs(__ballot_sync(kAll, head == best)) - 1;
+        int at = 0;
+#pragma unroll
+        for (int i = VPL - 1; i >= 0; --i) at = key[i] == best ? i : at;
+        const int e = __shfl_sync(kAll, lane * VPL + at, from);
+        if (lane == r) my_id = e;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (lane == from && i == at) key[i] = -INFINITY;
+      }
+    }
+
+    // lane r: the score of choice r, from its logit (still in a cache)
     float l = -INFINITY;
-    if (e < E) {
+    if (my_id >= 0) {
       if (BF16)
-        l = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + e)) << 16);
+        l = __uint_as_float(
+            static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + my_id)) << 16);
       else
-        l = __ldg(static_cast<const float*>(p.logits) + t * p.ld + e);
+        l = __ldg(static_cast<const float*>(p.logits) + t * p.ld + my_id);
+      l = fminf(l, FLT_MAX);
     }
-    l = l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;     // NaN: not usable
-    s[i] = l;
-    m = fmaxf(m, l);
-  }
-  const bool need_score_key = p.bias != nullptr;
-  if (SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] = s[i] > -INFINITY ? order_key(s[i]) : 0u;
-      s[i] = key[i] ? __fdiv_rn(1.f, 1.f + expf(-s[i])) : 0.f;
+    if (!sig && !need_max) m = __shfl_sync(kAll, l, 0);              // the largest logit is the first choice
+    float w = 0.f;
+    if (my_id >= 0) w = sig ? sigmoid(l) : expf(l - m) * inv;
+    if (renorm) {
+      float total = w;
+      for (int o = p.kr_lanes >> 1; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+      w = total > 0.f ? __fdiv_rn(w, total) : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] = s[i] > -INFINITY ? order_key(s[i]) : 0u;
-      s[i] = key[i] ? expf(s[i] - m) : 0.f;
-      sum += s[i];
+    if (lane < p.kr) {
+      p.ids[t * p.kr + lane] = my_id;
+      p.weights[t * p.kr + lane] = w * p.scale;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] *= inv;
-  }
-  if (need_score_key) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && key[i]) {
-        const float v = s[i] + __ldg(p.bias + e);
-        key[i] = v > -INFINITY ? order_key(v) : 0u;
-      }
-    }
-  }
-  if (p.G > 1) {
-    // group scores: lane g reduces group g from shared memory
-    float* val = s_val[warp];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      // a value that orders the group: s (+ b) for the sum of two, the key itself for the maximum
-      float v = -INFINITY;
-      if (key[i]) v = (TOP2 && !need_score_key) ? s[i] : key_value(key[i]);
-      val[lane + 32 * i] = v;
-    }
-    __syncwarp();
-    const int per = E / p.G;
-    float gs = -INFINITY;
-    if (lane < p.G) {
-      float a = -INFINITY, b = -INFINITY;
-      for (int i = 0; i < per; ++i) {
-        const float v = val[lane * per + i];
-        if (TOP2) b = fmaxf(b, fminf(a, v));
-        a = fmaxf(a, v);
-      }
-      gs = TOP2 && b > -INFINITY ? a + b : a;
-    }
-    int rank = 0;
-    for (int g = 0; g < p.G; ++g) {
-      const float o = __shfl_sync(0xffffffffu, gs, g);
-      rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
-    }
-    const uint32_t keep = __ballot_sync(0xffffffffu, lane < p.G && rank < p.kept);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const uint32_t g = (static_cast<uint32_t>(lane + 32 * i) * p.group_magic) >> 22;
-      if (!((keep >> (g & 31)) & 1u)) key[i] = 0u;
-    }
-  }
-  // kr rounds: the warp's largest key, the lowest expert that has it
-  int my_id = -1;
-  float my_s = 0.f;
-  for (int r = 0; r < p.kr; ++r) {
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(0xffffffffu, best);
-    if (best == 0u) break;
-    uint32_t e = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == best) e = lane + 32 * i;
-    e = __reduce_min_sync(0xffffffffu, e);
-    float se = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e == static_cast<uint32_t>(lane + 32 * i)) {
-        key[i] = 0u;
-        se = s[i];
-      }
-    se = __shfl_sync(0xffffffffu, se, e & 31);
-    if (lane == r) {
-      my_id = static_cast<int>(e);
-      my_s = se;
-    }
-  }
-  float w = my_s;
-  if (RENORM) {
-    float total = my_s;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    w = total > 0.f ? __fdiv_rn(my_s, total) : 0.f;
-  }
-  if (lane < p.kr) {
-    p.ids[t * p.kr + lane] = my_id;
-    p.weights[t * p.kr + lane] = w * p.scale;
   }
 }
 
-template <int VPL, bool BF16>
-void launch_gate(const GateArgs& a, int flags, unsigned blocks, cudaStream_t s) {
-  const bool sg = flags & BSF_GATE_SIGMOID, t2 = flags & BSF_GATE_GROUP_TOP2, rn = flags & BSF_GATE_RENORMALISE;
-#define BSF_GATE_LAUNCH(S, P, R) gate_kernel<VPL, BF16, S, P, R><<<blocks, 32 * kGateWarps, 0, s>>>(a)
-  if (sg) {
-    if (t2) { if (rn) BSF_GATE_LAUNCH(true, true, true); else BSF_GATE_LAUNCH(true, true, false); }
-    else { if (rn) BSF_GATE_LAUNCH(true, false, true); else BSF_GATE_LAUNCH(true, false, false); }
-  } else {
-    if (t2) { if (rn) BSF_GATE_LAUNCH(false, true, true); else BSF_GATE_LAUNCH(false, true, false); }
-    else { if (rn) BSF_GATE_LAUNCH(false, false, true); else BSF_GATE_LAUNCH(false, false, false); }
-  }
-#undef BSF_GATE_LAUNCH
-}
-
-template <bool BF16>
-void launch_gate_width(const GateArgs& a, int flags, unsigned blocks, cudaStream_t s) {
-  if (a.E <= 32) launch_gate<1, BF16>(a, flags, blocks, s);
-  else if (a.E <= 64) launch_gate<2, BF16>(a, flags, blocks, s);
-  else if (a.E <= 128) launch_gate<4, BF16>(a, flags, blocks, s);
-  else if (a.E <= 256) launch_gate<8, BF16>(a, flags, blocks, s);
-  else if (a.E <= 512) launch_gate<16, BF16>(a, flags, blocks, s);
-  else launch_gate<32, BF16>(a, flags, blocks, s);
+template <int VPL>
+void launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
+  const int size = bf16 ? 2 : 4;
+  const int bytes = VPL * size % 16 == 0 ? 16 : VPL * size % 8 == 0 ? 8 : VPL * size % 4 == 0 ? 4 : 2;
+  a.wide = a.E == 32 * VPL && reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 && a.ld * size % bytes == 0;
+  a.lane_groups = a.E == 32 * VPL && 32 % a.G == 0;
+  while ((a.G << (a.group_shift + 1)) <= 32) ++a.group_shift;
+  // one row per warp until every SM has its warps, then each warp goes on with the next row in flight
+  const int64_t most = static_cast<int64_t>(sm_count()) * (VPL <= 8 ? 10 : 5);
+  const int64_t need = (a.T + kGateWarps - 1) / kGateWarps;
+  const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
+  if (bf16) gate_kernel<VPL, true><<<blocks, 32 * kGateWarps, 0, s>>>(a);
+  else gate_kernel<VPL, false><<<blocks, 32 * kGateWarps, 0, s>>>(a);
 }
 
 }  // namespace
@@ -225,7 +343,7 @@ extern "C" bsf_status bsf_gate(const void* logits, int logits_type, int64_t T, i
       (reinterpret_cast<uintptr_t>(topk_ids) & 3) || (reinterpret_cast<uintptr_t>(topk_weights) & 3))
     return BSF_ERR_MISALIGNED;
   if (!fits_rows(T, ld)) return BSF_ERR_UNSUPPORTED;
-  GateArgs a;
+  GateArgs a = {};
   a.logits = logits;
   a.ld = ld;
   a.bias = bias;
@@ -234,14 +352,27 @@ extern "C" bsf_status bsf_gate(const void* logits, int logits_type, int64_t T, i
   a.G = static_cast<int>(groups);
   a.kept = static_cast<int>(kept_groups);
   a.kr = static_cast<int>(kr);
+  a.kr_lanes = 1;
+  while (a.kr_lanes < a.kr) a.kr_lanes *= 2;
   const uint32_t per = static_cast<uint32_t>(E / groups);
   a.group_magic = ((1u << 22) + per - 1) / per;
+  a.flags = flags;
   a.scale = scale;
   a.ids = topk_ids;
   a.weights = topk_weights;
-  const unsigned blocks = static_cast<unsigned>((T + kGateWarps - 1) / kGateWarps);
+  const bool bf16 = logits_type == BSF_TYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (logits_type == BSF_TYPE_F32) launch_gate_width<false>(a, flags, blocks, s);
-  else launch_gate_width<true>(a, flags, blocks, s);
+  const int vpl = (a.E + 31) / 32;
+  if (vpl == 1) launch_gate<1>(a, bf16, s);
+  else if (vpl == 2) launch_gate<2>(a, bf16, s);
+  else if (vpl == 3) launch_gate<3>(a, bf16, s);
+  else if (vpl == 4) launch_gate<4>(a, bf16, s);
+  else if (vpl == 5) launch_gate<5>(a, bf16, s);
+  else if (vpl == 6) launch_gate<6>(a, bf16, s);
+  else if (vpl == 7) launch_gate<7>(a, bf16, s);
+  else if (vpl == 8) launch_gate<8>(a, bf16, s);
+  else if (vpl <= 12) launch_gate<12>(a, bf16, s);
+  else if (vpl <= 16) launch_gate<16>(a, bf16, s);
+  else launch_gate<32>(a, bf16, s);
   return launch_status();
 }
