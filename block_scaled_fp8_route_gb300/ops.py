@@ -430,31 +430,45 @@ GATE_SIGMOID = 0x1
 GATE_GROUP_TOP2 = 0x2
 GATE_RENORMALISE = 0x4
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}       # BSF_TYPE_F32, BSF_TYPE_BF16
+_SCORES = {"softmax": 0, "sigmoid": GATE_SIGMOID}
+_GROUP_SCORES = {"max": 0, "top2": GATE_GROUP_TOP2}
+
+
+def _refuse(t, dtype, what):
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
 
 
 def _dptr(t, dtype, what):
-    """Address of a CUDA tensor of the given type whose rows are contiguous."""
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
+    """Address of a CUDA tensor of the given type."""
+    if t.dtype != dtype or not t.is_cuda:
+        _refuse(t, dtype, what)
     return t.data_ptr()
 
 
 def _row_stride(t, what):
     """Row stride of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    stride = t.stride()
+    if cols > 1 and stride[1] != 1:
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
+    return stride[0] if rows > 1 else max(stride[0], cols)
 
 
 def _whole(t, shape, what):
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _raw_stream(stream, t):
+    """Handle of the given stream, or of the current stream of the tensor's device (looked up without
+    making a stream object, which costs 2.8 us of a small call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, group_score="max", renormalise=True,
@@ -464,9 +478,10 @@ def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, gro
     ``bias`` float32 [E] the choice goes by score + bias; of ``groups`` groups of experts only the
     ``kept_groups`` best take part (``group_score`` "max" or "top2"); ids of -1 where too few experts can
     be chosen (a logit of -inf or NaN masks its expert)."""
-    if logits.dtype not in _TYPES:
+    kind = _TYPES.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
-    if score not in ("softmax", "sigmoid") or group_score not in ("max", "top2"):
+    if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError(f"score {score!r} / group_score {group_score!r}: expected softmax or sigmoid / max or top2")
     ld = _row_stride(logits, "logits")
     T, E = logits.shape
@@ -476,15 +491,18 @@ def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, gro
         topk_weights = torch.empty((T, kr), dtype=torch.float32, device=logits.device)
     _whole(topk_ids, (T, kr), "topk_ids")
     _whole(topk_weights, (T, kr), "topk_weights")
+    b = None
     if bias is not None:
         _whole(bias, (E,), "bias")
-    flags = ((GATE_SIGMOID if score == "sigmoid" else 0) | (GATE_GROUP_TOP2 if group_score == "top2" else 0)
-             | (GATE_RENORMALISE if renormalise else 0))
-    _lib.check(_lib.load().bsf_gate(
-        _dptr(logits, logits.dtype, "logits"), _TYPES[logits.dtype], T, E, ld,
-        None if bias is None else _dptr(bias, torch.float32, "bias"), groups,
-        groups if kept_groups is None else kept_groups, kr, flags, scale, _dptr(topk_ids, torch.int32, "topk_ids"),
-        _dptr(topk_weights, torch.float32, "topk_weights"), _raw_stream(stream)), "gate")
+        b = _dptr(bias, torch.float32, "bias")
+    status = _lib.load().bsf_gate(
+        _dptr(logits, logits.dtype, "logits"), kind, T, E, ld, b, groups,
+        groups if kept_groups is None else kept_groups, kr,
+        _SCORES[score] | _GROUP_SCORES[group_score] | (GATE_RENORMALISE if renormalise else 0), scale,
+        _dptr(topk_ids, torch.int32, "topk_ids"), _dptr(topk_weights, torch.float32, "topk_weights"),
+        _raw_stream(stream, logits))
+    if status:
+        _lib.check(status, "gate")
     return topk_ids, topk_weights
 
 
@@ -493,16 +511,18 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
     (q uint8 [T, Kp], sf int32 [ceil(Kp/512), >= T]) of silu(gate) * up, Kp = K rounded up to 128.
     ``rows`` as in ``quantise_act``: only the routed rows of a packed operand."""
     ld = _row_stride(y, "y")
-    T, K = y.shape[0], y.shape[1] // 2
-    if y.shape[1] % 2:
-        raise ValueError(f"y: expected an even number of columns, got {y.shape[1]}")
+    T, K = y.shape
+    if K % 2:
+        raise ValueError(f"y: expected an even number of columns, got {K}")
+    K //= 2
     Kp = (K + 127) // 128 * 128
     if q is None:
         q = torch.empty((T, Kp), dtype=torch.uint8, device=y.device)
     if sf is None:
         sf = torch.empty((sf_words(Kp), sf_ld(T)), dtype=torch.int32, device=y.device)
     _whole(q, (T, Kp), "q")
-    _whole(sf, (sf_words(Kp), sf.shape[1]), "sf")
+    ld_sf = sf.shape[-1]
+    _whole(sf, (sf_words(Kp), ld_sf), "sf")
     token_of_row = rows_used = None
     if rows is not None:
         token_of_row, rows_used = rows
@@ -510,9 +530,11 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
             raise ValueError("rows: expected token_of_row of at least T entries and rows_used of one")
         token_of_row = _dptr(token_of_row, torch.int32, "token_of_row")
         rows_used = _dptr(rows_used, torch.int32, "rows_used")
-    _lib.check(_lib.load().bsf_swiglu_quantise(
+    status = _lib.load().bsf_swiglu_quantise(
         _dptr(y, torch.bfloat16, "y"), T, K, ld, token_of_row, rows_used, _dptr(q, torch.uint8, "q"),
-        _dptr(sf, torch.int32, "sf"), sf.shape[1], _raw_stream(stream)), "swiglu_quantise")
+        _dptr(sf, torch.int32, "sf"), ld_sf, _raw_stream(stream, y))
+    if status:
+        _lib.check(status, "swiglu_quantise")
     return q, sf
 
 
@@ -534,22 +556,25 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
     N = Np if N is None else N
     if (N + 127) // 128 * 128 != Np:
         raise ValueError(f"b: expected {(N + 127) // 128 * 128} rows for N = {N}, got {Np}")
+    words, ld_sf = sf_words(K), sfa.shape[-1]
     _whole(a, (M, K), "a")
     _whole(b, (Np, K), "b")
-    _whole(sfa, (sf_words(K), sfa.shape[1]), "sfa")
-    _whole(sfb, (sf_words(K), Np), "sfb")
+    _whole(sfa, (words, ld_sf), "sfa")
+    _whole(sfb, (words, Np), "sfb")
     if d is None:
         d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    elif d.shape != (M, N):
+        raise ValueError(f"d: expected shape {(M, N)}, got {tuple(d.shape)}")
     ldd = _row_stride(d, "d")
     ldc, c = 0, None
     if addend is not None:
-        ldc, c = _row_stride(addend, "addend"), _dptr(addend, torch.bfloat16, "addend")
         if addend.shape != (M, N):
             raise ValueError(f"addend: expected shape {(M, N)}, got {tuple(addend.shape)}")
-    if d.shape != (M, N):
-        raise ValueError(f"d: expected shape {(M, N)}, got {tuple(d.shape)}")
-    _lib.check(_lib.load().bsf_dense_gemm(
-        _dptr(a, torch.uint8, "a"), _dptr(sfa, torch.int32, "sfa"), sfa.shape[1], M, _dptr(b, torch.uint8, "b"),
+        ldc, c = _row_stride(addend, "addend"), _dptr(addend, torch.bfloat16, "addend")
+    status = _lib.load().bsf_dense_gemm(
+        _dptr(a, torch.uint8, "a"), _dptr(sfa, torch.int32, "sfa"), ld_sf, M, _dptr(b, torch.uint8, "b"),
         _dptr(sfb, torch.int32, "sfb"), N, K, c, ldc, _dptr(d, torch.bfloat16, "d"), ldd, flags,
-        _raw_stream(stream)), "dense_gemm")
+        _raw_stream(stream, a))
+    if status:
+        _lib.check(status, "dense_gemm")
     return d
