@@ -69,6 +69,17 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t local_smem, uint32_t ra
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
 }
+// Bounded wait for a copy of this thread's own: it goes on after an abort (the copy has to land before the
+// CTA exits), and says so if the limit is reached.
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity, int* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_error(err, BSF_DEVERR_TIMEOUT);
+      return;
+    }
+  }
+}
 __device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -281,6 +292,480 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.split > 1) cluster_sync();
 }
 
+// ---------------------------------------------------------------- CTA pairs: 256 x up to 224 output tiles
+constexpr int kPairW = 256;                                // weight rows of a tile (MMA M), 128 per CTA
+constexpr int kPairMaxTok = 224;                           // tokens of a tile (MMA N), half staged by each CTA
+constexpr int kPairMaxStages = 4;                          // a stage is 256 K of both operands
+// warps: 0 weight loads, 1 MMA issuer, 2-5 scales, 6-13 epilogue, 14 waiter, 15 token loads
+constexpr int kPairThreads = 32 * 16;
+constexpr int kPairWaiter = 14, kPairTokLoads = 15;
+constexpr int kBoxBytes = 32 * 64;                         // 32 tokens x 32 bf16 columns of D
+constexpr int kPairBarBytes = 512;
+
+struct PairArgs {
+  const int32_t* sfa;
+  int64_t sfa_ld;
+  const int32_t* sfb;
+  int64_t Np;
+  const uint16_t* addend;
+  int64_t ldc;
+  uint16_t* d;
+  int64_t ldd;
+  int M, N, nkb, nw;
+  int tiles_m, tiles_n;      // token tiles, weight tiles
+  int tok;                   // tokens of a tile: a multiple of 32, at most kPairMaxTok
+  int stages;
+  int tiled, vec8;
+  int* err;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// shared::cluster address of this CTA's shared-memory address in the CTA of the given rank
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+// Arrivals and waits between the CTAs of a pair that order tensor-memory accesses only: relaxed, because the
+// tcgen05 fences on both sides order those accesses.  (Release and acquire at cluster scope also
+// order all of generic memory, and cost a stage of the main loop about 100 cycles.)
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t spins = 0;
+  while (true) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((++spins & 63u) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        raise_error(err, BSF_DEVERR_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_cluster_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, wait_cluster(bar, parity, abort, err));
+}
+// TMA box into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// Executed by the whole warp, issued by the lane whose `lead` is non-zero.
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(lead)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3)), "r"(lead)
+      : "memory");
+}
+// One box of shared memory into a 2-D tensor (part of the calling thread's bulk group).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ CUtensorMap tmap_a,
+                      const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_c,
+                      const PairArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int half_tok = p.tok >> 1;
+  // a stage: 128 weight rows of two K-blocks, then half of the tile's tokens of the same two
+  const int tok_bytes = half_tok * kTileK;
+  const int stage_bytes = 2 * (kTileW * kTileK + tok_bytes);
+  uint8_t* store = smem + p.stages * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(store + 16 * kBoxBytes);                // used in rank 0
+  uint64_t* empty = full + kPairMaxStages;
+  uint64_t* sf_full = empty + kPairMaxStages;                                           // used in rank 0
+  uint64_t* sf_empty = sf_full + kSfSlots;
+  uint64_t* acc_full = sf_empty + kSfSlots;
+  uint64_t* acc_empty = acc_full + 2;                                                   // used in rank 0
+  uint64_t* add_full = acc_empty + 2;                                                   // two per epilogue warp
+  uint64_t* mma_done = add_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int total = p.tiles_m * p.tiles_n;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sf_full[s], 8);
+      mbar_init(&sf_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 16);
+    }
+    for (int s = 0; s < 16; ++s) mbar_init(&add_full[s], 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_b);
+    tma_prefetch_desc(&tmap_a);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();                           // barriers of both CTAs are initialised
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_sf = tmem_base + 2 * p.tok;            // behind the two accumulators
+
+  if (warp == 0 || warp == kPairTokLoads) {
+    // ------------------------------------------------------------ TMA producers (each CTA loads its halves)
+    // One warp per operand, two K-blocks per barrier: a load takes its issuing thread about 170 cycles and
+    // a wait or commit 100 and more, against 448 cycles of MMAs per K-block.  (Where K has an odd number
+    // of blocks the last stage's second half is loaded but not multiplied: past K it is zeros.)
+    if (lane == 0) {
+      const bool weights = warp == 0;
+      uint32_t stage = 0, phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+        const int row = tm * p.tok + static_cast<int>(rank) * half_tok;
+        const int wt = tn * 2 + static_cast<int>(rank);               // 128-row weight tile of this CTA
+        for (int kb = 0; kb < p.nkb; kb += 2) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
+          const uint32_t bar = map_rank(&full[stage], 0);
+          uint8_t* dst = smem + stage * stage_bytes;
+          if (weights) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
+            if (p.tiled) {                                            // two blocks are one 32 KB run
+              pair_load_2d(dst, &tmap_b, bar, 0, (wt * p.nkb + kb) * kTileW);
+            } else {
+              pair_load_2d(dst, &tmap_b, bar, kb * kTileK, wt * kTileW);
+              pair_load_2d(dst + kTileW * kTileK, &tmap_b, bar, (kb + 1) * kTileK, wt * kTileW);
+            }
+          } else {
+            dst += 2 * kTileW * kTileK;
+            pair_load_2d(dst, &tmap_a, bar, kb * kTileK, row);
+            pair_load_2d(dst + tok_bytes, &tmap_a, bar, (kb + 1) * kTileK, row);
+          }
+          ++issued;
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (rank == 0) {
+        // both CTAs' loads complete on these barriers; rank 1 waits for rank 0 at the last cluster barrier
+        const int outstanding = issued < p.stages ? issued : p.stages;
+        for (int j = 0; j < outstanding; ++j) {
+          if (stage == 0) { stage = p.stages; phase ^= 1u; }
+          --stage;
+          wait_quiet(&full[stage], phase);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (rank 0)
+    // The issuing thread reads no shared memory between stages: the waiter warp does every wait and hands
+    // each stage over through a named barrier whose OR-reduced predicate carries an abort.
+    if (rank == 0) {
+      const uint32_t lead = lane == 0;
+      uint32_t stage = 0, slot = 0, acc = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        const uint32_t d_tmem = tmem_base + acc * p.tok;
+        for (int kb = 0; kb < p.nkb; kb += 2) {
+          if (named_barrier_or(1, 64, false)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sf = tmem_sf + slot * kSfCols;
+          const uint8_t* src = smem + stage * stage_bytes;
+          uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
+          uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + 2 * kTileW * kTileK));
+          uint32_t idesc = idesc_mxf8_e4m3(kPairW, p.tok, kb & 3, kb & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, (kb | k) != 0, lead);
+          if (kb + 1 < p.nkb) {
+            adesc += kTileW * kTileK >> 4;
+            bdesc += tok_bytes >> 4;
+            idesc = idesc_mxf8_e4m3(kPairW, p.tok, (kb + 1) & 3, (kb + 1) & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, 1, lead);
+          }
+          pair_commit(&empty[stage], lead);
+          if (++stage == static_cast<uint32_t>(p.stages)) stage = 0;
+          if ((kb & 2) || kb + 2 >= p.nkb) {
+            pair_commit(&sf_empty[slot], lead);
+            if (++slot == kSfSlots) slot = 0;
+          }
+        }
+        if (!ok) break;
+        pair_commit(&acc_full[acc], lead);
+        acc ^= 1u;
+      }
+      pair_commit(mma_done, lead);
+      if (lane == 0) wait_quiet(mma_done, 0);
+    }
+    __syncwarp();
+  } else if (warp == kPairWaiter) {
+    // ------------------------------------------------------------ waiter (rank 0): the issuer's waits, in its order
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0, slot = 0, sf_phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        bool good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
+        for (int kb = 0; kb < p.nkb; kb += 2) {
+          if (good && (kb & 3) == 0) good = wait_cluster_all(&sf_full[slot], sf_phase, abort_flag, p.err);
+          if (good) good = wait_all(&full[stage], phase, abort_flag, p.err);
+          if (named_barrier_or(1, 64, !good)) { ok = false; break; }
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+          if ((kb & 2) || kb + 2 >= p.nkb)
+            if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
+        }
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  } else if (warp < 6) {
+    // ------------------------------------------------------------ scale words (each CTA into its own tensor memory)
+    // columns 0-3 of a slot: this CTA's 128 weight rows; from 4: all tokens of the tile
+    const int q = warp & 3;
+    const uint32_t quad = tmem_sf + (static_cast<uint32_t>(32 * q) << 16);
+    const int ncols = p.tok >> 5;
+    uint32_t slot = 0, sf_phase = 0;
+    // the words of the next slot are in flight while this one's are written: a load's latency is as long as
+    // two stages' MMAs, and a slot serves four
+    uint32_t w[4], a[kPairMaxTok / 32];
+    auto load = [&](int t, int g) {
+      const int row = t % p.tiles_m * p.tok + lane;
+      const int wrow = t / p.tiles_m * kPairW + static_cast<int>(rank) * 128 + lane;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        w[c] = wrow + 32 * c < p.Np ? static_cast<uint32_t>(__ldg(p.sfb + g * p.Np + wrow + 32 * c)) : 0x7F7F7F7Fu;
+#pragma unroll
+      for (int c = 0; c < kPairMaxTok / 32; ++c)
+        a[c] = c < ncols && row + 32 * c < p.M ? static_cast<uint32_t>(__ldg(p.sfa + g * p.sfa_ld + row + 32 * c))
+                                               : 0x7F7F7F7Fu;
+    };
+    int t = pair, g = 0;
+    load(t, g);
+    while (true) {
+      uint32_t w0[4], a0[kPairMaxTok / 32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w0[c] = w[c];
+#pragma unroll
+      for (int c = 0; c < kPairMaxTok / 32; ++c) a0[c] = a[c];
+      if (++g == p.nw) {
+        g = 0;
+        t += npairs;
+      }
+      if (t < total) load(t, g);
+      if (!wait_all(&sf_empty[slot], sf_phase ^ 1u, abort_flag, p.err)) break;
+      tc_fence_after();
+      const uint32_t col = quad + slot * kSfCols;
+      tmem_st_x4(col, w0[0], w0[1], w0[2], w0[3]);
+      tmem_st_x4(col + 4, a0[0], a0[1], a0[2], a0[3]);
+      tmem_st_x2(col + 8, a0[4], a0[5]);
+      tmem_st_x1(col + 10, a0[6]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(map_rank(&sf_full[slot], 0));
+      if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
+      if (t >= total) break;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue: lane = weight row, 32 tokens at a time
+    // Two warps share a quadrant's tokens.  After one exchange with its neighbour a lane holds two weight
+    // rows of one token (4 bytes).  With 16-byte aligned rows of D the 32 x 32 boxes go through this warp's
+    // shared memory (64-byte swizzle: 16-byte piece j of token i sits at j ^ (i / 2 % 4)); the addend is
+    // loaded the same way, ahead of the accumulator.  TMA cuts the boxes at the edges.
+    const int q = warp & 3, ew = warp - 6;
+    const int nc = p.tok >> 5, c_first = ew < 4 ? 0 : (nc + 1) >> 1, c_last = ew < 4 ? (nc + 1) >> 1 : nc;
+    const int odd = lane & 1;
+    uint8_t* bufs = store + ew * 2 * kBoxBytes;
+    uint32_t acc = 0, acc_phase = 0, add_phase = 0;        // add_phase: bit b for buffer b
+    int box = 0;                            // next box buffer
+    for (int t = pair; t < total; t += npairs) {
+      const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+      const int n0 = tn * kPairW + static_cast<int>(rank) * 128 + 32 * q;
+      const int tok0 = tm * p.tok;
+      // boxes of this warp that touch D
+      const int cuts = n0 < p.N ? min(c_last, (p.M - tok0 + 31) >> 5) - c_first : 0;
+      const bool boxed_add = p.addend && p.vec8 && cuts > 0;
+      // addend box i of the tile into its buffer (its last store has been read)
+      auto load_add = [&](int i) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive_expect_tx(&add_full[ew * 2 + (i & 1)], kBoxBytes);
+        tma_load_2d(bufs + (i & 1) * kBoxBytes, &tmap_c, &add_full[ew * 2 + (i & 1)], n0, tok0 + 32 * (c_first + i));
+      };
+      int loaded = 0;                       // addend boxes of this tile
+      if (boxed_add) {
+        box = 0;
+        loaded = min(2, cuts);
+        if (lane == 0)
+          for (int i = 0; i < loaded; ++i) load_add(i);
+        __syncwarp();
+      }
+      if (!wait_all(&acc_full[acc], acc_phase, abort_flag, p.err)) {
+        // the copies must have landed before this CTA may exit
+        for (int i = 0; i < loaded; ++i) wait_landed(&add_full[ew * 2 + i], (add_phase >> i) & 1u, p.err);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * p.tok;
+      for (int c = c_first; c < c_last; ++c) {
+        uint32_t r[32];
+        tmem_ld_x32(taddr + 32 * c, r);
+        tmem_wait_ld_regs(r);
+        if (c == c_last - 1) {              // the accumulator's last columns are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(map_rank(&acc_empty[acc], 0));
+        }
+        if (c - c_first >= cuts) continue;
+        if (p.vec8) {
+          uint8_t* buf = bufs + box * kBoxBytes;
+          if (boxed_add) {
+            wait_landed(&add_full[ew * 2 + box], (add_phase >> box) & 1u, p.err);
+            __syncwarp();
+            add_phase ^= 1u << box;
+          } else {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before last is read
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float v0 = __uint_as_float(r[j]), v1 = __uint_as_float(r[j + 1]);
+            const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            v0 = odd ? x : v0;
+            v1 = odd ? v1 : x;
+            uint32_t* at = reinterpret_cast<uint32_t*>(buf + (j + odd) * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) +
+                                                       (lane & 6) * 2);
+            if (boxed_add) {
+              const uint32_t a = *at;
+              v0 += __uint_as_float(a << 16);
+              v1 += __uint_as_float(a & 0xFFFF0000u);
+            }
+            *at = pack_bf16x2(v0, v1);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmap_d, buf, n0, tok0 + 32 * c);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            if (boxed_add && loaded < cuts) load_add(loaded);
+          }
+          ++loaded;
+          box ^= 1;
+        } else if (n0 + lane < p.N) {
+          const int64_t row = tok0 + 32 * c;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (row + j < p.M) {
+              float f = __uint_as_float(r[j]);
+              if (p.addend)
+                f += __uint_as_float(static_cast<uint32_t>(p.addend[(row + j) * p.ldc + n0 + lane]) << 16);
+              p.d[(row + j) * p.ldd + n0 + lane] = static_cast<uint16_t>(pack_bf16x2(f, 0.f) & 0xFFFFu);
+            }
+          }
+        }
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    // the issuer's last commit has reached this CTA's barriers too, so none arrives after it exits
+    if (warp == 6 && lane == 0) wait_quiet(mma_done, 0);
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync();                           // no load, MMA or remote arrival of the pair is outstanding
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+}
+
+bsf_status launch_cluster(const void* kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                          cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return BSF_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+bsf_status allow_smem(const void* kernel, size_t bytes, std::atomic<bool>* set) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+      return BSF_ERR_CUDA;
+    set[dev].store(true, std::memory_order_release);
+  }
+  return BSF_OK;
+}
+
 }  // namespace
 }  // namespace bsf
 
@@ -300,20 +785,71 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   if (!fits_rows(M, K) || !fits_rows(M, ldd) || (addend && ldc > kMaxRowWidth) || N > kMaxRowWidth || sfa_ld > kMaxRows)
     return BSF_ERR_UNSUPPORTED;
   const int64_t ntn = (N + kTileW - 1) / kTileW, nkb = K / kTileK;
-  if (ntn * kTileW * nkb > INT32_MAX) return BSF_ERR_UNSUPPORTED;
-  const int64_t chunks = (M + kMaxTok - 1) / kMaxTok;
-  const int64_t tiles = ntn * chunks;
+  if ((ntn + 2) * kTileW * nkb > INT32_MAX || M > kMaxRows - 256) return BSF_ERR_UNSUPPORTED;
   int* err = device_error_ptr();
   if (!err) return BSF_ERR_CUDA;
+  const bool tiled = (flags & BSF_B_TILED) != 0;
+  const int64_t Np = ntn * kTileW;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  static std::atomic<bool> split_set[64], pair_set[64];
+  bsf_status st;
+  CUtensorMap map_a, map_b, map_d, map_c;
+  const int64_t tiles_n = (ntn + 1) / 2, pairs = sm_count() / 2;
+  if (M > kMaxTok && (M + 127) / 128 * tiles_n >= 48) {
+    int tok = 0;
+    int64_t least = INT64_MAX;
+    for (int n = kPairMaxTok; n >= 128; n -= 32) {
+      const int64_t tiles = (M + n - 1) / n * tiles_n;
+      const int64_t cost = (tiles + pairs - 1) / pairs * (nkb * (2 * n > 400 ? 2 * n : 400) + 1000);
+      if (cost < least) least = cost, tok = n;
+    }
+    const int64_t tiles_m = (M + tok - 1) / tok;
+    if (tiles_m * tiles_n > INT32_MAX) return BSF_ERR_UNSUPPORTED;
+    PairArgs p;
+    p.sfa = sfa;
+    p.sfa_ld = sfa_ld;
+    p.sfb = sfb;
+    p.Np = Np;
+    p.addend = static_cast<const uint16_t*>(addend);
+    p.ldc = ldc;
+    p.d = static_cast<uint16_t*>(d);
+    p.ldd = ldd;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.nkb = static_cast<int>(nkb);
+    p.nw = static_cast<int>((nkb + 3) / 4);
+    p.tiles_m = static_cast<int>(tiles_m);
+    p.tiles_n = static_cast<int>(tiles_n);
+    p.tok = tok;
+    p.tiled = tiled;
+    p.vec8 = aligned16(d) && ldd % 8 == 0 && (!addend || (aligned16(addend) && ldc % 8 == 0));
+    const int stage_bytes = 2 * (kTileW + tok / 2) * kTileK;
+    p.stages = (kSmemBytes - 1024 - kPairBarBytes - 16 * kBoxBytes) / stage_bytes;
+    if (p.stages > kPairMaxStages) p.stages = kPairMaxStages;
+    p.err = err;
+    if (tiled ? !make_map(&map_b, b, Np * nkb, 128, 2 * kTileW) : !make_map(&map_b, b, Np, K, kTileW))
+      return BSF_ERR_CUDA;
+    if (!make_map(&map_a, a, M, K, tok / 2)) return BSF_ERR_CUDA;
+    map_d = map_c = map_a;                           // (not used without 16-byte aligned rows)
+    if (p.vec8 && !make_map_bf16(&map_d, d, M, N, ldd)) return BSF_ERR_CUDA;
+    if (p.vec8 && addend && !make_map_bf16(&map_c, addend, M, N, ldc)) return BSF_ERR_CUDA;
+    if ((st = allow_smem(reinterpret_cast<const void*>(dense_pair_kernel), kSmemBytes, pair_set)) != BSF_OK) return st;
+    const int64_t used = tiles_m * tiles_n < pairs ? tiles_m * tiles_n : pairs;
+    void* args[] = {&map_b, &map_a, &map_d, &map_c, &p};
+    return launch_cluster(reinterpret_cast<const void*>(dense_pair_kernel), static_cast<unsigned>(2 * used), kPairThreads,
+                          kSmemBytes, 2, s, args);
+  }
+
+  const int64_t chunks = (M + kMaxTok - 1) / kMaxTok;
+  const int64_t tiles = ntn * chunks;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= sm_count() && nkb >= split * 4) split *= 2;
   if (tiles * split > INT32_MAX) return BSF_ERR_UNSUPPORTED;
-
   DenseArgs p;
   p.sfa = sfa;
   p.sfa_ld = sfa_ld;
   p.sfb = sfb;
-  p.Np = ntn * kTileW;
+  p.Np = Np;
   p.addend = static_cast<const uint16_t*>(addend);
   p.ldc = ldc;
   p.d = static_cast<uint16_t*>(d);
@@ -323,47 +859,22 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   p.nkb = static_cast<int>(nkb);
   p.nw = static_cast<int>((nkb + 3) / 4);
   p.chunks = static_cast<int>(chunks);
+  // equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * 256 < M)
   p.per = static_cast<int>(((M + chunks - 1) / chunks + 15) / 16 * 16);
-  // (equal chunks: the last one may be shorter; rounding up to 16 never leaves one empty)
   p.split = split;
   const int stage_bytes = kTileW * kTileK + p.per * kTileK;
   p.stages = (kSmemBytes - 1024 - kBarBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int cols = kAccCol + (p.per + 31) / 32 * 32;
   p.tmem_cols = cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
-  p.tiled = (flags & BSF_B_TILED) != 0;
+  p.tiled = tiled;
   p.vec4 = (reinterpret_cast<uintptr_t>(d) & 7) == 0 && ldd % 4 == 0 &&
            (!addend || ((reinterpret_cast<uintptr_t>(addend) & 7) == 0 && ldc % 4 == 0));
   p.err = err;
-
-  CUtensorMap map_a, map_b;
+  if (tiled ? !make_map(&map_b, b, Np * nkb, 128, kTileW) : !make_map(&map_b, b, Np, K, kTileW)) return BSF_ERR_CUDA;
   if (!make_map(&map_a, a, M, K, p.per)) return BSF_ERR_CUDA;
-  if (p.tiled ? !make_map(&map_b, b, p.Np * nkb, 128, kTileW) : !make_map(&map_b, b, p.Np, K, kTileW))
-    return BSF_ERR_CUDA;
-  static std::atomic<bool> attr_set[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dense_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
-        cudaSuccess)
-      return BSF_ERR_CUDA;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, dense_split_kernel, map_b, map_a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return BSF_ERR_CUDA;
-  }
-  return launch_status();
+  if ((st = allow_smem(reinterpret_cast<const void*>(dense_split_kernel), kSmemBytes, split_set)) != BSF_OK) return st;
+  void* args[] = {&map_b, &map_a, &p};
+  return launch_cluster(reinterpret_cast<const void*>(dense_split_kernel), static_cast<unsigned>(tiles * split), kThreads,
+                        kSmemBytes, static_cast<unsigned>(split), s, args);
 }
