@@ -7,15 +7,20 @@
 // UE8M0 block scales (kind::mxf8f6f4, one scale per row per 32 K; a 128-wide
 // block's byte serves its four K = 32 steps, picked by the scale-factor id).
 //
-// One weight matrix gives only N / 128 tiles of 128 weight rows, too few for
-// 152 SMs, so a tile's K is split over a cluster of S CTAs: each multiplies its
-// share of the K-blocks into tensor memory, writes the FP32 partial to its own
-// shared memory, and after a cluster barrier every CTA sums a slice of the
-// tile's tokens over the S partials through distributed shared memory, in rank
-// order (no atomics, no workspace, bit-identical from run to run).
+// Weights are the MMA's M = 128 rows (256 in a CTA pair) and tokens its N, so one token costs a 128 x 16
+// product.  Two forms, chosen by the time each would take (choose_plan):
 //
-// Weights are the MMA's M = 128 rows and tokens its N (16..256), so one token
-// costs a 128 x 16 product.
+// * Split (few tokens).  One weight matrix gives only N / 128 tiles of 128 weight rows, too few for 152 SMs
+//   that each take about 52 bytes a cycle from L2, so a tile's K is split over a cluster of S CTAs: each
+//   multiplies its share of the K-blocks into tensor memory, writes the FP32 partial to its own shared
+//   memory, and after a cluster barrier every CTA sums a slice of the tile's tokens over the S partials
+//   through distributed shared memory, in rank order (no atomics, no workspace, bit-identical from run
+//   to run).  Bound by latency: 1 x 4096 x 7168 takes 7.6 us, of which the 29 MB of weights need 4.3.
+// * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 224 tokens with one cta_group::2 MMA per
+//   32 K: each stages 128 weight rows and half of the tokens, so a staged byte feeds twice the products
+//   that it would in one CTA, which shared memory could not keep up with.  Two accumulators let a tile's
+//   output drain under the next tile's MMAs.  Bound by the tensor cores and, in long runs, by power:
+//   8192 x 4096 x 7168 takes 144 us, 3.34 PFLOP/s, 87 % of twice the measured bf16 burst rate.
 #include "common.cuh"
 #include "host_utils.h"
 #include "tma_map.h"
@@ -25,14 +30,16 @@ namespace {
 
 constexpr int kTileW = 128;                     // weight rows per tile
 constexpr int kTileK = 128;                     // K per stage
-constexpr int kMaxTok = 256;                    // tokens per tile
+constexpr int kMaxTok = 128;                    // tokens per tile
 constexpr int kSfSlots = 4;                     // ring of scale words in tensor memory (512 K each)
-constexpr int kSfCols = 16;                     // columns per slot: 4 of weights, up to 8 of tokens at 4
+constexpr int kSfCols = 16;                     // columns per slot: 4 of weights, then the tokens' from 4 on
 constexpr int kAccCol = kSfSlots * kSfCols;     // accumulator columns start here
-constexpr int kThreads = 192;                   // producer, issuer, 4 scale + epilogue warps
+constexpr int kMaxIssuers = 2;
+constexpr int kThreads = 32 * (1 + kMaxIssuers + 4);   // producer, issuers, 4 scale + epilogue warps
 constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
 constexpr int kSmemBytes = 227 * 1024;
+constexpr int kHalfSmemBytes = 112 * 1024;      // two CTAs per SM
 
 struct DenseArgs {
   const int32_t* sfa;
@@ -43,9 +50,10 @@ struct DenseArgs {
   int64_t ldc;
   uint16_t* d;
   int64_t ldd;
-  int M, N, nkb, nw;
+  int M, N, nkb;
   int chunks, per;           // token chunks per weight tile, tokens of a full chunk (multiple of 16)
   int split, stages;
+  int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between their accumulators
   uint32_t tmem_cols;
   int tiled;
   int vec4;                  // four neighbouring columns of D (and C) are 8-byte aligned
@@ -55,15 +63,18 @@ struct DenseArgs {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t local_smem, uint32_t rank) {
+// shared::cluster address of this CTA's shared-memory address in the CTA of the given rank
+__device__ __forceinline__ uint32_t map_rank(uint32_t local_smem, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local_smem), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-      : "r"(local_smem), "r"(rank)
-      : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
@@ -87,7 +98,58 @@ __device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// Tokens [j0, j1) of a tile: their S partials part[token][weight row], one in each CTA of the cluster,
+// summed in rank order and stored.  A thread takes items (token, four weight rows) and has the loads of
+// U of them in flight: a load from another CTA's shared memory takes about as long as a whole sum.
+template <int S, int U>
+__device__ __forceinline__ void sum_and_store(const DenseArgs& p, uint32_t part, int n0, int tok0, int j0, int j1) {
+  uint32_t base[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) base[s] = map_rank(part, s);
+  for (int i0 = threadIdx.x + j0 * 32; i0 < j1 * 32; i0 += U * kThreads) {
+    float4 v[U][S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * kThreads, j1 * 32 - 1);     // (past the end: the last item again, not stored)
+#pragma unroll
+      for (int s = 0; s < S; ++s) v[u][s] = ld_cluster_f4(base[s] + i * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= j1 * 32) break;
+      float f[4] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w};
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        f[0] += v[u][s].x;
+        f[1] += v[u][s].y;
+        f[2] += v[u][s].z;
+        f[3] += v[u][s].w;
+      }
+      const int n = n0 + (i & 31) * 4;
+      const int64_t row = tok0 + (i >> 5);
+      if (p.vec4 && n + 4 <= p.N) {
+        if (p.addend) {
+          const uint2 cv = *reinterpret_cast<const uint2*>(p.addend + row * p.ldc + n);
+          f[0] += __uint_as_float(cv.x << 16);
+          f[1] += __uint_as_float(cv.x & 0xFFFF0000u);
+          f[2] += __uint_as_float(cv.y << 16);
+          f[3] += __uint_as_float(cv.y & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(p.d + row * p.ldd + n) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          if (n + x >= p.N) break;
+          const float a = p.addend ? __uint_as_float(static_cast<uint32_t>(p.addend[row * p.ldc + n + x]) << 16) : 0.f;
+          p.d[row * p.ldd + n + x] = static_cast<uint16_t>(pack_bf16x2((x & 2 ? x & 1 ? f[3] : f[2] : x & 1 ? f[1] : f[0]) + a, 0.f) & 0xFFFFu);
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
     dense_split_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ CUtensorMap tmap_a,
                        const DenseArgs p) {
   extern __shared__ uint8_t smem_raw[];
@@ -118,23 +180,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSfSlots; ++s) {
       mbar_init(&sf_full[s], 4);
-      mbar_init(&sf_empty[s], 1);
+      mbar_init(&sf_empty[s], p.issuers);
     }
-    mbar_init(acc_full, 1);
+    mbar_init(acc_full, p.issuers);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_b);
     tma_prefetch_desc(&tmap_a);
   }
+  pdl_launch_dependents();
+  // Dependent launch: the weights are not written by the preceding kernel, so while it drains their first
+  // stages are pulled into L2; nothing that it writes, and no global memory it may still read, is touched
+  // before it has completed.
+  if (warp == 0 && lane == 0) {
+    const int most = min(kb1, kb0 + p.stages);
+    for (int kb = kb0; kb < most; ++kb) {
+      if (p.tiled)
+        tma_prefetch_l2(&tmap_b, 0, (nt * p.nkb + kb) * kTileW);
+      else
+        tma_prefetch_l2(&tmap_b, kb * kTileK, nt * kTileW);
+    }
+  }
+  pdl_wait();
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  // (the producer, whose own thread initialised the barriers, does not wait for the others)
+  if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  else asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = warp != 0 ? *tmem_slot : 0u;
 
   bool have = false;                       // this warp holds a complete accumulator (epilogue warps)
   if (warp == 0) {
@@ -163,36 +241,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, slot = 0, sf_phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (kb == kb0 || (kb & 3) == 0) {
-          if (!mbar_wait(&sf_full[slot], sf_phase, abort_flag, p.err)) { ok = false; break; }
-        }
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
-        tc_fence_after();
+  } else if (warp <= kMaxIssuers) {
+    // ------------------------------------------------------------ MMA issuers
+    // Issuer i takes the K-blocks kb % issuers == i into an accumulator of its own: a narrow MMA keeps its
+    // issuing thread busy for about 75 cycles whatever its N, and each wait about 150, so one thread
+    // takes 620 cycles per K-block where the product of up to 64 tokens needs 130.
+    const int me = warp - 1;
+    if (me < p.issuers && lane == 0) {
+      const uint32_t d_tmem = tmem_base + kAccCol + me * p.acc_stride;
+      uint32_t slot = 0, sf_phase = 0;
+      uint32_t stage = (me - kb0) & (p.issuers - 1), phase = 0;    // of this issuer's first K-block
+      bool ok = true, first = true;
+      for (int g = kb0 >> 2; g <= (kb1 - 1) >> 2 && ok; ++g) {
+        if (!mbar_wait(&sf_full[slot], sf_phase, abort_flag, p.err)) break;
         const uint32_t sfw = tmem_base + slot * kSfCols;
-        const uint8_t* src = smem + stage * stage_bytes;
-        const uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
-        const uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + kTileW * kTileK));
-        const uint32_t idesc = idesc_mxf8_e4m3(kTileW, mma_n, kb & 3, kb & 3);
+        for (int kb = 4 * g + me; kb < 4 * g + 4; kb += p.issuers) {
+          if (kb < kb0 || kb >= kb1) continue;
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+          tc_fence_after();
+          const uint8_t* src = smem + stage * stage_bytes;
+          const uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
+          const uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + kTileW * kTileK));
+          const uint32_t idesc = idesc_mxf8_e4m3(kTileW, mma_n, kb & 3, kb & 3);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_mxf8(tmem_base + kAccCol, adesc + 2 * k, bdesc + 2 * k, idesc, sfw, sfw + 4, kb != kb0 || k != 0);
-        tc_commit(&empty[stage]);
-        if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
-        if ((kb & 3) == 3) {
-          tc_commit(&sf_empty[slot]);
-          if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
+          for (int k = 0; k < 4; ++k)
+            mma_mxf8(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sfw, sfw + 4, !first || k != 0);
+          first = false;
+          tc_commit(&empty[stage]);
+          stage += p.issuers;              // (stages are a multiple of issuers)
+          if (stage >= static_cast<uint32_t>(p.stages)) { stage -= p.stages; phase ^= 1u; }
         }
+        if (!ok) break;
+        tc_commit(&sf_empty[slot]);
+        if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
       }
       // commits on every way out: TMEM is released only after the issued MMAs are done
       tc_commit(acc_full);
       wait_quiet(acc_full, 0);
-      if (!ok) *abort_flag = 1;
     }
     __syncwarp();
   } else {
@@ -204,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ncols = (mma_n + 31) / 32;
     uint32_t slot = 0, sf_phase = 0;
     bool ok = true;
-    for (int g = kb0 >> 2; g <= (kb1 - 1) >> 2; ++g) {
-      uint32_t w[4], a[kMaxTok / 32];
+    const int g_last = (kb1 - 1) >> 2;
+    // the next word is in flight while one is written
+    uint32_t w[4], a[kMaxTok / 32];
+    auto load = [&](int g) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         w[c] = static_cast<uint32_t>(__ldg(p.sfb + g * p.Np + nt * kTileW + 32 * c + lane));
@@ -215,12 +302,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         a[c] = 0x7F7F7F7Fu;
         if (c < ncols && r < p.M) a[c] = static_cast<uint32_t>(__ldg(p.sfa + g * p.sfa_ld + r));
       }
+    };
+    load(kb0 >> 2);
+    for (int g = kb0 >> 2; g <= g_last; ++g) {
+      uint32_t w0[4], a0[kMaxTok / 32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w0[c] = w[c];
+#pragma unroll
+      for (int c = 0; c < kMaxTok / 32; ++c) a0[c] = a[c];
+      if (g < g_last) load(g + 1);
       if (!wait_all(&sf_empty[slot], sf_phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
-      tmem_st_x4(quad + slot * kSfCols, w[0], w[1], w[2], w[3]);
+      tmem_st_x4(quad + slot * kSfCols, w0[0], w0[1], w0[2], w0[3]);
 #pragma unroll
       for (int c = 0; c < kMaxTok / 32; ++c)
-        if (c < ncols) tmem_st_x1(quad + slot * kSfCols + 4 + c, a[c]);
+        if (c < ncols) tmem_st_x1(quad + slot * kSfCols + 4 + c, a0[c]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -231,61 +327,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       have = *abort_flag == 0;
       have = __all_sync(0xffffffffu, have);
       tc_fence_after();
-      // partial[token][weight row]: every stage has been consumed, so their memory holds it
-      float* part = reinterpret_cast<float*>(smem);
-      for (int c0 = 0; have && c0 < ntok; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld_x32(quad + kAccCol + c0, r);
-        tmem_wait_ld_regs(r);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c0 + j < ntok) part[(c0 + j) * kTileW + 32 * q + lane] = __uint_as_float(r[j]);
-      }
     }
     if (!have && lane == 0) *abort_flag = 1;
   }
 
+  // ---------------------------------------------------------------- partial to shared memory, sum, store
+  // part[token][weight row] takes the place of the stages, which have all been consumed.  (Writing the
+  // partials straight into the shared memory of the CTAs that sum them took 0.8 us longer for 64 tokens:
+  // it needs another cluster barrier first, and remote 4-byte stores are slow.)
+  if (have) {
+    const int q = warp & 3;
+    const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol;
+    float* part = reinterpret_cast<float*>(smem) + 32 * q + lane;
+    for (int c0 = 0; c0 < ntok; c0 += 32) {      // (whole chunks: the rows past ntok are not read)
+      uint32_t r[32], o[32];
+      tmem_ld_x32(quad + c0, r);
+      if (p.issuers == 2) tmem_ld_x32(quad + p.acc_stride + c0, o);
+      tmem_wait_ld_regs(r);
+      if (p.issuers == 2) {
+        tmem_wait_ld_regs(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[(c0 + j) * kTileW] = __uint_as_float(r[j]);
+    }
+  }
   tc_fence_before();
   if (p.split > 1) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.tmem_cols);
   }
-  // ---------------------------------------------------------------- sum over the cluster, store
   if (*abort_flag == 0) {
-    const int j0 = ntok * rank / p.split, j1 = ntok * (rank + 1) / p.split;
-    const uint32_t base = smem_u32(smem);
-    for (int i = threadIdx.x + j0 * 32; i < j1 * 32; i += kThreads) {
-      const int j = i >> 5, c = (i & 31) * 4;
-      const int n = nt * kTileW + c;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const uint32_t at = base + (j * kTileW + c) * 4;
-      for (int s = 0; s < p.split; ++s) {
-        const float4 v = ld_cluster_f4(at, s);
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-      }
-      const int64_t row = tok0 + j;
-      float f[4] = {acc.x, acc.y, acc.z, acc.w};
-      if (p.vec4 && n + 4 <= p.N) {
-        if (p.addend) {
-          const uint2 cv = *reinterpret_cast<const uint2*>(p.addend + row * p.ldc + n);
-          f[0] += __uint_as_float(cv.x << 16);
-          f[1] += __uint_as_float(cv.x & 0xFFFF0000u);
-          f[2] += __uint_as_float(cv.y << 16);
-          f[3] += __uint_as_float(cv.y & 0xFFFF0000u);
-        }
-        *reinterpret_cast<uint2*>(p.d + row * p.ldd + n) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (n + x >= p.N) break;
-          if (p.addend) f[x] += __uint_as_float(static_cast<uint32_t>(p.addend[row * p.ldc + n + x]) << 16);
-          p.d[row * p.ldd + n + x] = static_cast<uint16_t>(pack_bf16x2(f[x], 0.f) & 0xFFFFu);
-        }
-      }
+    const int j0 = ntok * rank / p.split, j1 = ntok * (rank + 1) / p.split, n0 = nt * kTileW;
+    const uint32_t part = smem_u32(smem);
+    switch (p.split) {
+      case 1: sum_and_store<1, 4>(p, part, n0, tok0, j0, j1); break;
+      case 2: sum_and_store<2, 4>(p, part, n0, tok0, j0, j1); break;
+      case 4: sum_and_store<4, 2>(p, part, n0, tok0, j0, j1); break;
+      default: sum_and_store<8, 1>(p, part, n0, tok0, j0, j1); break;
     }
   }
   // a CTA's shared memory stays until every CTA of the cluster has read it
@@ -323,12 +404,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
-}
-// shared::cluster address of this CTA's shared-memory address in the CTA of the given rank
-__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
 }
 // Arrivals and waits between the CTAs of a pair that order tensor-memory accesses only: relaxed, because the
 // tcgen05 fences on both sides order those accesses.  (Release and acquire at cluster scope also
@@ -451,6 +526,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&tmap_b);
     tma_prefetch_desc(&tmap_a);
   }
+  pdl_launch_dependents();
+  pdl_wait();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
@@ -479,7 +556,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int wt = tn * 2 + static_cast<int>(rank);               // 128-row weight tile of this CTA
         for (int kb = 0; kb < p.nkb; kb += 2) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
-          const uint32_t bar = map_rank(&full[stage], 0);
+          const uint32_t bar = map_rank(smem_u32(&full[stage]), 0);
           uint8_t* dst = smem + stage * stage_bytes;
           if (weights) {
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
@@ -616,7 +693,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(map_rank(&sf_full[slot], 0));
+      if (lane == 0) arrive_cluster(map_rank(smem_u32(&sf_full[slot]), 0));
       if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
       if (t >= total) break;
     }
@@ -667,7 +744,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (c == c_last - 1) {              // the accumulator's last columns are in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(map_rank(&acc_empty[acc], 0));
+          if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
         }
         if (c - c_first >= cuts) continue;
         if (p.vec8) {
@@ -734,36 +811,113 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ClusterLaunch(unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t stream) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Clusters and programmatic dependents: every kernel here waits (pdl_wait) before it touches memory that the
+// preceding kernel may use.
 bsf_status launch_cluster(const void* kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
                           cudaStream_t stream, void** args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
+  ClusterLaunch launch(grid, threads, smem, cluster, stream);
+  if (cudaLaunchKernelExC(&launch.cfg, kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return BSF_ERR_CUDA;
   }
   return launch_status();
 }
 
-bsf_status allow_smem(const void* kernel, size_t bytes, std::atomic<bool>* set) {
+// Once per device: both kernels may use all shared memory, and the number of CTAs of the split kernel that
+// run at once, one per SM, in clusters of 1, 2, 4 and 8 (a cluster lives in one GPC, so 8 leave SMs idle).
+struct DeviceLimits {
+  std::atomic<int> ctas[4];
+  std::atomic<bool> ready;
+};
+bsf_status device_limits(const DeviceLimits** out) {
+  static DeviceLimits limits[64];
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
-      return BSF_ERR_CUDA;
-    set[dev].store(true, std::memory_order_release);
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BSF_ERR_CUDA;
+  DeviceLimits& l = limits[dev];
+  if (!l.ready.load(std::memory_order_acquire)) {      // (racing first calls store the same values)
+    const void* kernels[2] = {reinterpret_cast<const void*>(dense_split_kernel),
+                              reinterpret_cast<const void*>(dense_pair_kernel)};
+    for (const void* k : kernels) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+          cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+              cudaSuccess)
+        return BSF_ERR_CUDA;
+    }
+    for (int i = 0; i < 4; ++i) {
+      ClusterLaunch launch(8u << i, kThreads, kSmemBytes, 1u << i, nullptr);
+      launch.cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernels[0], &launch.cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return BSF_ERR_CUDA;
+      }
+      l.ctas[i].store(n << i, std::memory_order_relaxed);
+    }
+    l.ready.store(true, std::memory_order_release);
   }
+  *out = &l;
   return BSF_OK;
+}
+
+// Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to
+// 140 products (1 .. 5000 tokens; weights 256 x 7168, 512 x 4096, 1024 x 1024, 2112 x 7168, 4096 x 2048,
+// 4096 x 7168, 7168 x 2048, 8192 x 512) timed in every form on a GB300: the choice is within 0.5 % of the
+// best form on average, within 12 % at worst.  Both sides, 4096 x 7168: 256 tokens 14.6 us split against
+// 19.6 in pairs, 1024 tokens 38.7 against 33.4; 1024 x 1024 takes 1024 tokens in 6.4 us split, 7.5 in pairs.
+struct Plan {
+  bool pair;
+  int tok;                  // pairs: tokens per tile; split: most tokens per tile
+  int split;
+};
+Plan choose_plan(int64_t M, int64_t N, int64_t nkb, const DeviceLimits& limits) {
+  const int64_t ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
+  Plan best = {false, 64, 1};
+  int64_t least = INT64_MAX;
+  for (int tok = 64; tok <= kMaxTok; tok += 64) {
+    if (tok > 64 && M <= 64) break;
+    const int64_t chunks = (M + tok - 1) / tok, per = ((M + chunks - 1) / chunks + 15) / 16 * 16;
+    const int64_t alone = per > 64;                    // one CTA per SM: it cannot start under its predecessor
+    for (int i = 0; i < 4; ++i) {
+      const int64_t split = int64_t(1) << i, ctas = ntn * chunks * split;
+      if (i > 0 && (nkb < 2 * split || ctas > 2 * sms)) break;
+      const int64_t at_once = alone ? limits.ctas[i].load(std::memory_order_relaxed) : sms;
+      const int64_t rounds = (ctas + at_once - 1) / at_once, kbs = (nkb + split - 1) / split;
+      const int64_t ns = 3700 + 5 * per + 500 * i + 1200 * alone + rounds * kbs * 230 + (rounds - 1) * (1300 + 3600 * alone);
+      if (ns < least) {
+        least = ns;
+        best = {false, tok, static_cast<int>(split)};
+      }
+    }
+  }
+  for (int tok = kPairMaxTok; tok >= 128; tok -= 32) {
+    const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
+    const int64_t step = 22 * tok / 10 > 470 ? 22 * tok / 10 : 470;        // two K-blocks
+    const int64_t ns = 4300 + waves * ((nkb + 1) / 2 * step - 500 + 14 * tok);
+    if (ns < least) {
+      least = ns;
+      best = {true, tok, 1};
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -791,20 +945,16 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   const bool tiled = (flags & BSF_B_TILED) != 0;
   const int64_t Np = ntn * kTileW;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  static std::atomic<bool> split_set[64], pair_set[64];
-  bsf_status st;
-  CUtensorMap map_a, map_b, map_d, map_c;
-  const int64_t tiles_n = (ntn + 1) / 2, pairs = sm_count() / 2;
-  if (M > kMaxTok && (M + 127) / 128 * tiles_n >= 48) {
-    int tok = 0;
-    int64_t least = INT64_MAX;
-    for (int n = kPairMaxTok; n >= 128; n -= 32) {
-      const int64_t tiles = (M + n - 1) / n * tiles_n;
-      const int64_t cost = (tiles + pairs - 1) / pairs * (nkb * (2 * n > 400 ? 2 * n : 400) + 1000);
-      if (cost < least) least = cost, tok = n;
-    }
-    const int64_t tiles_m = (M + tok - 1) / tok;
-    if (tiles_m * tiles_n > INT32_MAX) return BSF_ERR_UNSUPPORTED;
+  const DeviceLimits* limits;
+  const bsf_status st = device_limits(&limits);
+  if (st != BSF_OK) return st;
+  const Plan plan = choose_plan(M, N, nkb, *limits);
+  CUtensorMap map_a, map_b;
+
+  if (plan.pair) {
+    const int tok = plan.tok;
+    const int64_t tiles_m = (M + tok - 1) / tok, tiles_n = (ntn + 1) / 2, tiles = tiles_m * tiles_n;
+    if (tiles > INT32_MAX) return BSF_ERR_UNSUPPORTED;
     PairArgs p;
     p.sfa = sfa;
     p.sfa_ld = sfa_ld;
@@ -827,24 +977,21 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
     p.stages = (kSmemBytes - 1024 - kPairBarBytes - 16 * kBoxBytes) / stage_bytes;
     if (p.stages > kPairMaxStages) p.stages = kPairMaxStages;
     p.err = err;
+    CUtensorMap map_d, map_c;
     if (tiled ? !make_map(&map_b, b, Np * nkb, 128, 2 * kTileW) : !make_map(&map_b, b, Np, K, kTileW))
       return BSF_ERR_CUDA;
     if (!make_map(&map_a, a, M, K, tok / 2)) return BSF_ERR_CUDA;
     map_d = map_c = map_a;                           // (not used without 16-byte aligned rows)
     if (p.vec8 && !make_map_bf16(&map_d, d, M, N, ldd)) return BSF_ERR_CUDA;
     if (p.vec8 && addend && !make_map_bf16(&map_c, addend, M, N, ldc)) return BSF_ERR_CUDA;
-    if ((st = allow_smem(reinterpret_cast<const void*>(dense_pair_kernel), kSmemBytes, pair_set)) != BSF_OK) return st;
-    const int64_t used = tiles_m * tiles_n < pairs ? tiles_m * tiles_n : pairs;
+    const int64_t pairs = sm_count() / 2, used = tiles < pairs ? tiles : pairs;
     void* args[] = {&map_b, &map_a, &map_d, &map_c, &p};
     return launch_cluster(reinterpret_cast<const void*>(dense_pair_kernel), static_cast<unsigned>(2 * used), kPairThreads,
                           kSmemBytes, 2, s, args);
   }
 
-  const int64_t chunks = (M + kMaxTok - 1) / kMaxTok;
-  const int64_t tiles = ntn * chunks;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= sm_count() && nkb >= split * 4) split *= 2;
-  if (tiles * split > INT32_MAX) return BSF_ERR_UNSUPPORTED;
+  const int64_t chunks = (M + plan.tok - 1) / plan.tok, tiles = ntn * chunks;
+  if (tiles * plan.split > INT32_MAX) return BSF_ERR_UNSUPPORTED;
   DenseArgs p;
   p.sfa = sfa;
   p.sfa_ld = sfa_ld;
@@ -857,15 +1004,20 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.nkb = static_cast<int>(nkb);
-  p.nw = static_cast<int>((nkb + 3) / 4);
   p.chunks = static_cast<int>(chunks);
-  // equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * 256 < M)
+  // equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * tok < M)
   p.per = static_cast<int>(((M + chunks - 1) / chunks + 15) / 16 * 16);
-  p.split = split;
-  const int stage_bytes = kTileW * kTileK + p.per * kTileK;
-  p.stages = (kSmemBytes - 1024 - kBarBytes) / stage_bytes;
+  p.split = plan.split;
+  const int stage_bytes = (kTileW + p.per) * kTileK;
+  const size_t smem = p.per <= 64 ? kHalfSmemBytes : kSmemBytes;
+  p.stages = (static_cast<int>(smem) - 1024 - kBarBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int cols = kAccCol + (p.per + 31) / 32 * 32;
+  p.acc_stride = (p.per + 31) / 32 * 32;
+  // (an issuer without a K-block would leave its accumulator unwritten)
+  p.issuers = nkb / p.split >= kMaxIssuers ? kMaxIssuers : 1;
+  // a stage always goes to the same issuer, whose own waits then see its barrier's phases in order
+  p.stages = p.stages / p.issuers * p.issuers;
+  const int cols = kAccCol + p.issuers * p.acc_stride;
   p.tmem_cols = cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
   p.tiled = tiled;
   p.vec4 = (reinterpret_cast<uintptr_t>(d) & 7) == 0 && ldd % 4 == 0 &&
@@ -873,8 +1025,7 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   p.err = err;
   if (tiled ? !make_map(&map_b, b, Np * nkb, 128, kTileW) : !make_map(&map_b, b, Np, K, kTileW)) return BSF_ERR_CUDA;
   if (!make_map(&map_a, a, M, K, p.per)) return BSF_ERR_CUDA;
-  if ((st = allow_smem(reinterpret_cast<const void*>(dense_split_kernel), kSmemBytes, split_set)) != BSF_OK) return st;
   void* args[] = {&map_b, &map_a, &p};
-  return launch_cluster(reinterpret_cast<const void*>(dense_split_kernel), static_cast<unsigned>(tiles * split), kThreads,
-                        kSmemBytes, static_cast<unsigned>(split), s, args);
+  return launch_cluster(reinterpret_cast<const void*>(dense_split_kernel), static_cast<unsigned>(tiles * p.split), kThreads,
+                        smem, static_cast<unsigned>(p.split), s, args);
 }

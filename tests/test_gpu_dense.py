@@ -81,7 +81,11 @@ def test_inner_lengths(dev, K, M):
     p.check(p.run(), f"K={K}")
 
 
-@pytest.mark.parametrize("M,N,K", [(2048, 1536, 512), (1500, 2304, 1024), (4100, 640, 256), (513, 4096, 384)])
+# (sizes that reach every tile of the CTA pairs: 224, 192, 160 and 128 tokens, one tile per pair and several,
+# odd counts of 128-row weight tiles and of K-blocks)
+@pytest.mark.parametrize("M,N,K", [(2048, 1536, 512), (1500, 2304, 1024), (4100, 640, 256), (513, 4096, 384),
+                                   (777, 4096, 2048), (1500, 4096, 896), (640, 4096, 1152), (4700, 1100, 2048),
+                                   (1024, 7168, 640), (5000, 4096, 128)])
 def test_larger_products(dev, M, N, K):
     p = Problem(M, N, K, dev, seed=M, addend=True)
     p.check(p.run())
