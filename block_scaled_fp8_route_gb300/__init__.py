@@ -11,4 +11,4 @@ from .ops import (  # noqa: F401
     route_capacity, dispatch, dispatch_supported, grouped_gemm_contig, grouped_gemm_masked, combine, device_error, sf_ld, sf_words,
     gate, swiglu_quantise, prepare_dense_weight, dense_gemm,
 )
-from .pipeline import MoEPath, HostStreamedPath  # noqa: F401
+from .pipeline import MoEPath, MoEBlock, HostStreamedPath  # noqa: F401

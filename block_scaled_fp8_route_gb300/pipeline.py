@@ -222,6 +222,82 @@ class MoEPath:
         return self.z
 
 
+class MoEBlock:
+    """A whole MoE block on resident FP8 weights, from router logits to the block's output:
+
+        logits --gate--> topk ids, weights;  x --route--> gate-up GEMM --swiglu_quantise--> down GEMM
+        --combine--> z  (+ an expert that every token takes: dense gate-up, SwiGLU, dense down onto z)
+
+    ``w13_bf16`` [E, 2 I, K] holds each expert's gate rows and then its up rows, ``w2_bf16`` [E, K, I] its
+    down projection; ``shared`` = (w13 [2 S, K], w2 [K, S]) of the always-active expert, any width S.  The
+    other keyword arguments are those of ``ops.gate`` (``score``, ``bias``, ``groups``, ...).  Every step is
+    a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be captured."""
+
+    def __init__(self, E, kr, T, K, I, w13_bf16, w2_bf16, shared=None, layout=ops.CONTIGUOUS, align_or_max_m=128,
+                 device="cuda", expected_m=0, **gate):
+        if tuple(w13_bf16.shape) != (E, 2 * I, K) or tuple(w2_bf16.shape) != (E, K, I):
+            raise ValueError(f"expected w13 {(E, 2 * I, K)} and w2 {(E, K, I)}, got {tuple(w13_bf16.shape)} and "
+                             f"{tuple(w2_bf16.shape)}")
+        self.T, self.K, self.I, self.kr, self.gate_args = T, K, I, kr, gate
+        self.path = MoEPath(E, kr, T, K, 2 * I, w13_bf16, layout=layout, align_or_max_m=align_or_max_m,
+                            w2_bf16=w2_bf16, device=device, expected_m=expected_m)
+        self.z = self.path.z
+        self.topk_ids = torch.empty((T, kr), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((T, kr), dtype=torch.float32, device=device)
+        self.shared = None
+        if shared is not None:
+            w13, w2 = (w.to(device) for w in shared)
+            S = w2.shape[1]
+            if tuple(w13.shape) != (2 * S, K) or w2.shape[0] != K or S % 8:
+                raise ValueError(f"shared expert: expected w13 (2 S, {K}) and w2 ({K}, S) with S a multiple of 8, got "
+                                 f"{tuple(w13.shape)} and {tuple(w2.shape)}")
+            self.shared = (ops.prepare_dense_weight(w13), ops.prepare_dense_weight(w2))
+            Sp = (S + 127) // 128 * 128
+            self.shared_y = torch.empty((T, 2 * S), dtype=torch.bfloat16, device=device)
+            self.shared_q = torch.empty((T, Sp), dtype=torch.uint8, device=device)
+            self.shared_sf = torch.empty((ops.sf_words(Sp), ops.sf_ld(T)), dtype=torch.int32, device=device)
+
+    def step(self, x, logits, z=None, timer=None):
+        """x bf16 [T, K], logits [T, E] (float32 or bf16) -> z bf16 [T, K].  A token all of whose logits are
+        masked gets the always-active expert alone (zero without one)."""
+        t = timer if timer is not None else _no_timer
+        p, b = self.path, self.path.bufs
+        z = self.z if z is None else z
+        with t("gate"):
+            ops.gate(logits, self.kr, topk_ids=self.topk_ids, topk_weights=self.topk_weights, **self.gate_args)
+        p._stage_in(x, self.topk_ids, t)
+        with t("gemm"):
+            p.gemm(b.a_packed, b.sfa_packed, p.wq, p.sfb, p.y)
+        with t("swiglu"):
+            ops.swiglu_quantise(p.y, rows=(b.token_of_row, b.seg_start[p.E:]), q=p.q2, sf=p.sf2)
+        with t("gemm2"):
+            p.gemm(p.q2, p.sf2, p.w2q, p.sfb2, p.y2)
+        with t("combine"):
+            ops.combine(p.y2, b.output_index, self.topk_weights, z=z)
+        if self.shared is not None:
+            (b13, sfb13), (b2, sfb2) = self.shared
+            with t("shared"):
+                ops.quantise_act(x, q=p.q, sf=p.sf)
+                ops.dense_gemm(p.q, p.sf, b13, sfb13, self.shared_y.shape[1], d=self.shared_y)
+                ops.swiglu_quantise(self.shared_y, q=self.shared_q, sf=self.shared_sf)
+                ops.dense_gemm(self.shared_q, self.shared_sf, b2, sfb2, self.K, addend=z, d=z)
+        return z
+
+    def capture(self, x, logits):
+        """Record one step on these (static) tensors into a CUDA graph; ``replay()`` runs it on whatever they hold."""
+        self.step(x, logits)
+        torch.cuda.synchronize()
+        self._graph_inputs = (x, logits)             # the graph reads their memory: keep them alive with it
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.step(x, logits)
+        return self.graph
+
+    def replay(self):
+        self.graph.replay()
+        return self.z
+
+
 class HostStreamedPath:
     """Runs a MoEPath over batches held in pinned host memory, overlapping each
     batch's host-to-device copy and the previous result's device-to-host copy
