@@ -108,14 +108,46 @@ __device__ __forceinline__ void load_row(const GateArgs& p, int64_t t, int lane,
   }
 }
 
+// Order-preserving unsigned image of a float that is not NaN; 0 for -inf.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);                     // (-0 as +0)
+  const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return v > -INFINITY ? u : 0u;
+}
+
+// c[0] >= c[1] >= ... by Batcher's odd-even merge network (pruned to N; the comparators of an index past N
+// would only meet values that sort last).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&c)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1) {
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1) {
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(c[i + j], c[i + j + k]), lo = min(c[i + j], c[i + j + k]);
+            c[i + j] = hi;
+            c[i + j + k] = lo;
+          }
+        }
+      }
+    }
+  }
+}
+
 // What bounds it: a row is 4 E bytes, but choosing takes a fixed chain of warp operations, so short
-// batches are bound by that chain's latency and long ones by issue slots.  A row's keys are sorted once
-// within each lane (VPL <= 8; a stable exchange of neighbours, about 2.5 VPL^2 slots) so that a round of
-// the choice looks at one key per lane: one reduction, one ballot, and a shift in the lane that gave.
-// Wider lanes (VPL > 8) look through all their keys in each round instead, 5 VPL slots a round, which
-// is less than the sort for the kr of such routers.
-// Scores are computed only where they decide: with no bias the choice goes by the logits, and only the
-// kr chosen get an exp (plus the sum of a softmax that is not renormalised).
+// batches are bound by that chain's latency and long ones by issue slots.
+// * A key and its expert share one word: the key's leading bits, then the complement of the expert, so
+//   that the words are distinct, a tie goes to the lowest expert, and a maximum names its owner.  Lanes
+//   sort their words once (VPL <= 8; two instructions per comparator), and a round of the choice is one
+//   reduction and a shift in the lane that gave.  Wider lanes look through all their words in each round.
+// * The key's last bits do not fit.  bf16 logits have none there; otherwise, where two neighbours in the
+//   order agree in the bits that do fit (about one row in fifty), the row is chosen again by whole keys.
+// * Scores are computed only where they decide: with no bias the choice goes by the logits, and only the
+//   kr chosen get an exp (plus the sum of a softmax that is not renormalised).
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p) {
   pdl_launch_dependents();
@@ -222,62 +254,64 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
       }
     }
 
-    int my_id = -1;
-    if constexpr (VPL <= 8) {
-      uint32_t order = 0x76543210u;                 // nibble j: position of the j-th largest key
-      int idx[VPL];
+    if (!open) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) idx[i] = i;
+      for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
+    }
+    constexpr int kIdBits = VPL == 1 ? 5 : VPL == 2 ? 6 : VPL <= 4 ? 7 : VPL <= 8 ? 8 : VPL <= 16 ? 9 : 10;
+    constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
+    uint32_t c[VPL];
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) {
+    for (int i = 0; i < VPL; ++i) {
+      const uint32_t u = order_bits(key[i]);
+      c[i] = u ? (u & ~kIdMask) | (kIdMask - static_cast<uint32_t>(lane * VPL + i)) : 0u;
+    }
+    if constexpr (VPL <= 8) sort_down(c);
+    // round r's word ends up in lane r; one round more shows whether the last choice was clear
+    uint32_t mine = 0u, after = 0u;
+    for (int r = 0; r <= p.kr; ++r) {
+      uint32_t head = c[0];
+      if constexpr (VPL > 8) {
 #pragma unroll
-        for (int j = i; j > 0; --j) {
-          const bool up = key[j] > key[j - 1];
-          const float hi = fmaxf(key[j], key[j - 1]), lo = fminf(key[j], key[j - 1]);
-          const int ih = up ? idx[j] : idx[j - 1], il = up ? idx[j - 1] : idx[j];
-          key[j] = lo, key[j - 1] = hi;
-          idx[j] = il, idx[j - 1] = ih;
+        for (int i = 1; i < VPL; ++i) head = max(head, c[i]);
+      }
+      const uint32_t best = __reduce_max_sync(kAll, head);
+      if (r < p.kr) mine = lane == r ? best : mine; else after = best;
+      if (best == 0u) break;
+      if constexpr (VPL <= 8) {
+        if (c[0] == best) {
+#pragma unroll
+          for (int i = 0; i + 1 < VPL; ++i) c[i] = c[i + 1];
+          c[VPL - 1] = 0u;
         }
-      }
-      if constexpr (VPL > 1) {
-        order = 0;
+      } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) order |= static_cast<uint32_t>(idx[i]) << (4 * i);
+        for (int i = 0; i < VPL; ++i) c[i] = c[i] == best ? 0u : c[i];
       }
-      if (!open) key[0] = -INFINITY;                // a lane that never gives
-      for (int r = 0; r < p.kr; ++r) {
-        const float best = warp_max(key[0]);
-        if (best == -INFINITY) break;
-        const int from = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
-        const int e = __shfl_sync(kAll, lane * VPL + static_cast<int>(order & 15u), from);
-        if (lane == r) my_id = e;
-        if (lane == from) {
+    }
+    int my_id = mine ? static_cast<int>(kIdMask - (mine & kIdMask)) : -1;
+    if (!BF16 || biased) {
+      uint32_t next_word = __shfl_down_sync(kAll, mine, 1);
+      if (lane == p.kr - 1) next_word = after;
+      const bool unclear = lane < p.kr && next_word != 0u && ((mine ^ next_word) >> kIdBits) == 0u;
+      if (__any_sync(kAll, unclear)) {
+        my_id = -1;
+        for (int r = 0; r < p.kr; ++r) {
+          float head = key[0];
 #pragma unroll
-          for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
-          key[VPL - 1] = -INFINITY;
-          order >>= 4;
+          for (int i = 1; i < VPL; ++i) head = fmaxf(head, key[i]);
+          const float best = warp_max(head);
+          if (best == -INFINITY) break;
+          const int from = __ffs(__ballot_sync(kAll, head == best)) - 1;
+          int at = 0;
+#pragma unroll
+          for (int i = VPL - 1; i >= 0; --i) at = key[i] == best ? i : at;
+          const int e = __shfl_sync(kAll, lane * VPL + at, from);
+          if (lane == r) my_id = e;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (lane == from && i == at) key[i] = -INFINITY;
         }
-      }
-    } else {
-      if (!open) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
-      }
-      for (int r = 0; r < p.kr; ++r) {
-        float head = key[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i) head = fmaxf(head, key[i]);
-        const float best = warp_max(head);
-        if (best == -INFINITY) break;
-        const int from = __ffs(__ballot_sync(kAll, head == best)) - 1;
-        int at = 0;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i) at = key[i] == best ? i : at;
-        const int e = __shfl_sync(kAll, lane * VPL + at, from);
-        if (lane == r) my_id = e;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (lane == from && i == at) key[i] = -INFINITY;
       }
     }
 
@@ -314,7 +348,7 @@ void launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
   a.lane_groups = a.E == 32 * VPL && 32 % a.G == 0;
   while ((a.G << (a.group_shift + 1)) <= 32) ++a.group_shift;
   // one row per warp until every SM has its warps, then each warp goes on with the next row in flight
-  const int64_t most = static_cast<int64_t>(sm_count()) * (VPL <= 8 ? 10 : 5);
+  const int64_t most = static_cast<int64_t>(sm_count()) * (VPL <= 4 ? 12 : VPL <= 8 ? 8 : 4);
   const int64_t need = (a.T + kGateWarps - 1) / kGateWarps;
   const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
   if (bf16) gate_kernel<VPL, true><<<blocks, 32 * kGateWarps, 0, s>>>(a);
