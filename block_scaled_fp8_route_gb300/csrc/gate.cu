@@ -151,6 +151,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&c)[N]) {
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p) {
   pdl_launch_dependents();
+  pdl_wait();                                       // (launched as a dependent: nothing is read before)
   __shared__ float s_val[kGateWarps][VPL * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = p.E;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
 }
 
 template <int VPL>
-void launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
+bsf_status launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
   const int size = bf16 ? 2 : 4;
   const int bytes = VPL * size % 16 == 0 ? 16 : VPL * size % 8 == 0 ? 8 : VPL * size % 4 == 0 ? 4 : 2;
   a.wide = a.E == 32 * VPL && reinterpret_cast<uintptr_t>(a.logits) % bytes == 0 && a.ld * size % bytes == 0;
@@ -351,8 +352,7 @@ void launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(sm_count()) * (VPL <= 4 ? 12 : VPL <= 8 ? 8 : 4);
   const int64_t need = (a.T + kGateWarps - 1) / kGateWarps;
   const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
-  if (bf16) gate_kernel<VPL, true><<<blocks, 32 * kGateWarps, 0, s>>>(a);
-  else gate_kernel<VPL, false><<<blocks, 32 * kGateWarps, 0, s>>>(a);
+  return launch_dependent(bf16 ? gate_kernel<VPL, true> : gate_kernel<VPL, false>, blocks, 32 * kGateWarps, 0, s, a);
 }
 
 }  // namespace
@@ -397,16 +397,15 @@ extern "C" bsf_status bsf_gate(const void* logits, int logits_type, int64_t T, i
   const bool bf16 = logits_type == BSF_TYPE_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int vpl = (a.E + 31) / 32;
-  if (vpl == 1) launch_gate<1>(a, bf16, s);
-  else if (vpl == 2) launch_gate<2>(a, bf16, s);
-  else if (vpl == 3) launch_gate<3>(a, bf16, s);
-  else if (vpl == 4) launch_gate<4>(a, bf16, s);
-  else if (vpl == 5) launch_gate<5>(a, bf16, s);
-  else if (vpl == 6) launch_gate<6>(a, bf16, s);
-  else if (vpl == 7) launch_gate<7>(a, bf16, s);
-  else if (vpl == 8) launch_gate<8>(a, bf16, s);
-  else if (vpl <= 12) launch_gate<12>(a, bf16, s);
-  else if (vpl <= 16) launch_gate<16>(a, bf16, s);
-  else launch_gate<32>(a, bf16, s);
-  return launch_status();
+  if (vpl == 1) return launch_gate<1>(a, bf16, s);
+  if (vpl == 2) return launch_gate<2>(a, bf16, s);
+  if (vpl == 3) return launch_gate<3>(a, bf16, s);
+  if (vpl == 4) return launch_gate<4>(a, bf16, s);
+  if (vpl == 5) return launch_gate<5>(a, bf16, s);
+  if (vpl == 6) return launch_gate<6>(a, bf16, s);
+  if (vpl == 7) return launch_gate<7>(a, bf16, s);
+  if (vpl == 8) return launch_gate<8>(a, bf16, s);
+  if (vpl <= 12) return launch_gate<12>(a, bf16, s);
+  if (vpl <= 16) return launch_gate<16>(a, bf16, s);
+  return launch_gate<32>(a, bf16, s);
 }

@@ -35,10 +35,10 @@ inline bsf_status launch_status() {
 // that kernel drains, and it must call pdl_wait() before its first global memory access.
 // Returns the launch's configuration status.
 template <class... Params, class... Args>
-inline bsf_status launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+inline bsf_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
                                    cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

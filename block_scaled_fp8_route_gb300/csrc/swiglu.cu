@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(256, 4) swiglu_quantise_kernel(const uint16_t*
                                                                  const int32_t* __restrict__ row_token,
                                                                  const int32_t* __restrict__ rows_used, int rpw) {
   pdl_launch_dependents();
+  pdl_wait();                                       // (launched as a dependent: nothing is read before)
   const int Kp = (K + 127) & ~127;
   const int lane = threadIdx.x & 31;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * (8 * rpw) + (threadIdx.x >> 5);
@@ -193,7 +194,7 @@ extern "C" bsf_status bsf_swiglu_quantise(const void* y, int64_t T, int64_t K, i
   int rpw = 8;
   while (rpw > 1 && (T + 8 * rpw - 1) / (8 * rpw) * groups < least) rpw /= 2;
   const dim3 grid(static_cast<unsigned>((T + 8 * rpw - 1) / (8 * rpw)), static_cast<unsigned>(groups));
-  swiglu_quantise_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint16_t*>(y), T, static_cast<int>(K), ld, q, sf, sf_ld, token_of_row, rows_used, rpw);
-  return launch_status();
+  return launch_dependent(swiglu_quantise_kernel, grid, 256, 0, reinterpret_cast<cudaStream_t>(stream),
+                          static_cast<const uint16_t*>(y), T, static_cast<int>(K), ld, q, sf, sf_ld, token_of_row,
+                          rows_used, rpw);
 }

@@ -434,41 +434,42 @@ _SCORES = {"softmax": 0, "sigmoid": GATE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": GATE_GROUP_TOP2}
 
 
-def _refuse(t, dtype, what):
+# The checks of these operators are written out in the calls rather than shared: on a call of a few
+# microseconds every attribute of a tensor that is read, and every Python call, is a tenth of one.
+def _refuse(t, dtype, shape, what):
+    """Why tensor ``t`` is not a contiguous CUDA tensor of this type and shape."""
     if t.dtype != dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     raise ValueError(f"{what}: expected a CUDA tensor, got one on {t.device}")
 
 
-def _dptr(t, dtype, what):
-    """Address of a CUDA tensor of the given type."""
-    if t.dtype != dtype or not t.is_cuda:
-        _refuse(t, dtype, what)
-    return t.data_ptr()
+def _row_stride(t, rows, cols, what):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
+    return ld if rows > 1 else max(ld, cols)
 
 
-def _row_stride(t, what):
-    """Row stride of a 2-D tensor with contiguous rows."""
+def _two_dims(t, what):
     if t.dim() != 2:
-        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
-    rows, cols = t.shape
-    stride = t.stride()
-    if cols > 1 and stride[1] != 1:
-        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
-    return stride[0] if rows > 1 else max(stride[0], cols)
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows, got {t.dim()} dimensions")
+    return t.shape
 
 
-def _whole(t, shape, what):
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+def _used_on(stream, *tensors):
+    """The allocator keeps the memory of these outputs until the work queued on ``stream`` is done."""
+    for t in tensors:
+        if t.is_cuda:
+            t.record_stream(stream)
 
 
-def _raw_stream(stream, t):
-    """Handle of the given stream, or of the current stream of the tensor's device (looked up without
-    making a stream object, which costs 2.8 us of a small call)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+# handle of a device's current stream, without making a stream object (2.8 us of a call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, group_score="max", renormalise=True,
@@ -483,24 +484,30 @@ def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, gro
         raise ValueError(f"logits: expected float32 or bfloat16, got {logits.dtype}")
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError(f"score {score!r} / group_score {group_score!r}: expected softmax or sigmoid / max or top2")
-    ld = _row_stride(logits, "logits")
-    T, E = logits.shape
+    T, E = _two_dims(logits, "logits")
+    ld = _row_stride(logits, T, E, "logits")
+    out = (T, kr)
     if topk_ids is None:
-        topk_ids = torch.empty((T, kr), dtype=torch.int32, device=logits.device)
+        topk_ids = torch.empty(out, dtype=_I32, device=logits.device)
+    elif topk_ids.dtype != _I32 or topk_ids.shape != out or not topk_ids.is_contiguous():
+        _refuse(topk_ids, _I32, out, "topk_ids")
     if topk_weights is None:
-        topk_weights = torch.empty((T, kr), dtype=torch.float32, device=logits.device)
-    _whole(topk_ids, (T, kr), "topk_ids")
-    _whole(topk_weights, (T, kr), "topk_weights")
-    b = None
+        topk_weights = torch.empty(out, dtype=_F32, device=logits.device)
+    elif topk_weights.dtype != _F32 or topk_weights.shape != out or not topk_weights.is_contiguous():
+        _refuse(topk_weights, _F32, out, "topk_weights")
     if bias is not None:
-        _whole(bias, (E,), "bias")
-        b = _dptr(bias, torch.float32, "bias")
+        if bias.dtype != _F32 or bias.shape != (E,) or not bias.is_contiguous() or not bias.is_cuda:
+            _refuse(bias, _F32, (E,), "bias")
+        bias = bias.data_ptr()
+    if stream is not None:                     # used there, whatever stream they were made on
+        _used_on(stream, topk_ids, topk_weights)
+    if not (logits.is_cuda and topk_ids.is_cuda and topk_weights.is_cuda):
+        raise ValueError("logits, topk_ids, topk_weights: a host tensor where each must be a CUDA tensor")
     status = _lib.load().bsf_gate(
-        _dptr(logits, logits.dtype, "logits"), kind, T, E, ld, b, groups,
-        groups if kept_groups is None else kept_groups, kr,
+        logits.data_ptr(), kind, T, E, ld, bias, groups, groups if kept_groups is None else kept_groups, kr,
         _SCORES[score] | _GROUP_SCORES[group_score] | (GATE_RENORMALISE if renormalise else 0), scale,
-        _dptr(topk_ids, torch.int32, "topk_ids"), _dptr(topk_weights, torch.float32, "topk_weights"),
-        _raw_stream(stream, logits))
+        topk_ids.data_ptr(), topk_weights.data_ptr(),
+        _current_stream(logits.get_device()) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "gate")
     return topk_ids, topk_weights
@@ -510,29 +517,38 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
     """y bf16 [T, 2 K] (gate columns, then up columns; any row stride that is a multiple of 8) ->
     (q uint8 [T, Kp], sf int32 [ceil(Kp/512), >= T]) of silu(gate) * up, Kp = K rounded up to 128.
     ``rows`` as in ``quantise_act``: only the routed rows of a packed operand."""
-    ld = _row_stride(y, "y")
-    T, K = y.shape
+    T, K = _two_dims(y, "y")
+    ld = _row_stride(y, T, K, "y")
     if K % 2:
         raise ValueError(f"y: expected an even number of columns, got {K}")
+    if y.dtype != _BF16:
+        _refuse(y, _BF16, None, "y")
     K //= 2
     Kp = (K + 127) // 128 * 128
+    words = (Kp + 511) // 512
     if q is None:
-        q = torch.empty((T, Kp), dtype=torch.uint8, device=y.device)
+        q = torch.empty((T, Kp), dtype=_U8, device=y.device)
+    elif q.dtype != _U8 or q.shape != (T, Kp) or not q.is_contiguous():
+        _refuse(q, _U8, (T, Kp), "q")
     if sf is None:
-        sf = torch.empty((sf_words(Kp), sf_ld(T)), dtype=torch.int32, device=y.device)
-    _whole(q, (T, Kp), "q")
+        sf = torch.empty((words, sf_ld(T)), dtype=_I32, device=y.device)
     ld_sf = sf.shape[-1]
-    _whole(sf, (sf_words(Kp), ld_sf), "sf")
+    if sf.dtype != _I32 or sf.shape != (words, ld_sf) or not sf.is_contiguous():
+        _refuse(sf, _I32, (words, ld_sf), "sf")
     token_of_row = rows_used = None
     if rows is not None:
         token_of_row, rows_used = rows
-        if token_of_row.numel() < T or rows_used.numel() < 1 or not token_of_row.is_contiguous():
-            raise ValueError("rows: expected token_of_row of at least T entries and rows_used of one")
-        token_of_row = _dptr(token_of_row, torch.int32, "token_of_row")
-        rows_used = _dptr(rows_used, torch.int32, "rows_used")
+        if (token_of_row.dtype != _I32 or rows_used.dtype != _I32 or token_of_row.numel() < T or rows_used.numel() < 1
+                or not token_of_row.is_cuda or not rows_used.is_cuda or not token_of_row.is_contiguous()):
+            raise ValueError("rows: expected CUDA int32 tensors, token_of_row of at least T entries and rows_used of one")
+        token_of_row, rows_used = token_of_row.data_ptr(), rows_used.data_ptr()
+    if stream is not None:
+        _used_on(stream, q, sf)
+    if not (y.is_cuda and q.is_cuda and sf.is_cuda):
+        raise ValueError("y, q, sf: a host tensor where each must be a CUDA tensor")
     status = _lib.load().bsf_swiglu_quantise(
-        _dptr(y, torch.bfloat16, "y"), T, K, ld, token_of_row, rows_used, _dptr(q, torch.uint8, "q"),
-        _dptr(sf, torch.int32, "sf"), ld_sf, _raw_stream(stream, y))
+        y.data_ptr(), T, K, ld, token_of_row, rows_used, q.data_ptr(), sf.data_ptr(), ld_sf,
+        _current_stream(y.get_device()) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "swiglu_quantise")
     return q, sf
@@ -551,30 +567,38 @@ def prepare_dense_weight(w):
 def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, stream=None):
     """a uint8 [M, K] with scales sfa, b uint8 [Np, K] with scales sfb (``prepare_dense_weight``) ->
     d bf16 [M, N], N <= Np < N + 128 (default Np); ``addend`` bf16 [M, N] is added before the rounding."""
-    M, K = a.shape
+    M, K = _two_dims(a, "a")
     Np = b.shape[0]
     N = Np if N is None else N
     if (N + 127) // 128 * 128 != Np:
         raise ValueError(f"b: expected {(N + 127) // 128 * 128} rows for N = {N}, got {Np}")
-    words, ld_sf = sf_words(K), sfa.shape[-1]
-    _whole(a, (M, K), "a")
-    _whole(b, (Np, K), "b")
-    _whole(sfa, (words, ld_sf), "sfa")
-    _whole(sfb, (words, Np), "sfb")
+    words, ld_sf = (K + 511) // 512, sfa.shape[-1]
+    if a.dtype != _U8 or not a.is_contiguous():
+        _refuse(a, _U8, (M, K), "a")
+    if b.dtype != _U8 or b.shape != (Np, K) or not b.is_contiguous():
+        _refuse(b, _U8, (Np, K), "b")
+    if sfa.dtype != _I32 or sfa.shape != (words, ld_sf) or not sfa.is_contiguous():
+        _refuse(sfa, _I32, (words, ld_sf), "sfa")
+    if sfb.dtype != _I32 or sfb.shape != (words, Np) or not sfb.is_contiguous():
+        _refuse(sfb, _I32, (words, Np), "sfb")
+    out = (M, N)
     if d is None:
-        d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
-    elif d.shape != (M, N):
-        raise ValueError(f"d: expected shape {(M, N)}, got {tuple(d.shape)}")
-    ldd = _row_stride(d, "d")
+        d = torch.empty(out, dtype=_BF16, device=a.device)
+    elif d.dtype != _BF16 or d.shape != out:
+        _refuse(d, _BF16, out, "d")
+    ldd = _row_stride(d, M, N, "d")
     ldc, c = 0, None
     if addend is not None:
-        if addend.shape != (M, N):
-            raise ValueError(f"addend: expected shape {(M, N)}, got {tuple(addend.shape)}")
-        ldc, c = _row_stride(addend, "addend"), _dptr(addend, torch.bfloat16, "addend")
+        if addend.dtype != _BF16 or addend.shape != out or not addend.is_cuda:
+            _refuse(addend, _BF16, out, "addend")
+        ldc, c = _row_stride(addend, M, N, "addend"), addend.data_ptr()
+    if stream is not None:
+        _used_on(stream, d)
+    if not (a.is_cuda and sfa.is_cuda and b.is_cuda and sfb.is_cuda and d.is_cuda):
+        raise ValueError("a, sfa, b, sfb, d: a host tensor where each must be a CUDA tensor")
     status = _lib.load().bsf_dense_gemm(
-        _dptr(a, torch.uint8, "a"), _dptr(sfa, torch.int32, "sfa"), ld_sf, M, _dptr(b, torch.uint8, "b"),
-        _dptr(sfb, torch.int32, "sfb"), N, K, c, ldc, _dptr(d, torch.bfloat16, "d"), ldd, flags,
-        _raw_stream(stream, a))
+        a.data_ptr(), sfa.data_ptr(), ld_sf, M, b.data_ptr(), sfb.data_ptr(), N, K, c, ldc, d.data_ptr(), ldd, flags,
+        _current_stream(a.get_device()) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "dense_gemm")
     return d
