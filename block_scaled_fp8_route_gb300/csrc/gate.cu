@@ -26,6 +26,9 @@ constexpr int kGateMaxGroups = 32;
 constexpr int kGateMaxKr = 32;
 constexpr int kGateWarps = 4;           // warps per CTA
 constexpr unsigned kAll = 0xffffffffu;
+// CTAs per SM: the more warps the better until the registers run out (65533 x 192: 34.7 us with 10 CTAs of
+// 48 registers, 40.9 with the 7 that 70 leave; 8192 x 256: 9.8 us with 8, 10.5 with 10, which spill).
+constexpr int gate_ctas(int vpl) { return vpl <= 3 ? 12 : vpl <= 6 ? 10 : vpl <= 8 ? 8 : vpl <= 16 ? 4 : 2; }
 
 struct GateArgs {
   const void* logits;
@@ -57,13 +60,22 @@ __device__ __forceinline__ float reciprocal(float x) {
 }
 __device__ __forceinline__ float sigmoid(float l) { return reciprocal(1.f + expf(-l)); }
 
-// The VPL logits of this lane: -inf where there is no usable expert (past E, -inf, NaN), +inf as the
-// largest finite float.
+// 2**x to 2 units in the last place (0 below 2**-126).  The scores that only decide the choice, and the
+// softmax's sum, are built on it: the argument l * log2(e) is off by 2**-24 of itself, so a score is
+// within 2**-21 of its size, as with expf, in 3 or 4 instructions instead of 10.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The VPL logits of this lane (-inf past E); `lane_row` is the row's base plus this lane's first expert.
 template <int VPL, bool BF16>
-__device__ __forceinline__ void load_row(const GateArgs& p, int64_t t, int lane, float (&l)[VPL]) {
+__device__ __forceinline__ void load_row(const GateArgs& p, const char* lane_row, int lane, float (&l)[VPL]) {
   const int e0 = lane * VPL;
   if (BF16) {
-    const uint16_t* row = static_cast<const uint16_t*>(p.logits) + t * p.ld + e0;
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(lane_row);
     constexpr int W = VPL % 8 == 0 ? 8 : VPL % 4 == 0 ? 4 : VPL % 2 == 0 ? 2 : 1;   // values per load
     if (W > 1 && p.wide) {
 #pragma unroll
@@ -88,7 +100,7 @@ __device__ __forceinline__ void load_row(const GateArgs& p, int64_t t, int lane,
         l[i] = e0 + i < p.E ? __uint_as_float(static_cast<uint32_t>(__ldg(row + i)) << 16) : -INFINITY;
     }
   } else {
-    const float* row = static_cast<const float*>(p.logits) + t * p.ld + e0;
+    const float* row = reinterpret_cast<const float*>(lane_row);
     constexpr int W = VPL % 4 == 0 ? 4 : VPL % 2 == 0 ? 2 : 1;
     if (W > 1 && p.wide) {
 #pragma unroll
@@ -108,11 +120,11 @@ __device__ __forceinline__ void load_row(const GateArgs& p, int64_t t, int lane,
   }
 }
 
-// Order-preserving unsigned image of a float that is not NaN; 0 for -inf.
+// Order-preserving unsigned image of a float that is not NaN (-0 as +0); below kFirstFinite for -inf.
+constexpr uint32_t kFirstFinite = 0x00800000u;
 __device__ __forceinline__ uint32_t order_bits(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);                     // (-0 as +0)
-  const uint32_t u = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-  return v > -INFINITY ? u : 0u;
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
 // c[0] >= c[1] >= ... by Batcher's odd-even merge network (pruned to N; the comparators of an index past N
@@ -139,7 +151,10 @@ __device__ __forceinline__ void sort_down(uint32_t (&c)[N]) {
 }
 
 // What bounds it: a row is 4 E bytes, but choosing takes a fixed chain of warp operations, so short
-// batches are bound by that chain's latency and long ones by issue slots.
+// batches are bound by that chain's latency (one token 2.9 us with its launch) and long ones by issue
+// slots: about 490 per token of 192 experts in 8 groups (65533 tokens in 34.7 us, 1.5 TB/s, 23 % of the
+// copy rate), of which the rounds of the choice and the weights are half whatever E is.  Four lanes per
+// token with sorted lists in registers, and one thread per token, took as many slots and twice the latency.
 // * A key and its expert share one word: the key's leading bits, then the complement of the expert, so
 //   that the words are distinct, a tie goes to the lowest expert, and a maximum names its owner.  Lanes
 //   sort their words once (VPL <= 8; two instructions per comparator), and a round of the choice is one
@@ -149,7 +164,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&c)[N]) {
 // * Scores are computed only where they decide: with no bias the choice goes by the logits, and only the
 //   kr chosen get an exp (plus the sum of a softmax that is not renormalised).
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p) {
+__global__ void __launch_bounds__(32 * kGateWarps, gate_ctas(VPL)) gate_kernel(const GateArgs p) {
   pdl_launch_dependents();
   pdl_wait();                                       // (launched as a dependent: nothing is read before)
   __shared__ float s_val[kGateWarps][VPL * 32];
@@ -159,20 +174,25 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
   const bool renorm = p.flags & BSF_GATE_RENORMALISE, biased = p.bias != nullptr;
   const bool need_max = !sig && (biased || !renorm || (top2 && p.G > 1));
   const bool need_sum = !sig && (biased || !renorm);
-  float bias[VPL];
+  const int groups = p.G, kr = p.kr;
+  float bias[VPL];                                  // (NaN as -inf: such an expert is never chosen)
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) bias[i] = biased && lane * VPL + i < E ? __ldg(p.bias + lane * VPL + i) : 0.f;
+  for (int i = 0; i < VPL; ++i)
+    bias[i] = biased && lane * VPL + i < E ? fmaxf(__ldg(p.bias + lane * VPL + i), -INFINITY) : 0.f;
 
+  constexpr int kSize = BF16 ? 2 : 4;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGateWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
   if (t >= p.T) return;
+  const char* row = static_cast<const char*>(p.logits) + t * p.ld * kSize;
+  const int64_t row_step = step * p.ld * kSize;
   float next[VPL];
-  load_row<VPL, BF16>(p, t, lane, next);
-  for (; t < p.T; t += step) {
-    float key[VPL];
+  load_row<VPL, BF16>(p, row + lane * VPL * kSize, lane, next);
+  for (; t < p.T; t += step, row += row_step) {
+    float key[VPL];                                 // -inf: not usable (-inf, NaN); +inf as the largest finite float
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = next[i] > -INFINITY ? fminf(next[i], FLT_MAX) : -INFINITY;
-    if (t + step < p.T) load_row<VPL, BF16>(p, t + step, lane, next);
+    for (int i = 0; i < VPL; ++i) key[i] = fminf(fmaxf(next[i], -INFINITY), FLT_MAX);
+    if (t + step < p.T) load_row<VPL, BF16>(p, row + row_step + lane * VPL * kSize, lane, next);
 
     float m = 0.f, inv = 1.f;
     if (need_max) {
@@ -181,56 +201,66 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
       for (int i = 1; i < VPL; ++i) m = fmaxf(m, key[i]);
       m = fmaxf(warp_max(m), -FLT_MAX);            // (finite also where nothing is usable)
     }
+    auto exp_rel = [&](float k) { return exp2_approx((k - m) * kLog2e); };
     if (need_sum) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += expf(key[i] - m);          // exp(-inf) = 0
+      for (int i = 0; i < VPL; ++i) sum += exp_rel(key[i]);            // exp(-inf) = 0
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
       inv = sum > 0.f ? reciprocal(sum) : 0.f;        // (the largest term is 1)
     }
+    auto score = [&](float k) { return sig ? reciprocal(1.f + exp2_approx(-kLog2e * k)) : exp_rel(k); };
     if (biased) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float v = (sig ? sigmoid(key[i]) : expf(key[i] - m) * inv) + bias[i];
-        key[i] = key[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;
+        const float v = fmaf(score(key[i]), inv, bias[i]);
+        key[i] = key[i] > -INFINITY ? v : -INFINITY;
       }
     }
     // what a group's two largest keys count for in its score (scores rise with the logits)
-    auto counts = [&](float k) { return biased || !top2 ? k : sig ? sigmoid(k) : expf(k - m); };
+    auto counts = [&](float k) { return biased || !top2 ? k : score(k); };
 
     bool open = true;                               // this lane's experts take part
-    if (p.G > 1 && p.lane_groups) {
+    if (groups > 1 && p.lane_groups) {
       const int mine = lane >> p.group_shift;
-      float a = key[0], b = -INFINITY;
+      float gs = key[0];
+      if (top2) {
+        float a = key[0], b = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < VPL; ++i) {
-        b = fmaxf(b, fminf(a, key[i]));
-        a = fmaxf(a, key[i]);
+        for (int i = 1; i < VPL; ++i) {
+          b = fmaxf(b, fminf(a, key[i]));
+          a = fmaxf(a, key[i]);
+        }
+        for (int o = 1; o < 1 << p.group_shift; o <<= 1) {
+          const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+          b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+          a = fmaxf(a, a2);
+        }
+        gs = a > -INFINITY ? counts(a) + (b > -INFINITY ? counts(b) : 0.f) : -INFINITY;
+      } else {
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) gs = fmaxf(gs, key[i]);
+        for (int o = 1; o < 1 << p.group_shift; o <<= 1) gs = fmaxf(gs, __shfl_xor_sync(kAll, gs, o));
       }
-      for (int o = 1; o < 1 << p.group_shift; o <<= 1) {
-        const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
-        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
-        a = fmaxf(a, a2);
-      }
-      float gs = -INFINITY;
-      if (a > -INFINITY) gs = counts(a) + (top2 && b > -INFINITY ? counts(b) : 0.f);
       open = false;
       for (int r = 0; r < p.kept; ++r) {
-        const float v = open ? -INFINITY : gs;
-        const float best = warp_max(v);
+        const float best = warp_max(gs);
         if (best == -INFINITY) break;
-        open |= mine == (__ffs(__ballot_sync(kAll, v == best)) - 1) >> p.group_shift;
+        if (mine == (__ffs(__ballot_sync(kAll, gs == best)) - 1) >> p.group_shift) {
+          open = true;
+          gs = -INFINITY;
+        }
       }
-    } else if (p.G > 1) {
+    } else if (groups > 1) {
       // groups that end inside a lane: lane g reduces group g from shared memory
       float* val = s_val[warp];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) val[lane * VPL + i] = key[i];
       __syncwarp();
-      const int per = E / p.G;
+      const int per = E / groups;
       float gs = -INFINITY;
-      if (lane < p.G) {
+      if (lane < groups) {
         float a = -INFINITY, b = -INFINITY;
         for (int i = 0; i < per; ++i) {
           const float v = val[lane * per + i];
@@ -255,30 +285,30 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
       }
     }
 
-    if (!open) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
-    }
     constexpr int kIdBits = VPL == 1 ? 5 : VPL == 2 ? 6 : VPL <= 4 ? 7 : VPL <= 8 ? 8 : VPL <= 16 ? 9 : 10;
     constexpr uint32_t kIdMask = (1u << kIdBits) - 1u;
     uint32_t c[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const uint32_t u = order_bits(key[i]);
-      c[i] = u ? (u & ~kIdMask) | (kIdMask - static_cast<uint32_t>(lane * VPL + i)) : 0u;
+    for (int i = 0; i < VPL; ++i)
+      c[i] = (order_bits(key[i]) & ~kIdMask) | (kIdMask - static_cast<uint32_t>(lane * VPL + i));
+    if constexpr (VPL <= 8) {
+      sort_down(c);
+      if (!open) c[0] = 0u;                         // a lane that never gives
+    } else if (!open) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = 0u;
     }
-    if constexpr (VPL <= 8) sort_down(c);
     // round r's word ends up in lane r; one round more shows whether the last choice was clear
-    uint32_t mine = 0u, after = 0u;
-    for (int r = 0; r <= p.kr; ++r) {
+    uint32_t mine = 0u, best = 0u;
+    for (int r = 0; r <= kr; ++r) {
       uint32_t head = c[0];
       if constexpr (VPL > 8) {
 #pragma unroll
         for (int i = 1; i < VPL; ++i) head = max(head, c[i]);
       }
-      const uint32_t best = __reduce_max_sync(kAll, head);
-      if (r < p.kr) mine = lane == r ? best : mine; else after = best;
-      if (best == 0u) break;
+      best = __reduce_max_sync(kAll, head);
+      if (best < kFirstFinite) break;
+      if (lane == r) mine = best;
       if constexpr (VPL <= 8) {
         if (c[0] == best) {
 #pragma unroll
@@ -290,23 +320,27 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
         for (int i = 0; i < VPL; ++i) c[i] = c[i] == best ? 0u : c[i];
       }
     }
-    int my_id = mine ? static_cast<int>(kIdMask - (mine & kIdMask)) : -1;
+    int my_id = mine && lane < kr ? static_cast<int>(kIdMask - (mine & kIdMask)) : -1;
     if (!BF16 || biased) {
       uint32_t next_word = __shfl_down_sync(kAll, mine, 1);
-      if (lane == p.kr - 1) next_word = after;
-      const bool unclear = lane < p.kr && next_word != 0u && ((mine ^ next_word) >> kIdBits) == 0u;
+      if (lane == kr - 1) next_word = best;
+      const bool unclear = my_id >= 0 && next_word >= kFirstFinite && ((mine ^ next_word) >> kIdBits) == 0u;
       if (__any_sync(kAll, unclear)) {
         my_id = -1;
-        for (int r = 0; r < p.kr; ++r) {
+        if (!open) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) key[i] = -INFINITY;
+        }
+        for (int r = 0; r < kr; ++r) {
           float head = key[0];
 #pragma unroll
           for (int i = 1; i < VPL; ++i) head = fmaxf(head, key[i]);
-          const float best = warp_max(head);
-          if (best == -INFINITY) break;
-          const int from = __ffs(__ballot_sync(kAll, head == best)) - 1;
+          const float most = warp_max(head);
+          if (most == -INFINITY) break;
+          const int from = __ffs(__ballot_sync(kAll, head == most)) - 1;
           int at = 0;
 #pragma unroll
-          for (int i = VPL - 1; i >= 0; --i) at = key[i] == best ? i : at;
+          for (int i = VPL - 1; i >= 0; --i) at = key[i] == most ? i : at;
           const int e = __shfl_sync(kAll, lane * VPL + at, from);
           if (lane == r) my_id = e;
 #pragma unroll
@@ -319,11 +353,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
     // lane r: the score of choice r, from its logit (still in a cache)
     float l = -INFINITY;
     if (my_id >= 0) {
+      const char* at = row + my_id * kSize;
       if (BF16)
-        l = __uint_as_float(
-            static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + my_id)) << 16);
+        l = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(at))) << 16);
       else
-        l = __ldg(static_cast<const float*>(p.logits) + t * p.ld + my_id);
+        l = __ldg(reinterpret_cast<const float*>(at));
       l = fminf(l, FLT_MAX);
     }
     if (!sig && !need_max) m = __shfl_sync(kAll, l, 0);              // the largest logit is the first choice
@@ -334,9 +368,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs p)
       for (int o = p.kr_lanes >> 1; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
       w = total > 0.f ? __fdiv_rn(w, total) : 0.f;
     }
-    if (lane < p.kr) {
-      p.ids[t * p.kr + lane] = my_id;
-      p.weights[t * p.kr + lane] = w * p.scale;
+    if (lane < kr) {
+      p.ids[t * kr + lane] = my_id;
+      p.weights[t * kr + lane] = w * p.scale;
     }
   }
 }
@@ -349,7 +383,7 @@ bsf_status launch_gate(GateArgs a, bool bf16, cudaStream_t s) {
   a.lane_groups = a.E == 32 * VPL && 32 % a.G == 0;
   while ((a.G << (a.group_shift + 1)) <= 32) ++a.group_shift;
   // one row per warp until every SM has its warps, then each warp goes on with the next row in flight
-  const int64_t most = static_cast<int64_t>(sm_count()) * (VPL <= 4 ? 12 : VPL <= 8 ? 8 : 4);
+  const int64_t most = static_cast<int64_t>(sm_count()) * gate_ctas(VPL);
   const int64_t need = (a.T + kGateWarps - 1) / kGateWarps;
   const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
   return launch_dependent(bf16 ? gate_kernel<VPL, true> : gate_kernel<VPL, false>, blocks, 32 * kGateWarps, 0, s, a);
