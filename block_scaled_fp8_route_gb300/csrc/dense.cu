@@ -55,7 +55,7 @@ struct DenseArgs {
   int split, stages;
   int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between their accumulators
   uint32_t tmem_cols;
-  int tiled;
+  int tiled, withhold;       // withhold: BSF_DEBUG_WITHHOLD_LOADS
   int vec4;                  // four neighbouring columns of D (and C) are 8-byte aligned
   int* err;
 };
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1 && !p.withhold; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) break;
         uint8_t* dst = smem + stage * stage_bytes;
         mbar_arrive_expect_tx(&full[stage], stage_bytes);
@@ -396,7 +396,7 @@ struct PairArgs {
   int tiles_m, tiles_n;      // token tiles, weight tiles
   int tok;                   // tokens of a tile: a multiple of 32, at most kPairMaxTok
   int stages;
-  int tiled, vec8;
+  int tiled, vec8, withhold;
   int* err;
 };
 
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const bool weights = warp == 0;
       uint32_t stage = 0, phase = 0;
       int issued = 0;
-      bool ok = true;
+      bool ok = !p.withhold;
       for (int t = pair; t < total && ok; t += npairs) {
         const int tm = t % p.tiles_m, tn = t / p.tiles_m;
         const int row = tm * p.tok + static_cast<int>(rank) * half_tok;
@@ -929,7 +929,7 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
                                      const uint8_t* b, const int32_t* sfb, int64_t N, int64_t K, const void* addend,
                                      int64_t ldc, void* d, int64_t ldd, int flags, bsf_stream_t stream) {
   if (M < 0 || N <= 0 || K <= 0 || K % 128) return BSF_ERR_INVALID_ARGUMENT;
-  if (flags & ~BSF_B_TILED) return BSF_ERR_INVALID_ARGUMENT;
+  if (flags & ~(BSF_B_TILED | BSF_DEBUG_WITHHOLD_LOADS)) return BSF_ERR_INVALID_ARGUMENT;
   if (M == 0) return BSF_OK;
   if (!a || !sfa || !b || !sfb || !d) return BSF_ERR_INVALID_ARGUMENT;
   if (sfa_ld < M || sfa_ld % 4 || ldd < N || (addend && ldc < N)) return BSF_ERR_INVALID_ARGUMENT;
@@ -942,7 +942,7 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   if ((ntn + 2) * kTileW * nkb > INT32_MAX || M > kMaxRows - 256) return BSF_ERR_UNSUPPORTED;
   int* err = device_error_ptr();
   if (!err) return BSF_ERR_CUDA;
-  const bool tiled = (flags & BSF_B_TILED) != 0;
+  const bool tiled = (flags & BSF_B_TILED) != 0, withhold = (flags & BSF_DEBUG_WITHHOLD_LOADS) != 0;
   const int64_t Np = ntn * kTileW;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const DeviceLimits* limits;
@@ -972,6 +972,7 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
     p.tiles_n = static_cast<int>(tiles_n);
     p.tok = tok;
     p.tiled = tiled;
+    p.withhold = withhold;
     p.vec8 = aligned16(d) && ldd % 8 == 0 && (!addend || (aligned16(addend) && ldc % 8 == 0));
     const int stage_bytes = 2 * (kTileW + tok / 2) * kTileK;
     p.stages = (kSmemBytes - 1024 - kPairBarBytes - 16 * kBoxBytes) / stage_bytes;
@@ -1020,6 +1021,7 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
   const int cols = kAccCol + p.issuers * p.acc_stride;
   p.tmem_cols = cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
   p.tiled = tiled;
+  p.withhold = withhold;
   p.vec4 = (reinterpret_cast<uintptr_t>(d) & 7) == 0 && ldd % 4 == 0 &&
            (!addend || ((reinterpret_cast<uintptr_t>(addend) & 7) == 0 && ldc % 4 == 0));
   p.err = err;

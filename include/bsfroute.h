@@ -283,7 +283,8 @@ bsf_status bsf_dispatch(const void* x, int64_t T, int64_t K, const int32_t* topk
  * (bsf_grouped_gemm_masked with max_m <= 64, or with expected_m <= 32 and
  * device-resident weights) is launched as a programmatic dependent
  * of the preceding kernel on the stream: its CTAs may be scheduled while that
- * kernel drains, and they touch no global memory until it has completed.
+ * kernel drains, and they touch no global memory until it has completed.  So
+ * are gate, swiglu_quantise and dense_gemm.
  *
  * Tensor memory: every GEMM CTA allocates its tensor-memory columns on entry
  * (tcgen05.alloc), which waits, with no time limit, until an SM has that many
@@ -546,7 +547,9 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
  *                 or -inf is not usable for that token; +inf counts as the
  *                 largest finite float32.
  *   score         s_e = 1 / (1 + exp(-l_e)), or exp(l_e - m) / sum exp(l_j - m)
- *                 over the usable experts, in float32.
+ *                 over the usable experts, in float32: within 2^-20 of these
+ *                 values where they decide a choice, within a few units in
+ *                 the last place (plus that of a rounded l - m) in the weights.
  *   bias          fp32 [E] or NULL.  With a bias the choice goes by s_e + b_e
  *                 (an expert for which that is NaN or -inf is never chosen);
  *                 without one by the logit itself.
@@ -604,8 +607,10 @@ bsf_status bsf_swiglu_quantise(const void* y, int64_t T, int64_t K, int64_t ld, 
  * FP32 accumulation on the tensor cores, a fixed order of sums (bit-identical
  * from run to run), round-to-nearest-even to bf16.  K % 128 == 0; 16-byte
  * aligned a, b, sfa, sfb; d and addend need only their element alignment (8
- * bytes and row strides of 4 elements are faster).  flags: BSF_B_TILED.
- * M == 0 is a no-op.  A wait that runs out sets BSF_DEVERR_TIMEOUT.
+ * bytes and row strides of 4 elements are faster, from 256 tokens on 16 bytes
+ * and 8 elements).  flags: BSF_B_TILED, and BSF_DEBUG_WITHHOLD_LOADS as for the
+ * grouped products.  M == 0 is a no-op.  A wait that runs out sets
+ * BSF_DEVERR_TIMEOUT.
  */
 bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, int64_t M, const uint8_t* b,
                           const int32_t* sfb, int64_t N, int64_t K, const void* addend, int64_t ldc, void* d,

@@ -181,3 +181,20 @@ def test_offsets_past_32_bits(dev):
     big = torch.empty(2100 << 20, dtype=torch.bfloat16, device=dev).view(2100, 1 << 20)
     d = ops.dense_gemm(p.a, p.sfa, p.b, p.sfb, 128, d=big[:, :128])
     assert torch.equal(d, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 256, 2048), (300, 512, 256), (2048, 1536, 512)])
+def test_withheld_loads_time_out_and_context_survives(dev, M, N, K):
+    """The loads never come: every wait of either kernel runs out, the error word says so, nothing is stored,
+    and the next product is right."""
+    p = Problem(M, N, K, dev, seed=21)
+    want = p.run()
+    torch.cuda.synchronize()
+    assert ops.device_error() == 0
+    d = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=dev)
+    p.run(d=d, flags=ops.B_TILED | 0x100)
+    torch.cuda.synchronize()
+    assert ops.device_error() & ops.DEVERR_TIMEOUT
+    assert (d == 7.0).all()
+    assert torch.equal(p.run(), want)
+    assert ops.device_error() == 0
