@@ -376,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------- CTA pairs: 256 x up to 224 output tiles
 constexpr int kPairW = 256;                                // weight rows of a tile (MMA M), 128 per CTA
 constexpr int kPairMaxTok = 224;                           // tokens of a tile (MMA N), half staged by each CTA
+constexpr int kTwoIssuerTok = 128;                         // up to here a pair has two issuing warps
 constexpr int kPairMaxStages = 4;                          // a stage is 256 K of both operands
-// warps: 0 weight loads, 1 MMA issuer, 2-5 scales, 6-13 epilogue, 14 waiter, 15 token loads
-constexpr int kPairThreads = 32 * 16;
-constexpr int kPairWaiter = 14, kPairTokLoads = 15;
+// warps: 0 weight loads, 1 MMA issuer, 2-5 scales, 6-13 epilogue, 14 waiter, 15 token loads, 16 second issuer
+constexpr int kPairWaiter = 14, kPairTokLoads = 15, kPairIssuer2 = 16;
 constexpr int kBoxBytes = 32 * 64;                         // 32 tokens x 32 bf16 columns of D
 constexpr int kPairBarBytes = 512;
 
@@ -395,6 +395,7 @@ struct PairArgs {
   int M, N, nkb, nw;
   int tiles_m, tiles_n;      // token tiles, weight tiles
   int tok;                   // tokens of a tile: a multiple of 32, at most kPairMaxTok
+  int accs;                  // sets of accumulators, one accumulator for each issuer in a set
   int stages;
   int tiled, vec8, withhold;
   int* err;
@@ -479,7 +480,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-__global__ void __launch_bounds__(kPairThreads, 1)
+// kIssuers: MMA-issuing warps, 1 or 2
+template <int kIssuers>
+__global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ CUtensorMap tmap_a,
                       const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_c,
                       const PairArgs p) {
@@ -513,14 +516,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int s = 0; s < kSfSlots; ++s) {
       mbar_init(&sf_full[s], 8);
-      mbar_init(&sf_empty[s], 1);
+      mbar_init(&sf_empty[s], kIssuers);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&acc_full[s], 1);
+    for (int s = 0; s < p.accs; ++s) {
+      mbar_init(&acc_full[s], kIssuers);
       mbar_init(&acc_empty[s], 16);
     }
     for (int s = 0; s < 16; ++s) mbar_init(&add_full[s], 1);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, kIssuers);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_b);
@@ -538,7 +541,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();                           // barriers of both CTAs are initialised
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t tmem_sf = tmem_base + 2 * p.tok;            // behind the two accumulators
+  const uint32_t acc_cols = kIssuers * p.tok;               // of a set of accumulators
+  const uint32_t tmem_sf = tmem_base + p.accs * acc_cols;
 
   if (warp == 0 || warp == kPairTokLoads) {
     // ------------------------------------------------------------ TMA producers (each CTA loads its halves)
@@ -586,67 +590,87 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (rank 0)
-    // The issuing thread reads no shared memory between stages: the waiter warp does every wait and hands
-    // each stage over through a named barrier whose OR-reduced predicate carries an abort.
+  } else if (warp == 1 || warp >= kPairIssuer2) {
+    // ------------------------------------------------------------ MMA issuers (rank 0)
+    // An issuing thread reads no shared memory between stages: the waiter warp does every wait and hands
+    // each stage over through a named barrier whose OR-reduced predicate carries an abort.  An MMA costs its
+    // issuing thread about 86 cycles whatever its N, so tiles of up to 128 tokens (64 cycles of tensor work)
+    // have two issuers that take a tile's stages in turn, each into an accumulator of its own: in tiles of
+    // 128 tokens 512 x 4096 x 7168 takes 18.7 us with two and 20.7 with one, 512 x 256 x 7168 14.4 and 19.1.
+    // Wider tiles are slower with two (their accumulators leave no second set, and the tensor cores are the
+    // limit): 2500 x 4096 x 7168 takes 53.5 us in tiles of 192 with one, 57.5 with two.
+    const int me = warp == 1 ? 0 : 1;
     if (rank == 0) {
       const uint32_t lead = lane == 0;
-      uint32_t stage = 0, slot = 0, acc = 0;
+      uint32_t stage = 0, slot = 0, acc = 0;           // stage: of the tile's next K-block pair, whoever takes it
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
-        const uint32_t d_tmem = tmem_base + acc * p.tok;
+        const uint32_t d_tmem = tmem_base + acc * acc_cols + me * p.tok;
+        uint32_t first = 1;
         for (int kb = 0; kb < p.nkb; kb += 2) {
-          if (named_barrier_or(1, 64, false)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sf = tmem_sf + slot * kSfCols;
-          const uint8_t* src = smem + stage * stage_bytes;
-          uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
-          uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + 2 * kTileW * kTileK));
-          uint32_t idesc = idesc_mxf8_e4m3(kPairW, p.tok, kb & 3, kb & 3);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, (kb | k) != 0, lead);
-          if (kb + 1 < p.nkb) {
-            adesc += kTileW * kTileK >> 4;
-            bdesc += tok_bytes >> 4;
-            idesc = idesc_mxf8_e4m3(kPairW, p.tok, (kb + 1) & 3, (kb + 1) & 3);
+          if (kIssuers == 1 || ((kb >> 1) & 1) == me) {
+            if (named_barrier_or(1 + me, 64, false)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sf = tmem_sf + slot * kSfCols;
+            const uint8_t* src = smem + stage * stage_bytes;
+            uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
+            uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + 2 * kTileW * kTileK));
+            uint32_t idesc = idesc_mxf8_e4m3(kPairW, p.tok, kb & 3, kb & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, 1, lead);
+              pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, k == 0 ? first ^ 1u : 1u, lead);
+            first = 0;
+            if (kb + 1 < p.nkb) {
+              adesc += kTileW * kTileK >> 4;
+              bdesc += tok_bytes >> 4;
+              idesc = idesc_mxf8_e4m3(kPairW, p.tok, (kb + 1) & 3, (kb + 1) & 3);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                pair_mma(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, sf, sf + 4, 1, lead);
+            }
+            pair_commit(&empty[stage], lead);
           }
-          pair_commit(&empty[stage], lead);
           if (++stage == static_cast<uint32_t>(p.stages)) stage = 0;
           if ((kb & 2) || kb + 2 >= p.nkb) {
-            pair_commit(&sf_empty[slot], lead);
+            pair_commit(&sf_empty[slot], lead);          // (from every issuer, also one that had no stage of it)
             if (++slot == kSfSlots) slot = 0;
           }
         }
         if (!ok) break;
         pair_commit(&acc_full[acc], lead);
-        acc ^= 1u;
+        if (++acc == static_cast<uint32_t>(p.accs)) acc = 0;
       }
       pair_commit(mma_done, lead);
       if (lane == 0) wait_quiet(mma_done, 0);
     }
     __syncwarp();
   } else if (warp == kPairWaiter) {
-    // ------------------------------------------------------------ waiter (rank 0): the issuer's waits, in its order
+    // ------------------------------------------------------------ waiter (rank 0): the issuers' waits, in their order
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, slot = 0, sf_phase = 0, acc = 0, acc_phase = 0;
-      bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
-        bool good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
-        for (int kb = 0; kb < p.nkb; kb += 2) {
+      bool good = true;
+      int t = pair, kb = 0;
+      while (t < total) {
+        good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
+        for (kb = 0; kb < p.nkb; kb += 2) {
           if (good && (kb & 3) == 0) good = wait_cluster_all(&sf_full[slot], sf_phase, abort_flag, p.err);
           if (good) good = wait_all(&full[stage], phase, abort_flag, p.err);
-          if (named_barrier_or(1, 64, !good)) { ok = false; break; }
+          if (!good) break;
+          named_barrier_or(kIssuers == 1 ? 1 : 1 + ((kb >> 1) & 1), 64, false);
           if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
           if ((kb & 2) || kb + 2 >= p.nkb)
             if (++slot == kSfSlots) { slot = 0; sf_phase ^= 1u; }
         }
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
+        if (!good) break;
+        if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
+        t += npairs;
+      }
+      if (!good) {
+        // the issuer of this stage is at its barrier or on its way to it, and so is the other one if any later
+        // stage is its own (with two issuers every tile has stages of both)
+        const int me = kIssuers == 1 ? 0 : (kb >> 1) & 1;
+        named_barrier_or(1 + me, 64, true);
+        if (kIssuers == 2 && (kb + 2 < p.nkb || t + npairs < total)) named_barrier_or(2 - me, 64, true);
       }
     }
   } else if (warp < 6) {
@@ -736,11 +760,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * p.tok;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * acc_cols;
       for (int c = c_first; c < c_last; ++c) {
-        uint32_t r[32];
+        uint32_t r[32], r2[32];
         tmem_ld_x32(taddr + 32 * c, r);
+        if (kIssuers == 2) tmem_ld_x32(taddr + p.tok + 32 * c, r2);
         tmem_wait_ld_regs(r);
+        if (kIssuers == 2) {
+          tmem_wait_ld_regs(r2);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
+        }
         if (c == c_last - 1) {              // the accumulator's last columns are in registers
           tc_fence_before();
           __syncwarp();
@@ -794,8 +824,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
       }
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     // the issuer's last commit has reached this CTA's barriers too, so none arrives after it exits
@@ -854,8 +883,9 @@ bsf_status device_limits(const DeviceLimits** out) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BSF_ERR_CUDA;
   DeviceLimits& l = limits[dev];
   if (!l.ready.load(std::memory_order_acquire)) {      // (racing first calls store the same values)
-    const void* kernels[2] = {reinterpret_cast<const void*>(dense_split_kernel),
-                              reinterpret_cast<const void*>(dense_pair_kernel)};
+    const void* kernels[3] = {reinterpret_cast<const void*>(dense_split_kernel),
+                              reinterpret_cast<const void*>(dense_pair_kernel<1>),
+                              reinterpret_cast<const void*>(dense_pair_kernel<2>)};
     for (const void* k : kernels) {
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
@@ -879,10 +909,11 @@ bsf_status device_limits(const DeviceLimits** out) {
 }
 
 // Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to
-// 140 products (1 .. 5000 tokens; weights 256 x 7168, 512 x 4096, 1024 x 1024, 2112 x 7168, 4096 x 2048,
-// 4096 x 7168, 7168 x 2048, 8192 x 512) timed in every form on a GB300: the choice is within 0.5 % of the
-// best form on average, within 12 % at worst.  Both sides, 4096 x 7168: 256 tokens 14.6 us split against
-// 19.6 in pairs, 1024 tokens 38.7 against 33.4; 1024 x 1024 takes 1024 tokens in 6.4 us split, 7.5 in pairs.
+// products of 1 .. 2600 tokens with 14 weights' widths from 256 to 12288 and 9 inner lengths from 512 to 7168,
+// timed in every form that could be the fastest: 9186 with weights that may be in L2 and 4174 with weights
+// that come from HBM.  On both, the choice is within 0.9 % of the best form on average; the worst is 22 % (a
+// product of 70 x 12288 x 2048 in pairs).  Both sides, 4096 x 7168: 256 tokens 14.6 us split against 17.7 in
+// pairs, 1024 tokens 38.7 against 30.6; 1024 x 1024 takes 1024 tokens in 6.2 us split, 7.2 in pairs.
 struct Plan {
   bool pair;
   int tok;                  // pairs: tokens per tile; split: most tokens per tile
@@ -895,23 +926,27 @@ Plan choose_plan(int64_t M, int64_t N, int64_t nkb, const DeviceLimits& limits) 
   for (int tok = 64; tok <= kMaxTok; tok += 64) {
     if (tok > 64 && M <= 64) break;
     const int64_t chunks = (M + tok - 1) / tok, per = ((M + chunks - 1) / chunks + 15) / 16 * 16;
-    const int64_t alone = per > 64;                    // one CTA per SM: it cannot start under its predecessor
     for (int i = 0; i < 4; ++i) {
       const int64_t split = int64_t(1) << i, ctas = ntn * chunks * split;
       if (i > 0 && (nkb < 2 * split || ctas > 2 * sms)) break;
-      const int64_t at_once = alone ? limits.ctas[i].load(std::memory_order_relaxed) : sms;
-      const int64_t rounds = (ctas + at_once - 1) / at_once, kbs = (nkb + split - 1) / split;
-      const int64_t ns = 3700 + 5 * per + 500 * i + 1200 * alone + rounds * kbs * 230 + (rounds - 1) * (1300 + 3600 * alone);
+      const int64_t at_once = limits.ctas[i].load(std::memory_order_relaxed), kbs = (nkb + split - 1) / split;
+      const int64_t load = (ctas + at_once - 1) / at_once;              // CTAs of the busiest SM
+      int64_t ns = 3100 + 6 * per + (i > 0 ? 400 + 400 * i : 0);
+      if (per > 64)         // one CTA per SM: it cannot start under its predecessor
+        ns += 800 + load * kbs * 270 + (load - 1) * 4700;
+      else                  // two CTAs on an SM share its 120 bytes a nanosecond from L2
+        ns += kbs * (load / 2 * (273 + 32 * per / 15) + load % 2 * 270) + (load - 1) * 1150;
       if (ns < least) {
         least = ns;
         best = {false, tok, static_cast<int>(split)};
       }
     }
   }
-  for (int tok = kPairMaxTok; tok >= 128; tok -= 32) {
+  for (int tok = kPairMaxTok; tok >= 96; tok -= 32) {
     const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
-    const int64_t step = 22 * tok / 10 > 470 ? 22 * tok / 10 : 470;        // two K-blocks
-    const int64_t ns = 4300 + waves * ((nkb + 1) / 2 * step - 500 + 14 * tok);
+    // two K-blocks: by the issuing threads, or by the tensor cores and shared memory
+    const int64_t issue = tok <= kTwoIssuerTok ? 320 : 470, multiply = (tok <= kTwoIssuerTok ? 30 : 22) * tok / 10;
+    const int64_t ns = 4600 + waves * ((nkb + 1) / 2 * (issue > multiply ? issue : multiply) + 13 * tok);
     if (ns < least) {
       least = ns;
       best = {true, tok, 1};
@@ -971,6 +1006,9 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
     p.tiles_m = static_cast<int>(tiles_m);
     p.tiles_n = static_cast<int>(tiles_n);
     p.tok = tok;
+    // (each issuer needs a stage of the tile; two sets of accumulators where they and the scales fit)
+    const int issuers = tok <= kTwoIssuerTok && nkb > 2 ? 2 : 1;
+    p.accs = 2 * issuers * tok + kSfSlots * kSfCols <= 512 ? 2 : 1;
     p.tiled = tiled;
     p.withhold = withhold;
     p.vec8 = aligned16(d) && ldd % 8 == 0 && (!addend || (aligned16(addend) && ldc % 8 == 0));
@@ -987,8 +1025,9 @@ extern "C" bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64
     if (p.vec8 && addend && !make_map_bf16(&map_c, addend, M, N, ldc)) return BSF_ERR_CUDA;
     const int64_t pairs = sm_count() / 2, used = tiles < pairs ? tiles : pairs;
     void* args[] = {&map_b, &map_a, &map_d, &map_c, &p};
-    return launch_cluster(reinterpret_cast<const void*>(dense_pair_kernel), static_cast<unsigned>(2 * used), kPairThreads,
-                          kSmemBytes, 2, s, args);
+    return launch_cluster(issuers == 2 ? reinterpret_cast<const void*>(dense_pair_kernel<2>)
+                                       : reinterpret_cast<const void*>(dense_pair_kernel<1>),
+                          static_cast<unsigned>(2 * used), 32 * (15 + issuers), kSmemBytes, 2, s, args);
   }
 
   const int64_t chunks = (M + plan.tok - 1) / plan.tok, tiles = ntn * chunks;

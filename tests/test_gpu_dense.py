@@ -91,6 +91,18 @@ def test_larger_products(dev, M, N, K):
     p.check(p.run())
 
 
+# (tiles of 96 and 128 tokens, which two warps multiply: one tile per pair and several, inner lengths of 2 to 57
+# blocks, a last tile of few tokens, a last weight tile of 4 rows)
+@pytest.mark.parametrize("M,N,K", [(300, 4096, 4096), (500, 4096, 7296), (520, 2112, 2176), (910, 4100, 1152),
+                                   (1230, 4096, 640), (970, 7168, 256), (1235, 4096, 384), (2600, 7168, 256)])
+@pytest.mark.parametrize("addend", [False, True])
+def test_products_in_narrow_pair_tiles(dev, M, N, K, addend):
+    p = Problem(M, N, K, dev, seed=M + N, addend=addend)
+    first = p.run()
+    p.check(first)
+    assert torch.equal(p.run(), first)
+
+
 def test_row_major_weights_give_the_same_bits(dev):
     for M in (5, 260, 2050):
         p = Problem(M, 300, 640, dev, seed=1)
@@ -198,3 +210,9 @@ def test_withheld_loads_time_out_and_context_survives(dev, M, N, K):
     assert (d == 7.0).all()
     assert torch.equal(p.run(), want)
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 4096, 2048), (1230, 4096, 640)])
+def test_withheld_loads_stop_both_issuers_of_a_pair(dev, M, N, K):
+    """Tiles of 96 tokens, one and several per pair: neither issuing warp is left at its barrier."""
+    test_withheld_loads_time_out_and_context_survives(dev, M, N, K)
