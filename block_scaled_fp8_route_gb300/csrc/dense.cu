@@ -15,12 +15,14 @@
 //   multiplies its share of the K-blocks into tensor memory, writes the FP32 partial to its own shared
 //   memory, and after a cluster barrier every CTA sums a slice of the tile's tokens over the S partials
 //   through distributed shared memory, in rank order (no atomics, no workspace, bit-identical from run
-//   to run).  Bound by latency: 1 x 4096 x 7168 takes 7.6 us, of which the 29 MB of weights need 4.3.
+//   to run).  Bound by latency: 1 x 4096 x 7168 takes 7.5 us, of which the 29 MB of weights need 4.3
+//   (9.5 us where none of them is in L2).
 // * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 224 tokens with one cta_group::2 MMA per
 //   32 K: each stages 128 weight rows and half of the tokens, so a staged byte feeds twice the products
 //   that it would in one CTA, which shared memory could not keep up with.  Two accumulators let a tile's
 //   output drain under the next tile's MMAs.  Bound by the tensor cores and, in long runs, by power:
-//   8192 x 4096 x 7168 takes 144 us, 3.34 PFLOP/s, 87 % of twice the measured bf16 burst rate.
+//   8192 x 4096 x 7168 takes 144-149 us, 3.34 PFLOP/s, 87 % of twice the measured bf16 burst rate.
+//   Tiles of up to 128 tokens are bound by MMA issue and have two issuing warps.
 #include "common.cuh"
 #include "host_utils.h"
 #include "tma_map.h"
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
     // each stage over through a named barrier whose OR-reduced predicate carries an abort.  An MMA costs its
     // issuing thread about 86 cycles whatever its N, so tiles of up to 128 tokens (64 cycles of tensor work)
     // have two issuers that take a tile's stages in turn, each into an accumulator of its own: in tiles of
-    // 128 tokens 512 x 4096 x 7168 takes 18.7 us with two and 20.7 with one, 512 x 256 x 7168 14.4 and 19.1.
+    // 128 tokens 512 x 4096 x 7168 takes 17.5 us with two and 20.7 with one, 512 x 256 x 7168 14.4 and 19.1.
     // Wider tiles are slower with two (their accumulators leave no second set, and the tensor cores are the
     // limit): 2500 x 4096 x 7168 takes 53.5 us in tiles of 192 with one, 57.5 with two.
     const int me = warp == 1 ? 0 : 1;
@@ -910,9 +912,9 @@ bsf_status device_limits(const DeviceLimits** out) {
 
 // Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to
 // products of 1 .. 2600 tokens with 14 weights' widths from 256 to 12288 and 9 inner lengths from 512 to 7168,
-// timed in every form that could be the fastest: 9186 with weights that may be in L2 and 4174 with weights
-// that come from HBM.  On both, the choice is within 0.9 % of the best form on average; the worst is 22 % (a
-// product of 70 x 12288 x 2048 in pairs).  Both sides, 4096 x 7168: 256 tokens 14.6 us split against 17.7 in
+// timed in every form that could be the fastest: 10177 with weights that may be in L2 and 5083 with weights
+// that come from HBM.  The choice is within 0.5 % and 1.1 % of the best form on average; the worst is 24 %
+// (1 x 5120 x 2560 with K over two CTAs and not four).  Both sides, 4096 x 7168: 256 tokens 14.6 us split against 17.7 in
 // pairs, 1024 tokens 38.7 against 30.6; 1024 x 1024 takes 1024 tokens in 6.2 us split, 7.2 in pairs.
 struct Plan {
   bool pair;
