@@ -728,7 +728,8 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
     // Two warps share a quadrant's tokens.  After one exchange with its neighbour a lane holds two weight
     // rows of one token (4 bytes).  With 16-byte aligned rows of D the 32 x 32 boxes go through this warp's
     // shared memory (64-byte swizzle: 16-byte piece j of token i sits at j ^ (i / 2 % 4)); the addend is
-    // loaded the same way, ahead of the accumulator.  TMA cuts the boxes at the edges.
+    // loaded the same way, ahead of the accumulator.  TMA cuts the boxes at the edges, but a row only at a
+    // multiple of 16 bytes: where N % 8 the last box of a row goes out by elements.
     const int q = warp & 3, ew = warp - 6;
     const int nc = p.tok >> 5, c_first = ew < 4 ? 0 : (nc + 1) >> 1, c_last = ew < 4 ? (nc + 1) >> 1 : nc;
     const int odd = lane & 1;
@@ -741,7 +742,8 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
       const int tok0 = tm * p.tok;
       // boxes of this warp that touch D
       const int cuts = n0 < p.N ? min(c_last, (p.M - tok0 + 31) >> 5) - c_first : 0;
-      const bool boxed_add = p.addend && p.vec8 && cuts > 0;
+      const bool boxed = p.vec8 && (p.N % 8 == 0 || n0 + 32 <= p.N);
+      const bool boxed_add = p.addend && boxed && cuts > 0;
       // addend box i of the tile into its buffer (its last store has been read)
       auto load_add = [&](int i) {
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
           if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
         }
         if (c - c_first >= cuts) continue;
-        if (p.vec8) {
+        if (boxed) {
           uint8_t* buf = bufs + box * kBoxBytes;
           if (boxed_add) {
             wait_landed(&add_full[ew * 2 + box], (add_phase >> box) & 1u, p.err);

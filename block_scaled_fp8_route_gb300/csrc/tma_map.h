@@ -58,7 +58,8 @@ inline bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
 }
 
 // 2-D bf16 tensor [rows, cols] (row pitch = ld elements), box {32 cols, 32 rows}, 64-byte swizzle; loads
-// past the edges read zeros, stores past them write nothing.
+// past the edges read zeros, stores past them write nothing, but the edge of a row counts in pieces of 16
+// bytes: a store also writes the columns from cols to the next multiple of 8.
 inline bool make_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld) {
   auto fn = encode_fn();
   if (!fn) return false;

@@ -607,7 +607,7 @@ bsf_status bsf_swiglu_quantise(const void* y, int64_t T, int64_t K, int64_t ld, 
  * FP32 accumulation on the tensor cores, a fixed order of sums (bit-identical
  * from run to run), round-to-nearest-even to bf16.  K % 128 == 0; 16-byte
  * aligned a, b, sfa, sfb; d and addend need only their element alignment (8
- * bytes and row strides of 4 elements are faster, from 256 tokens on 16 bytes
+ * bytes and row strides of 4 elements are faster, with many tokens 16 bytes
  * and 8 elements).  flags: BSF_B_TILED, and BSF_DEBUG_WITHHOLD_LOADS as for the
  * grouped products.  M == 0 is a no-op.  A wait that runs out sets
  * BSF_DEVERR_TIMEOUT.

@@ -128,6 +128,22 @@ def test_strides_alignment_and_bounds(dev, off, extra, coff, cextra, M, N):
     assert (wide_d == -3.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 4090, 2048), (1300, 2113, 512), (2100, 1541, 256), (900, 4095, 640),
+                                   (40, 1001, 256), (129, 27, 128)])
+@pytest.mark.parametrize("addend", [False, True])
+def test_columns_past_n_are_not_written(dev, M, N, K, addend):
+    """16-byte aligned rows of a width that is not a multiple of 8: what lies behind them stays."""
+    p = Problem(M, N, K, dev, seed=N, addend=addend)
+    wide = torch.full((M + 1, N + 8 + -N % 8), 7.0, dtype=torch.bfloat16, device=dev)
+    if addend:                                                   # the addend's rows are aligned too
+        c = torch.full((M, N + -N % 8), float("nan"), dtype=torch.bfloat16, device=dev)
+        c[:, :N] = p.c
+        p.c = c[:, :N]
+    d = p.run(d=wide[:M, :N])
+    p.check(d)
+    assert (wide[:M, N:] == 7.0).all() and (wide[M] == 7.0).all()
+
+
 def test_addend_may_be_the_output(dev):
     for M in (9, 1100):
         p = Problem(M, 512, 384, dev, seed=3, addend=True)
