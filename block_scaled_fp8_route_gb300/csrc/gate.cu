@@ -360,7 +360,9 @@ __global__ void __launch_bounds__(32 * kGateWarps, gate_ctas(VPL)) gate_kernel(c
         l = __ldg(reinterpret_cast<const float*>(at));
       l = fminf(l, FLT_MAX);
     }
-    if (!sig && !need_max) m = __shfl_sync(kAll, l, 0);              // the largest logit is the first choice
+    // weights that are divided by their sum are taken relative to the largest chosen logit (without a bias the
+    // first choice), which a bias may have put so far below the row's that every exp(l - m) would vanish
+    if (!sig && renorm) m = biased ? warp_max(l) : __shfl_sync(kAll, l, 0);
     float w = 0.f;
     if (my_id >= 0) w = sig ? sigmoid(l) : expf(l - m) * inv;
     if (renorm) {

@@ -135,7 +135,7 @@ __device__ __forceinline__ void quantise_piece(const RowPiece& p, bool active, i
 // Bound by HBM on paper (4 K read, K written a row) and near its limit of issue slots: exp and an IEEE
 // division took 48 slots a value (178 us for 65536 routed rows x 2048 of a 98048-row operand); pairs
 // of values that share a slot in everything but exp, and a quotient of 3 roundings, leave about 25.
-// With the next row's loads in flight that case takes 119.7 us, 5.6 TB/s, 83 % of the copy rate.
+// With the next row's loads in flight that case takes 114 us, 5.9 TB/s, 87 % of the copy rate.
 // At most 64 registers (4 CTAs per SM): 3 CTAs 126 us, 5 CTAs (48 registers) 132 us.
 __global__ void __launch_bounds__(256, 4) swiglu_quantise_kernel(const uint16_t* __restrict__ y, int64_t T, int K,
                                                                  int64_t ld, uint8_t* __restrict__ q,

@@ -550,6 +550,8 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
  *                 over the usable experts, in float32: within 2^-20 of these
  *                 values where they decide a choice, within a few units in
  *                 the last place (plus that of a rounded l - m) in the weights.
+ *                 A score below 2^-126 counts as 0, except in the softmax
+ *                 weights that BSF_GATE_RENORMALISE divides by their sum.
  *   bias          fp32 [E] or NULL.  With a bias the choice goes by s_e + b_e
  *                 (an expert for which that is NaN or -inf is never chosen);
  *                 without one by the logit itself.

@@ -74,6 +74,17 @@ def test_groups(dev, E, groups, kept, kr, top2, sigmoid, biased):
            most_unclear=0.25)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,groups,kept,kr", [(64, 1, 1, 6), (256, 8, 3, 8), (60, 12, 5, 4)])
+def test_renormalised_weights_far_below_the_largest_logit(dev, dtype, E, groups, kept, kr):
+    """A bias keeps out the experts of the largest logits, so the chosen scores are all near exp(-100)."""
+    logits = _logits(50, E, torch.float32, dev, seed=E)
+    logits[:, 1] = 100.0
+    bias = torch.linspace(0.5, 1.5, E, device=dev)[torch.randperm(E, generator=torch.Generator().manual_seed(2))]
+    bias[1] = -3.0
+    _check(logits.to(dtype), kr, dev, bias=bias, groups=groups, kept=kept)
+
+
 @pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
 def test_ties_go_to_the_lowest_index(dev, groups, kept):
     g = torch.Generator().manual_seed(1)
