@@ -24,6 +24,13 @@ def _no_timer(name):
     yield
 
 
+def _expect(t, what, dtype, shape, device):
+    """Refuse a tensor that a kernel would misread or write past: the library trusts types and sizes."""
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+
+
 class MoEPath:
     """``fmt`` = "fp8" (E4M3, UE8M0 per 1 x 128 / 128 x 128), "nvfp4" (E2M1, UE4M3 per 1 x 16, a
     power-of-two tensor exponent per expert for the weights and ``a_exp`` for the activations) or
@@ -263,6 +270,13 @@ class MoEBlock:
         t = timer if timer is not None else _no_timer
         p, b = self.path, self.path.bufs
         z = self.z if z is None else z
+        device = self.z.device
+        _expect(x, "x", torch.bfloat16, (self.T, self.K), device)
+        _expect(logits, "logits", torch.bfloat16 if logits.dtype == torch.bfloat16 else torch.float32,
+                (self.T, p.E), device)
+        _expect(z, "z", torch.bfloat16, (self.T, self.K), device)
+        if not z.is_contiguous():
+            raise ValueError("z: expected a contiguous tensor")
         with t("gate"):
             ops.gate(logits, self.kr, topk_ids=self.topk_ids, topk_weights=self.topk_weights, **self.gate_args)
         p._stage_in(x, self.topk_ids, t)
