@@ -158,6 +158,8 @@ class MoEPath:
         context manager wrapped around each stage (``dispatch`` or ``quantise`` + ``route``,
         ``gemm``, ``quantise2`` + ``gemm2``, ``combine``), e.g. to record CUDA events."""
         t = timer if timer is not None else _no_timer
+        z = self.z if z is None else z
+        self._check_inputs(x, topk_ids, topk_weights, h2, z)
         self._stage_in(x, topk_ids, t)
         with t("gemm"):
             self.gemm(self.bufs.a_packed, self.bufs.sfa_packed, self.wq, self.sfb, self.y, self.b_exp)
@@ -176,10 +178,25 @@ class MoEPath:
             with t("gemm2"):
                 self.gemm(self.q2, self.sf2, self.w2q, self.sfb2, self.y2, self.b2_exp)
             out = self.y2
-        z = self.z if z is None else z
         with t("combine"):
             ops.combine(out, self.bufs.output_index, topk_weights, z=z)
         return z
+
+    def _check_inputs(self, x, topk_ids, topk_weights, h2, z):
+        device = self.z.device
+        _expect(x, "x", torch.bfloat16, (self.T, self.K), device)
+        _expect(topk_ids, "topk_ids", torch.int32, (self.T, self.kr), device)
+        _expect(topk_weights, "topk_weights", torch.float32, (self.T, self.kr), device)
+        _expect(z, "z", torch.bfloat16, self.z.shape, device)
+        if not z.is_contiguous():
+            raise ValueError("z: expected a contiguous tensor")
+        if self.two_gemms:
+            # (fewer rows than the packed capacity will do: no segment may reach past them)
+            rows = max(self.bufs.m_cap, 1)
+            if h2 is None or h2.dim() != 2 or h2.shape[0] > rows:
+                raise ValueError(f"h2: expected at most {rows} rows of {self.K2} values for the second product, got "
+                                 f"{None if h2 is None else tuple(h2.shape)}")
+            _expect(h2, "h2", torch.bfloat16, (h2.shape[0], self.K2), device)
 
     def _stage_in(self, x, topk_ids, t):
         """Quantise + route + scatter of the activations into the packed operand."""

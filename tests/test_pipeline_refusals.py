@@ -66,3 +66,49 @@ def test_block_refuses_other_logits(block, logits):
 def test_block_refuses_other_outputs(block, z):
     with pytest.raises(ValueError, match="^z: "):
         block.step(X, LOGITS, z=z)
+
+
+M_CAP, K2, N2 = 24, 128, 384
+
+
+class _Bufs:
+    m_cap = M_CAP
+
+
+@pytest.fixture
+def path(monkeypatch):
+    def reached(*a, **k):
+        raise Reached
+    monkeypatch.setattr(MoEPath, "_stage_in", reached)
+    p = object.__new__(MoEPath)
+    p.E, p.kr, p.T, p.K, p.K2, p.N2, p.bufs, p.two_gemms = E, KR, T, K, K2, N2, _Bufs(), True
+    p.z = torch.zeros(T, N2, dtype=BF16)
+    return p
+
+
+IDS, WEIGHTS = torch.zeros(T, KR, dtype=torch.int32), torch.zeros(T, KR)
+H2 = torch.zeros(M_CAP, K2, dtype=BF16)
+
+
+def test_path_takes_what_it_was_made_for(path):
+    for h2 in (H2, H2[:M_CAP - 3]):
+        with pytest.raises(Reached):
+            path.step(X, IDS, WEIGHTS, h2, z=torch.zeros(T, N2, dtype=BF16))
+    path.two_gemms = False
+    with pytest.raises(Reached):
+        path.step(X, IDS, WEIGHTS)
+
+
+@pytest.mark.parametrize("name,value", [
+    ("x", torch.zeros(T + 1, K, dtype=BF16)), ("x", torch.zeros(T, K + 128, dtype=BF16)), ("x", torch.zeros(T, K)),
+    ("topk_ids", torch.zeros(T - 1, KR, dtype=torch.int32)), ("topk_ids", torch.zeros(T, KR, dtype=torch.int64)),
+    ("topk_ids", torch.zeros(T, KR + 1, dtype=torch.int32)), ("topk_weights", torch.zeros(T, KR - 1)),
+    ("topk_weights", torch.zeros(T, KR, dtype=BF16)), ("h2", None), ("h2", torch.zeros(M_CAP + 1, K2, dtype=BF16)),
+    ("h2", torch.zeros(M_CAP, K2 - 64, dtype=BF16)), ("h2", torch.zeros(M_CAP, K2)),
+    ("z", torch.zeros(T, K, dtype=BF16)), ("z", torch.zeros(T, N2)), ("z", torch.zeros(N2, T, dtype=BF16).t()),
+    ("x", X.to("meta")), ("topk_ids", IDS.to("meta")), ("topk_weights", WEIGHTS.to("meta")), ("h2", H2.to("meta"))])
+def test_path_refuses_other_inputs(path, name, value):
+    args = dict(x=X, topk_ids=IDS, topk_weights=WEIGHTS, h2=H2, z=None)
+    args[name] = value
+    with pytest.raises(ValueError, match=f"^{name}: "):
+        path.step(**args)
