@@ -253,15 +253,33 @@ class MoEBlock:
         --combine--> z  (+ an expert that every token takes: dense gate-up, SwiGLU, dense down onto z)
 
     ``w13_bf16`` [E, 2 I, K] holds each expert's gate rows and then its up rows, ``w2_bf16`` [E, K, I] its
-    down projection; ``shared`` = (w13 [2 S, K], w2 [K, S]) of the always-active expert, any width S.  The
-    other keyword arguments are those of ``ops.gate`` (``score``, ``bias``, ``groups``, ...).  Every step is
-    a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be captured."""
+    down projection (K and I multiples of 128); ``shared`` = (w13 [2 S, K], w2 [K, S]) of the always-active
+    expert, S any multiple of 8.  The other keyword arguments are those of ``ops.gate`` that say how to choose
+    (``score``, ``bias``, ``groups``, ``kept_groups``, ``group_score``, ``renormalise``, ``scale``).  Every step
+    is a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be captured."""
+
+    _GATE_ARGS = {"score", "bias", "groups", "kept_groups", "group_score", "renormalise", "scale"}
 
     def __init__(self, E, kr, T, K, I, w13_bf16, w2_bf16, shared=None, layout=ops.CONTIGUOUS, align_or_max_m=128,
                  device="cuda", expected_m=0, **gate):
         if tuple(w13_bf16.shape) != (E, 2 * I, K) or tuple(w2_bf16.shape) != (E, K, I):
             raise ValueError(f"expected w13 {(E, 2 * I, K)} and w2 {(E, K, I)}, got {tuple(w13_bf16.shape)} and "
                              f"{tuple(w2_bf16.shape)}")
+        if K % 128 or I % 128:
+            raise ValueError(f"expected K and I to be multiples of 128, got {K} and {I}")
+        for w in (w13_bf16, w2_bf16) + (() if shared is None else tuple(shared)):
+            if w.dtype != torch.bfloat16:
+                raise ValueError(f"expected bfloat16 weights, got {w.dtype}")
+        if shared is not None:
+            w13, w2 = shared
+            S = w2.shape[-1]
+            if w13.shape != (2 * S, K) or w2.shape != (K, S) or S % 8 or S == 0:
+                raise ValueError(f"shared expert: expected w13 (2 S, {K}) and w2 ({K}, S) with S a multiple of 8, got "
+                                 f"{tuple(w13.shape)} and {tuple(w2.shape)}")
+        if not gate.keys() <= self._GATE_ARGS:
+            raise TypeError(f"unexpected arguments {sorted(gate.keys() - self._GATE_ARGS)}")
+        # an empty batch: the gate's arguments are refused here, not at the first step
+        ops.gate(torch.empty((0, E), dtype=torch.float32, device=device), kr, **gate)
         self.T, self.K, self.I, self.kr, self.gate_args = T, K, I, kr, gate
         self.path = MoEPath(E, kr, T, K, 2 * I, w13_bf16, layout=layout, align_or_max_m=align_or_max_m,
                             w2_bf16=w2_bf16, device=device, expected_m=expected_m)
@@ -270,12 +288,7 @@ class MoEBlock:
         self.topk_weights = torch.empty((T, kr), dtype=torch.float32, device=device)
         self.shared = None
         if shared is not None:
-            w13, w2 = (w.to(device) for w in shared)
-            S = w2.shape[1]
-            if tuple(w13.shape) != (2 * S, K) or w2.shape[0] != K or S % 8:
-                raise ValueError(f"shared expert: expected w13 (2 S, {K}) and w2 ({K}, S) with S a multiple of 8, got "
-                                 f"{tuple(w13.shape)} and {tuple(w2.shape)}")
-            self.shared = (ops.prepare_dense_weight(w13), ops.prepare_dense_weight(w2))
+            self.shared = tuple(ops.prepare_dense_weight(w.to(device)) for w in shared)
             Sp = (S + 127) // 128 * 128
             self.shared_y = torch.empty((T, 2 * S), dtype=torch.bfloat16, device=device)
             self.shared_q = torch.empty((T, Sp), dtype=torch.uint8, device=device)
