@@ -557,7 +557,9 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
 def prepare_dense_weight(w):
     """w bf16 [N, K] -> (b uint8 [Np, Kp] tiled, sfb int32 [ceil(Kp/512), Np]) for ``dense_gemm`` with
     ``B_TILED``, on the current stream; N and K are rounded up to 128 with zero weights."""
-    N, K = w.shape
+    N, K = _two_dims(w, "w")
+    if w.dtype != _BF16 or not w.is_cuda:
+        _refuse(w, _BF16, None, "w")
     w = torch.nn.functional.pad(w, (0, -K % 128, 0, -N % 128))
     q, sf128 = quantise_weight(w.unsqueeze(0))
     sfb = prepare_weight_sf(sf128, w.shape[1])
