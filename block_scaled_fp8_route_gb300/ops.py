@@ -472,6 +472,21 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+# index of the device that the library launches on and whose SM count and error word it uses
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse_devices(names, operands, stream):
+    """Why these operands (None: not given) are not all on the current CUDA device."""
+    for name, t in zip(names.split(), operands):
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    on = [f"{name} on {t.device}" for name, t in zip(names.split(), operands) if t is not None]
+    if stream is not None:
+        on.append(f"stream on cuda:{stream.device_index}")
+    raise ValueError(f"expected every operand on the current device cuda:{_current_device()}: {', '.join(on)}")
+
+
 def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, group_score="max", renormalise=True,
          scale=1.0, topk_ids=None, topk_weights=None, stream=None):
     """Router logits [T, E] (float32 or bf16, any row stride) -> (topk_ids int32 [T, kr], topk_weights
@@ -498,16 +513,18 @@ def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, gro
     if bias is not None:
         if bias.dtype != _F32 or bias.shape != (E,) or not bias.is_contiguous() or not bias.is_cuda:
             _refuse(bias, _F32, (E,), "bias")
-        bias = bias.data_ptr()
     if stream is not None:                     # used there, whatever stream they were made on
         _used_on(stream, topk_ids, topk_weights)
-    if not (logits.is_cuda and topk_ids.is_cuda and topk_weights.is_cuda):
-        raise ValueError("logits, topk_ids, topk_weights: a host tensor where each must be a CUDA tensor")
+    device = logits.get_device()               # (-1 of a host tensor)
+    if (device < 0 or topk_ids.get_device() != device or topk_weights.get_device() != device
+            or (bias is not None and bias.get_device() != device) or device != _current_device()
+            or (stream is not None and stream.device_index != device)):
+        _refuse_devices("logits topk_ids topk_weights bias", (logits, topk_ids, topk_weights, bias), stream)
     status = _lib.load().bsf_gate(
-        logits.data_ptr(), kind, T, E, ld, bias, groups, groups if kept_groups is None else kept_groups, kr,
+        logits.data_ptr(), kind, T, E, ld, None if bias is None else bias.data_ptr(), groups, groups if kept_groups is None else kept_groups, kr,
         _SCORES[score] | _GROUP_SCORES[group_score] | (GATE_RENORMALISE if renormalise else 0), scale,
         topk_ids.data_ptr(), topk_weights.data_ptr(),
-        _current_stream(logits.get_device()) if stream is None else stream.cuda_stream)
+        _current_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "gate")
     return topk_ids, topk_weights
@@ -541,14 +558,17 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
         if (token_of_row.dtype != _I32 or rows_used.dtype != _I32 or token_of_row.numel() < T or rows_used.numel() < 1
                 or not token_of_row.is_cuda or not rows_used.is_cuda or not token_of_row.is_contiguous()):
             raise ValueError("rows: expected CUDA int32 tensors, token_of_row of at least T entries and rows_used of one")
-        token_of_row, rows_used = token_of_row.data_ptr(), rows_used.data_ptr()
     if stream is not None:
         _used_on(stream, q, sf)
-    if not (y.is_cuda and q.is_cuda and sf.is_cuda):
-        raise ValueError("y, q, sf: a host tensor where each must be a CUDA tensor")
+    device = y.get_device()
+    if (device < 0 or q.get_device() != device or sf.get_device() != device
+            or (rows is not None and (token_of_row.get_device() != device or rows_used.get_device() != device))
+            or device != _current_device() or (stream is not None and stream.device_index != device)):
+        _refuse_devices("y q sf token_of_row rows_used", (y, q, sf, token_of_row, rows_used), stream)
     status = _lib.load().bsf_swiglu_quantise(
-        y.data_ptr(), T, K, ld, token_of_row, rows_used, q.data_ptr(), sf.data_ptr(), ld_sf,
-        _current_stream(y.get_device()) if stream is None else stream.cuda_stream)
+        y.data_ptr(), T, K, ld, None if rows is None else token_of_row.data_ptr(),
+        None if rows is None else rows_used.data_ptr(), q.data_ptr(), sf.data_ptr(), ld_sf,
+        _current_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "swiglu_quantise")
     return q, sf
@@ -589,18 +609,22 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
     elif d.dtype != _BF16 or d.shape != out:
         _refuse(d, _BF16, out, "d")
     ldd = _row_stride(d, M, N, "d")
-    ldc, c = 0, None
+    ldc = 0
     if addend is not None:
         if addend.dtype != _BF16 or addend.shape != out or not addend.is_cuda:
             _refuse(addend, _BF16, out, "addend")
-        ldc, c = _row_stride(addend, M, N, "addend"), addend.data_ptr()
+        ldc = _row_stride(addend, M, N, "addend")
     if stream is not None:
         _used_on(stream, d)
-    if not (a.is_cuda and sfa.is_cuda and b.is_cuda and sfb.is_cuda and d.is_cuda):
-        raise ValueError("a, sfa, b, sfb, d: a host tensor where each must be a CUDA tensor")
+    device = a.get_device()
+    if (device < 0 or sfa.get_device() != device or b.get_device() != device or sfb.get_device() != device
+            or d.get_device() != device or (addend is not None and addend.get_device() != device)
+            or device != _current_device() or (stream is not None and stream.device_index != device)):
+        _refuse_devices("a sfa b sfb d addend", (a, sfa, b, sfb, d, addend), stream)
     status = _lib.load().bsf_dense_gemm(
-        a.data_ptr(), sfa.data_ptr(), ld_sf, M, b.data_ptr(), sfb.data_ptr(), N, K, c, ldc, d.data_ptr(), ldd, flags,
-        _current_stream(a.get_device()) if stream is None else stream.cuda_stream)
+        a.data_ptr(), sfa.data_ptr(), ld_sf, M, b.data_ptr(), sfb.data_ptr(), N, K,
+        None if addend is None else addend.data_ptr(), ldc, d.data_ptr(), ldd, flags,
+        _current_stream(device) if stream is None else stream.cuda_stream)
     if status:
         _lib.check(status, "dense_gemm")
     return d
