@@ -460,10 +460,22 @@ def _two_dims(t, what):
 
 
 def _used_on(stream, *tensors):
-    """The allocator keeps the memory of these outputs until the work queued on ``stream`` is done."""
+    """The allocator keeps the memory of these tensors until the work queued on ``stream`` is done, also if the
+    caller drops them at once."""
     for t in tensors:
-        if t.is_cuda:
+        if t is not None:
             t.record_stream(stream)
+
+
+def _empty(shape, dtype, like, stream):
+    """An output that ``stream`` (None: the current one) writes.  Memory that the current stream freed may still
+    be in use there, so another stream takes its own; the current stream is where the caller will use it."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
@@ -503,23 +515,23 @@ def gate(logits, kr, score="softmax", bias=None, groups=1, kept_groups=None, gro
     ld = _row_stride(logits, T, E, "logits")
     out = (T, kr)
     if topk_ids is None:
-        topk_ids = torch.empty(out, dtype=_I32, device=logits.device)
+        topk_ids = _empty(out, _I32, logits, stream)
     elif topk_ids.dtype != _I32 or topk_ids.shape != out or not topk_ids.is_contiguous():
         _refuse(topk_ids, _I32, out, "topk_ids")
     if topk_weights is None:
-        topk_weights = torch.empty(out, dtype=_F32, device=logits.device)
+        topk_weights = _empty(out, _F32, logits, stream)
     elif topk_weights.dtype != _F32 or topk_weights.shape != out or not topk_weights.is_contiguous():
         _refuse(topk_weights, _F32, out, "topk_weights")
     if bias is not None:
         if bias.dtype != _F32 or bias.shape != (E,) or not bias.is_contiguous() or not bias.is_cuda:
             _refuse(bias, _F32, (E,), "bias")
-    if stream is not None:                     # used there, whatever stream they were made on
-        _used_on(stream, topk_ids, topk_weights)
     device = logits.get_device()               # (-1 of a host tensor)
     if (device < 0 or topk_ids.get_device() != device or topk_weights.get_device() != device
             or (bias is not None and bias.get_device() != device) or device != _current_device()
             or (stream is not None and stream.device_index != device)):
         _refuse_devices("logits topk_ids topk_weights bias", (logits, topk_ids, topk_weights, bias), stream)
+    if stream is not None:
+        _used_on(stream, logits, topk_ids, topk_weights, bias)
     status = _lib.load().bsf_gate(
         logits.data_ptr(), kind, T, E, ld, None if bias is None else bias.data_ptr(), groups, groups if kept_groups is None else kept_groups, kr,
         _SCORES[score] | _GROUP_SCORES[group_score] | (GATE_RENORMALISE if renormalise else 0), scale,
@@ -544,11 +556,11 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
     Kp = (K + 127) // 128 * 128
     words = (Kp + 511) // 512
     if q is None:
-        q = torch.empty((T, Kp), dtype=_U8, device=y.device)
+        q = _empty((T, Kp), _U8, y, stream)
     elif q.dtype != _U8 or q.shape != (T, Kp) or not q.is_contiguous():
         _refuse(q, _U8, (T, Kp), "q")
     if sf is None:
-        sf = torch.empty((words, sf_ld(T)), dtype=_I32, device=y.device)
+        sf = _empty((words, sf_ld(T)), _I32, y, stream)
     ld_sf = sf.shape[-1]
     if sf.dtype != _I32 or sf.shape != (words, ld_sf) or not sf.is_contiguous():
         _refuse(sf, _I32, (words, ld_sf), "sf")
@@ -558,13 +570,13 @@ def swiglu_quantise(y, rows=None, q=None, sf=None, stream=None):
         if (token_of_row.dtype != _I32 or rows_used.dtype != _I32 or token_of_row.numel() < T or rows_used.numel() < 1
                 or not token_of_row.is_cuda or not rows_used.is_cuda or not token_of_row.is_contiguous()):
             raise ValueError("rows: expected CUDA int32 tensors, token_of_row of at least T entries and rows_used of one")
-    if stream is not None:
-        _used_on(stream, q, sf)
     device = y.get_device()
     if (device < 0 or q.get_device() != device or sf.get_device() != device
             or (rows is not None and (token_of_row.get_device() != device or rows_used.get_device() != device))
             or device != _current_device() or (stream is not None and stream.device_index != device)):
         _refuse_devices("y q sf token_of_row rows_used", (y, q, sf, token_of_row, rows_used), stream)
+    if stream is not None:
+        _used_on(stream, y, q, sf, token_of_row, rows_used)
     status = _lib.load().bsf_swiglu_quantise(
         y.data_ptr(), T, K, ld, None if rows is None else token_of_row.data_ptr(),
         None if rows is None else rows_used.data_ptr(), q.data_ptr(), sf.data_ptr(), ld_sf,
@@ -605,7 +617,7 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
         _refuse(sfb, _I32, (words, Np), "sfb")
     out = (M, N)
     if d is None:
-        d = torch.empty(out, dtype=_BF16, device=a.device)
+        d = _empty(out, _BF16, a, stream)
     elif d.dtype != _BF16 or d.shape != out:
         _refuse(d, _BF16, out, "d")
     ldd = _row_stride(d, M, N, "d")
@@ -614,13 +626,13 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
         if addend.dtype != _BF16 or addend.shape != out or not addend.is_cuda:
             _refuse(addend, _BF16, out, "addend")
         ldc = _row_stride(addend, M, N, "addend")
-    if stream is not None:
-        _used_on(stream, d)
     device = a.get_device()
     if (device < 0 or sfa.get_device() != device or b.get_device() != device or sfb.get_device() != device
             or d.get_device() != device or (addend is not None and addend.get_device() != device)
             or device != _current_device() or (stream is not None and stream.device_index != device)):
         _refuse_devices("a sfa b sfb d addend", (a, sfa, b, sfb, d, addend), stream)
+    if stream is not None:
+        _used_on(stream, a, sfa, b, sfb, d, addend)
     status = _lib.load().bsf_dense_gemm(
         a.data_ptr(), sfa.data_ptr(), ld_sf, M, b.data_ptr(), sfb.data_ptr(), N, K,
         None if addend is None else addend.data_ptr(), ldc, d.data_ptr(), ldd, flags,
