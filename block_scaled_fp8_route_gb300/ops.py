@@ -446,11 +446,12 @@ def _refuse(t, dtype, shape, what):
 
 
 def _row_stride(t, rows, cols, what):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
+    """Row stride of a 2-D tensor whose rows are contiguous.  That of a single row is never used: whatever the
+    view says (logits[:, -1] of one sequence strides over all of it), the next multiple of 8 is in every range."""
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _two_dims(t, what):
