@@ -218,8 +218,13 @@ __global__ void __launch_bounds__(32 * kGateWarps, gate_ctas(VPL)) gate_kernel(c
         key[i] = key[i] > -INFINITY ? v : -INFINITY;
       }
     }
-    // what a group's two largest keys count for in its score (scores rise with the logits)
-    auto counts = [&](float k) { return biased || !top2 ? k : score(k); };
+    // a group's score from its two largest keys a >= b (scores rise with the logits), -inf where none can be chosen.
+    // The sum of two is halved: with biases near the type's lowest value the sum itself would be -inf.
+    auto counts = [&](float k) { return biased ? k : score(k); };
+    auto group_score = [&](float a, float b) {
+      if (a == -INFINITY || !top2) return a;
+      return 0.5f * counts(a) + (b > -INFINITY ? 0.5f * counts(b) : 0.f);
+    };
 
     bool open = true;                               // this lane's experts take part
     if (groups > 1 && p.lane_groups) {
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, gate_ctas(VPL)) gate_kernel(c
           b = fmaxf(fmaxf(b, b2), fminf(a, a2));
           a = fmaxf(a, a2);
         }
-        gs = a > -INFINITY ? counts(a) + (b > -INFINITY ? counts(b) : 0.f) : -INFINITY;
+        gs = group_score(a, b);
       } else {
 #pragma unroll
         for (int i = 1; i < VPL; ++i) gs = fmaxf(gs, key[i]);
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(32 * kGateWarps, gate_ctas(VPL)) gate_kernel(c
           b = fmaxf(b, fminf(a, v));
           a = fmaxf(a, v);
         }
-        if (a > -INFINITY) gs = counts(a) + (top2 && b > -INFINITY ? counts(b) : 0.f);
+        gs = group_score(a, b);
       }
       __syncwarp();
       uint32_t keep = 0;
