@@ -547,9 +547,10 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
  *                 or -inf is not usable for that token; +inf counts as the
  *                 largest finite float32.
  *   score         s_e = 1 / (1 + exp(-l_e)), or exp(l_e - m) / sum exp(l_j - m)
- *                 over the usable experts, in float32: within 2^-20 of these
- *                 values where they decide a choice, within a few units in
- *                 the last place (plus that of a rounded l - m) in the weights.
+ *                 over the usable experts, in float32: within 2^-20 of their
+ *                 size (plus what a float32 l - m is rounded by) where they
+ *                 decide a choice, within a few units in the last place (plus
+ *                 the same) in the weights.
  *                 A score below 2^-126 counts as 0, except in the softmax
  *                 weights that BSF_GATE_RENORMALISE divides by their sum.
  *   bias          fp32 [E] or NULL.  With a bias the choice goes by s_e + b_e
