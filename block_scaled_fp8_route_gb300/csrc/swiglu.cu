@@ -44,20 +44,20 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// g / (1 + exp(-g)) * u of a pair with |g| <= kPlainGate: the quotient by the hardware reciprocal, then
+// g / (1 + exp(-g)) * u of a pair with |g| <= kPlainGate, from -g: the quotient by the hardware reciprocal, then
 // corrected once by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  For every bf16 g in that range this is the IEEE quotient bit for bit
-// (all of them compared on a GB300), except that -0 comes out as +0.
+// System/6000 processor", 1990).  For every bf16 g in that range this is the IEEE quotient (the test of both
+// branches compares the codes of all of them, with 128 ups each).  Numerator and reciprocal are taken negated: the
+// remainder of a zero is +0 either way, and times -r it leaves the sign of a zero quotient as it is.
 constexpr float kPlainGate = 80.f;
-__device__ __forceinline__ uint64_t swiglu_pair(float g0, float g1, uint64_t u) {
-  const uint64_t minus = pair(-1.f, -1.f);
-  const uint64_t nd = fma2(pair(expf(-g0), expf(-g1)), minus, minus);       // -(1 + e)
-  float n0, n1;
-  unpair(nd, n0, n1);
-  const uint64_t r = pair(rcp_approx(-n0), rcp_approx(-n1));
-  const uint64_t g = pair(g0, g1);
-  const uint64_t q = mul2(g, r);
-  return mul2(fma2(fma2(nd, q, g), r, q), u);
+__device__ __forceinline__ uint64_t swiglu_pair(float minus_g0, float minus_g1, uint64_t u) {
+  const uint64_t d = add2(pair(expf(minus_g0), expf(minus_g1)), pair(1.f, 1.f));
+  float d0, d1;
+  unpair(d, d0, d1);
+  const uint64_t minus_r = pair(rcp_approx(-d0), rcp_approx(-d1));
+  const uint64_t minus_g = pair(minus_g0, minus_g1);
+  const uint64_t q = mul2(minus_g, minus_r);
+  return mul2(fma2(fma2(d, q, minus_g), minus_r, q), u);
 }
 
 struct RowPiece {
@@ -87,7 +87,7 @@ __device__ __forceinline__ void quantise_piece(const RowPiece& p, bool active, i
   if (__low2float(most) <= kPlainGate && __high2float(most) <= kPlainGate) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = swiglu_pair(__uint_as_float(gw[i] << 16), __uint_as_float(gw[i] & 0xFFFF0000u),
+      v[i] = swiglu_pair(__uint_as_float((gw[i] << 16) ^ 0x80000000u), __uint_as_float((gw[i] & 0xFFFF0000u) ^ 0x80000000u),
                          pair(__uint_as_float(uw[i] << 16), __uint_as_float(uw[i] & 0xFFFF0000u)));
   } else {
     // gates so large that 1 + exp(-g) may leave the range of the reciprocal, infinities and NaN
