@@ -57,7 +57,7 @@ struct DenseArgs {
   int split, stages;
   int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between their accumulators
   uint32_t tmem_cols;
-  int tiled, withhold;       // withhold: BSF_DEBUG_WITHHOLD_LOADS
+  int tiled, withhold;       // withhold: BSF_DEBUG_WITHHOLD_LOADS, in the last CTA of each cluster
   int vec4;                  // four neighbouring columns of D (and C) are 8-byte aligned
   int* err;
 };
@@ -78,6 +78,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       int issued = 0;
-      for (int kb = kb0; kb < kb1 && !p.withhold; ++kb) {
+      for (int kb = kb0; kb < kb1 && !(p.withhold && rank == p.split - 1); ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) break;
         uint8_t* dst = smem + stage * stage_bytes;
         mbar_arrive_expect_tx(&full[stage], stage_bytes);
@@ -330,7 +333,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       have = __all_sync(0xffffffffu, have);
       tc_fence_after();
     }
-    if (!have && lane == 0) *abort_flag = 1;
+    // A wait that ran out anywhere in this CTA ends here, and keeps all of its cluster from storing sums with its
+    // partial.  (The other CTAs, launched with this one, have long been running.)
+    if (!have) {
+      if (lane == 0)
+        for (int s = 0; s < p.split; ++s) st_cluster_u32(map_rank(smem_u32(const_cast<int*>(abort_flag)), s), 1u);
+      __syncwarp();
+    }
   }
 
   // ---------------------------------------------------------------- partial to shared memory, sum, store

@@ -82,7 +82,9 @@ typedef enum bsf_status {
 /* Fault injection for tests of the failure path: the kernel's load producer
  * withholds every load, so each consumer's bounded wait runs out; the kernel
  * sets BSF_DEVERR_TIMEOUT, releases its tensor memory and returns without
- * writing d.  No GPU fault or hang is involved. */
+ * writing d.  (Where bsf_dense_gemm splits K over a cluster, only the last
+ * CTA of each cluster withholds its loads, and still none of them writes d.)
+ * No GPU fault or hang is involved. */
 #define BSF_DEBUG_WITHHOLD_LOADS 0x100
 
 const char* bsf_status_string(bsf_status status);
