@@ -30,12 +30,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 }
 
 // ---------------------------------------------------------------- programmatic dependent launch
-// A kernel launched with the programmatic-serialization attribute (launch_dependent in
+// A kernel launched with the programmatic-serialization attribute (DependentLaunch in
 // host_utils.h) may begin before the preceding kernel on its stream has finished: it is
 // scheduled once every CTA of that kernel has executed pdl_launch_dependents() or exited.
 // pdl_wait() then blocks until the preceding kernel has completed and its memory writes are
-// visible, so a dependent must not touch global memory before it.  Both are no-ops when the
-// kernel was launched without the attribute.
+// visible, so a dependent must not load from or store to global memory before it.  Both are
+// no-ops when the kernel was launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmap_a);
   }
   pdl_launch_dependents();
-  // Dependent launch: the weights are not written by the preceding kernel, so while it drains their first
-  // stages are pulled into L2; nothing that it writes, and no global memory it may still read, is touched
-  // before it has completed.
+  // Dependent launch: while the preceding kernel drains, the first stages of the weights are pulled into L2.
+  // (Also where that kernel writes them: it writes in L2, so the copies made here cannot go stale.)  No global
+  // memory is loaded or stored before it has completed.
   if (warp == 0 && lane == 0) {
     const int most = min(kb1, kb0 + p.stages);
     for (int kb = kb0; kb < most; ++kb) {
@@ -853,30 +853,10 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
   }
 }
 
-struct ClusterLaunch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  ClusterLaunch(unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t stream) {
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-  }
-};
-
-// Clusters and programmatic dependents: every kernel here waits (pdl_wait) before it touches memory that the
-// preceding kernel may use.
+// Clusters and programmatic dependents: every kernel here waits (pdl_wait) before it loads or stores.
 bsf_status launch_cluster(const void* kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
                           cudaStream_t stream, void** args) {
-  ClusterLaunch launch(grid, threads, smem, cluster, stream);
+  DependentLaunch launch(grid, threads, smem, stream, cluster);
   if (cudaLaunchKernelExC(&launch.cfg, kernel, args) != cudaSuccess) {
     cudaGetLastError();
     return BSF_ERR_CUDA;
@@ -906,8 +886,8 @@ bsf_status device_limits(const DeviceLimits** out) {
         return BSF_ERR_CUDA;
     }
     for (int i = 0; i < 4; ++i) {
-      ClusterLaunch launch(8u << i, kThreads, kSmemBytes, 1u << i, nullptr);
-      launch.cfg.numAttrs = 1;
+      DependentLaunch launch(8u << i, kThreads, kSmemBytes, nullptr, 1u << i);
+      launch.cfg.numAttrs = 1;                           // the cluster alone
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, kernels[0], &launch.cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();

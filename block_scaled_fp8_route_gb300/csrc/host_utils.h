@@ -30,28 +30,43 @@ inline bsf_status launch_status() {
   return err == cudaSuccess ? BSF_OK : BSF_ERR_CUDA;
 }
 
-// Launch `kernel` as a programmatic dependent of the preceding kernel on `stream`
-// (cudaLaunchAttributeProgrammaticStreamSerialization): its CTAs may be scheduled while
-// that kernel drains, and it must call pdl_wait() before its first global memory access.
-// Returns the launch's configuration status.
+// Launch configuration of a programmatic dependent (cudaLaunchAttributeProgrammaticStreamSerialization; an
+// ordinary launch if the library is built with BSF_DISABLE_PDL) and, if `cluster` is not 0, of clusters of that many
+// CTAs.  The kernel's CTAs may be scheduled while the preceding kernel on `stream` drains, so it must call
+// pdl_wait() before its first load from or store to global memory.  (A prefetch into L2 may come earlier: it
+// returns nothing, and what the preceding kernel still writes is written in L2.)
+struct DependentLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  DependentLaunch(dim3 grid, unsigned block, size_t smem, cudaStream_t stream, unsigned cluster = 0) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (cluster != 0) {
+      attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+      attr[cfg.numAttrs].val.clusterDim.x = cluster;
+      attr[cfg.numAttrs].val.clusterDim.y = 1;
+      attr[cfg.numAttrs].val.clusterDim.z = 1;
+      ++cfg.numAttrs;
+    }
+#ifndef BSF_DISABLE_PDL
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+#endif
+  }
+  DependentLaunch(const DependentLaunch&) = delete;        // (cfg points into attr)
+  DependentLaunch& operator=(const DependentLaunch&) = delete;
+};
+
+// Launch `kernel` as a programmatic dependent.  Returns the launch's configuration status.
 template <class... Params, class... Args>
 inline bsf_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
                                    cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-#ifdef BSF_DISABLE_PDL
-  cfg.numAttrs = 0;
-#else
-  cfg.numAttrs = 1;
-#endif
-  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...) != cudaSuccess) {
+  DependentLaunch launch(grid, block, smem, stream);
+  if (cudaLaunchKernelEx(&launch.cfg, kernel, static_cast<Args&&>(args)...) != cudaSuccess) {
     cudaGetLastError();
     return BSF_ERR_CUDA;
   }

@@ -286,7 +286,10 @@ bsf_status bsf_dispatch(const void* x, int64_t T, int64_t K, const int32_t* topk
  * device-resident weights) is launched as a programmatic dependent
  * of the preceding kernel on the stream: its CTAs may be scheduled while that
  * kernel drains, and they touch no global memory until it has completed.  So
- * are gate, swiglu_quantise and dense_gemm.
+ * are gate, swiglu_quantise and dense_gemm, except that dense_gemm may pull
+ * weights into L2 before: they may still be written by the preceding kernel,
+ * which writes in L2 too.  (Built with BSF_DISABLE_PDL, every launch is an
+ * ordinary one.)
  *
  * Tensor memory: every GEMM CTA allocates its tensor-memory columns on entry
  * (tcgen05.alloc), which waits, with no time limit, until an SM has that many
