@@ -87,7 +87,8 @@ __device__ __forceinline__ void quantise_piece(const RowPiece& p, bool active, i
   if (__low2float(most) <= kPlainGate && __high2float(most) <= kPlainGate) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = swiglu_pair(__uint_as_float((gw[i] << 16) ^ 0x80000000u), __uint_as_float((gw[i] & 0xFFFF0000u) ^ 0x80000000u),
+      v[i] = swiglu_pair(__uint_as_float((gw[i] << 16) ^ 0x80000000u),
+                         __uint_as_float((gw[i] & 0xFFFF0000u) ^ 0x80000000u),
                          pair(__uint_as_float(uw[i] << 16), __uint_as_float(uw[i] & 0xFFFF0000u)));
   } else {
     // gates so large that 1 + exp(-g) may leave the range of the reciprocal, infinities and NaN

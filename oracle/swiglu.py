@@ -37,4 +37,4 @@ def swiglu_quantise(y_bf16_bits):
     hb = padded_blocks(swiglu(y_bf16_bits))
     e = _block_exponent(np.max(np.abs(hb), axis=2))
     q = formats.e4m3_encode(np.ldexp(hb, -e[:, :, None]))
-    return q.reshape(hb.shape[0], -1), (e + 127).astype(np.uint8)
+    return q.reshape(hb.shape[0], hb.shape[1] * BLOCK), (e + 127).astype(np.uint8)
