@@ -9,8 +9,10 @@ for which that is NaN or -inf is never chosen.  Of G groups of consecutive
 experts the ``kept`` of the largest score (largest value, or sum of the two
 largest s (+ bias)) take part; the kr largest are chosen in descending order.
 Ties go to the lowest index.  Weights are s of the chosen, optionally divided
-by their sum (0 where the sum is 0), times ``scale``; missing choices are id -1
-with weight 0.
+by their sum, times ``scale``; missing choices are id -1 with weight 0.  A score
+that float64 cannot hold is 0 (and the weights divided by a sum of such sigmoid
+scores are), except in softmax weights that are divided by their sum: those are
+exp(l - l') / sum, l' the largest chosen logit.
 
 Pins: ``tests/test_oracle_gate.py`` (hand-computed rows, a sort-free brute
 force, shift invariance of the softmax, masked rows).
@@ -59,9 +61,21 @@ def group_scores(key, value, groups, top2):
     return v[:, :, -1] + np.where(np.isneginf(second), 0.0, second)
 
 
+def _cut(values, kept):
+    """Smallest difference of unequal values that decides which ``kept`` of these descending values are taken."""
+    if kept >= len(values):
+        return np.inf
+    last = values[kept - 1]
+    lower = [last - v for v in values[kept:] if v < last]
+    higher = [v - last for v in values[:kept] if v > last] if values[kept] == last else []
+    return min(lower[:1] + higher[-1:], default=np.inf)
+
+
 def gate(logits, kr, sigmoid=False, bias=None, groups=1, kept=1, top2=False, renormalise=True, scale=1.0):
     """(ids int32 [T, kr], weights float64 [T, kr], margin [T]): margin is the smallest difference, in any
-    comparison the choice rests on, of two unequal values (inf where there is none)."""
+    comparison the choice rests on, of two unequal values (inf where there is none).  Where values tie at the
+    place of the last one taken, that is also their difference to the nearest unequal ones, which less precise
+    arithmetic could add to the tie."""
     logits = np.asarray(logits, dtype=np.float64)
     T, E = logits.shape
     s, key, value = choice_keys(logits, sigmoid, bias)
@@ -71,20 +85,21 @@ def gate(logits, kr, sigmoid=False, bias=None, groups=1, kept=1, top2=False, ren
     gs = group_scores(key, value, groups, top2)
     for t in range(T):
         order = sorted(range(groups), key=lambda g: (-gs[t, g], g))
-        if kept < groups:
-            a, b = gs[t, order[kept - 1]], gs[t, order[kept]]
-            if a > b:
-                margin[t] = min(margin[t], a - b)
+        margin[t] = min(margin[t], _cut([gs[t, g] for g in order], kept))
         k = key[t].copy()
         for g in order[kept:]:
             k[g * (E // groups):(g + 1) * (E // groups)] = -np.inf
         ranked = sorted((e for e in range(E) if k[e] > -np.inf), key=lambda e: (-k[e], e))
-        for a, b in zip(ranked[:kr], ranked[1:kr + 1]):
+        for a, b in zip(ranked[:kr], ranked[1:kr]):
             if k[a] > k[b]:
                 margin[t] = min(margin[t], k[a] - k[b])
+        margin[t] = min(margin[t], _cut([k[e] for e in ranked], kr))
         for r, e in enumerate(ranked[:kr]):
             ids[t, r] = e
             w[t, r] = s[t, e]
+        if renormalise and not sigmoid and ranked:
+            l = np.minimum(logits[t, ranked[:kr]], F32_MAX)
+            w[t, :len(l)] = np.exp(l - l.max())
     if renormalise:
         total = w.sum(axis=1, keepdims=True)
         w = np.where(total > 0, w / np.where(total > 0, total, 1.0), 0.0)
