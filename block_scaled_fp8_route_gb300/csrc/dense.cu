@@ -15,7 +15,7 @@
 //   multiplies its share of the K-blocks into tensor memory, writes the FP32 partial to its own shared
 //   memory, and after a cluster barrier every CTA sums a slice of the tile's tokens over the S partials
 //   through distributed shared memory, in rank order (no atomics, no workspace, bit-identical from run
-//   to run).  Bound by latency: 1 x 4096 x 7168 takes 7.5 us, of which the 29 MB of weights need 4.3
+//   to run).  Bound by latency: 1 x 4096 x 7168 takes 7.2 us, of which the 29 MB of weights need 4.3
 //   (9.5 us where none of them is in L2).
 // * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 224 tokens with one cta_group::2 MMA per
 //   32 K: each stages 128 weight rows and half of the tokens, so a staged byte feeds twice the products

@@ -26,8 +26,12 @@ constexpr int kGateMaxGroups = 32;
 constexpr int kGateMaxKr = 32;
 constexpr int kGateWarps = 4;           // warps per CTA
 constexpr unsigned kAll = 0xffffffffu;
-// CTAs per SM: the more warps the better until the registers run out (65533 x 192: 34.7 us with 10 CTAs of
-// 48 registers, 40.9 with the 7 that 70 leave; 8192 x 256: 9.8 us with 8, 10.5 with 10, which spill).
+// CTAs per SM: the more warps the better until the registers run out (65533 x 192: 34.3 us with 10 CTAs of
+// 48 registers, 40.9 with the 7 that 70 leave; 8192 x 256: 9.9 us with 8, 10.5 with 10, which spill).  The other
+// widths, sigmoid + bias, top 8, 65536 and 8192 rows: 64 experts 24.5 and 4.7 us with 12, 24.9 and 5.5 with 8, 24.2
+// and 5.4 with 16; 384 experts 75.4 and 12.4 with 4, 83.9 and 16.0 with 3, 72.1 and 12.5 with 5; 512 experts 94.3
+// and 16.2 with 4, 103 and 20.9 with 3, 91.3 and 17.0 with 5; 1024 experts 223 and 36.9 with 2, 346 and 51.3
+// with 1 (3 would leave 168 registers: 193 and 34.9).
 constexpr int gate_ctas(int vpl) { return vpl <= 3 ? 12 : vpl <= 6 ? 10 : vpl <= 8 ? 8 : vpl <= 16 ? 4 : 2; }
 
 struct GateArgs {
@@ -160,7 +164,7 @@ __device__ __forceinline__ void sort_down(uint32_t (&c)[N]) {
 
 // What bounds it: a row is 4 E bytes, but choosing takes a fixed chain of warp operations, so short
 // batches are bound by that chain's latency (one token 2.9 us with its launch) and long ones by issue
-// slots: about 490 per token of 192 experts in 8 groups (65533 tokens in 34.7 us, 1.5 TB/s, 23 % of the
+// slots: about 484 per token of 192 experts in 8 groups (65533 tokens in 34.3 us, 1.5 TB/s, 23 % of the
 // copy rate), of which the rounds of the choice and the weights are half whatever E is.  Four lanes per
 // token with sorted lists in registers, and one thread per token, took as many slots and twice the latency.
 // * A key and its expert share one word: the key's leading bits, then the complement of the expert, so
