@@ -23,6 +23,7 @@
 //   output drain under the next tile's MMAs.  Bound by the tensor cores and, in long runs, by power:
 //   8192 x 4096 x 7168 takes 144-149 us, 3.34 PFLOP/s, 87 % of twice the measured bf16 burst rate.
 //   Tiles of up to 128 tokens are bound by MMA issue and have two issuing warps.
+#include "cluster.cuh"
 #include "common.cuh"
 #include "host_utils.h"
 #include "tma_map.h"
@@ -61,47 +62,6 @@ struct DenseArgs {
   int vec4;                  // four neighbouring columns of D (and C) are 8-byte aligned
   int* err;
 };
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// shared::cluster address of this CTA's shared-memory address in the CTA of the given rank
-__device__ __forceinline__ uint32_t map_rank(uint32_t local_smem, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local_smem), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
-}
-// Bounded wait for a copy of this thread's own: it goes on after an abort (the copy has to land before the
-// CTA exits), and says so if the limit is reached.
-__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity, int* err) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      raise_error(err, BSF_DEVERR_TIMEOUT);
-      return;
-    }
-  }
-}
-__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
-  }
-}
 
 // Tokens [j0, j1) of a tile: their S partials part[token][weight row], one in each CTA of the cluster,
 // summed in rank order and stored.  A thread takes items (token, four weight rows) and has the loads of
@@ -412,55 +372,6 @@ struct PairArgs {
   int* err;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Arrivals and waits between the CTAs of a pair that order tensor-memory accesses only: relaxed, because the
-// tcgen05 fences on both sides order those accesses.  (Release and acquire at cluster scope also
-// order all of generic memory, and cost a stage of the main loop about 100 cycles.)
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t spins = 0;
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if ((++spins & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        raise_error(err, BSF_DEVERR_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool wait_cluster_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return __all_sync(0xffffffffu, wait_cluster(bar, parity, abort, err));
-}
-// TMA box into this CTA's shared memory that completes on a barrier of either CTA of the pair.
-__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
-      "%4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
 // Executed by the whole warp, issued by the lane whose `lead` is non-zero.
 __device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate, uint32_t lead) {
@@ -472,23 +383,6 @@ __device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint6
           d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem), "r"(lead)
       : "memory");
-}
-// Arrive on the barrier at this offset in both CTAs once the MMAs issued so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3)), "r"(lead)
-      : "memory");
-}
-// One box of shared memory into a 2-D tensor (part of the calling thread's bulk group).
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(smem_u32(src))
-               : "memory");
 }
 
 // kIssuers: MMA-issuing warps, 1 or 2
@@ -851,17 +745,6 @@ __global__ void __launch_bounds__(32 * (15 + kIssuers), 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
   }
-}
-
-// Clusters and programmatic dependents: every kernel here waits (pdl_wait) before it loads or stores.
-bsf_status launch_cluster(const void* kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
-                          cudaStream_t stream, void** args) {
-  DependentLaunch launch(grid, threads, smem, stream, cluster);
-  if (cudaLaunchKernelExC(&launch.cfg, kernel, args) != cudaSuccess) {
-    cudaGetLastError();
-    return BSF_ERR_CUDA;
-  }
-  return launch_status();
 }
 
 // Once per device: both kernels may use all shared memory, and the number of CTAs of the split kernel that

@@ -73,6 +73,17 @@ inline bsf_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigne
   return launch_status();
 }
 
+// The same in clusters of `cluster` CTAs (0: none), arguments by address.
+inline bsf_status launch_cluster(const void* kernel, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                                 cudaStream_t stream, void** args) {
+  DependentLaunch launch(grid, threads, smem, stream, cluster);
+  if (cudaLaunchKernelExC(&launch.cfg, kernel, args) != cudaSuccess) {
+    cudaGetLastError();
+    return BSF_ERR_CUDA;
+  }
+  return launch_status();
+}
+
 // Per-device values the library resolves on first use are cached in atomics, so
 // first calls from several host threads at once are well defined (each stores
 // the same value).  The caches are not invalidated: after cudaDeviceReset() the
