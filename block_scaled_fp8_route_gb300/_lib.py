@@ -63,6 +63,9 @@ SIGNATURES = {
                                                _i64, _c_int, _p]),
     "bsf_gate": (_c_int, [_p, _c_int, _i64, _i64, _i64, _p, _i64, _i64, _i64, _c_int, ctypes.c_float, _p, _p, _p]),
     "bsf_swiglu_quantise": (_c_int, [_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p]),
+    "bsf_few_token_moe_workspace_bytes": (_size, [_i64, _i64, _i64, _i64]),
+    "bsf_few_token_moe": (_c_int, [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _c_int, _p, _p, _p, _p, _i64, _p, _p,
+                                   _p, _p, _p, _i64, _p, _i64, _p, _size, _c_int, _p]),
     "bsf_dense_gemm": (_c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p]),
 }
 

@@ -1,0 +1,855 @@
+// A whole mixture-of-experts layer for a few tokens (1 .. 32), sm_103a, in two kernels:
+//
+//   [g; u]_te = W13_e x_t                      for every expert e that token t chose
+//   h_te      = p_te * g / (1 + exp(-g)) * u
+//   z_t       = sum_e W2_e h_te  (+ an expert that every token takes, p = 1)  (+ addend)
+//
+// "GEMM 执行方式" (rainlin-net) §4.2-§4.4 defines routing, expert products and combine; bsf_dispatch ... bsf_combine
+// run them as separate kernels with quantised activations.  Here weights are E4M3 with 128 x 128 UE8M0 scales
+// (or bf16) and activations are not quantised.
+//
+// Such a layer is bound by the chosen experts' weights, which are read once; everything else has to hide
+// behind that stream.
+// * Work is cut into units of K-blocks, not of experts: every CTA takes the same number of boxes (128
+//   weight rows x 128 bytes, 16 KB, a contiguous run of tiled weights) whatever the routing is.  Each CTA derives
+//   routing, units and places from topk_ids itself.
+// * The first kernel multiplies gate and up rows of one 128-wide tile by the expert's tokens.  A tile whose
+//   K is shared by two or more CTAs leaves that many partial sums; nobody waits for anybody, because
+//   the second kernel adds them (in a fixed order) while it forms h.
+// * The second kernel, a programmatic dependent, is resident beside the first (half the shared memory each) and has
+//   its first weights in flight before the first one ends.  Contraction runs over (expert, i), so a cluster
+//   splits one long K and its CTAs exchange one partial of z through distributed shared memory, in rank order.
+// * FP8 weights meet unquantised activations on the FP8 tensor cores: a value scaled to its block of 128 is split
+//   into E4M3 terms, v = hi + lo / 16, which take two columns of the MMA.  A bf16 value has 8 significant bits and
+//   each term holds 4, so the split is exact down to 2**-14 of the block's largest value and off by at most
+//   2**-21 of that below; a float32 h is off by at most 2**-9 of its size or 2**-21 of the block's largest.  The weights
+//   go from HBM to the tensor core without passing a register.
+#include <cfloat>
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "host_utils.h"
+#include "quant_math.cuh"
+#include "tma_map.h"
+
+namespace bsf {
+namespace {
+
+constexpr int kMaxTokens = 32;
+constexpr int kMaxKr = 32;
+constexpr int kMaxExperts = 1024;
+constexpr int kBoxBytes = 16384;               // 128 weight rows x 128 bytes
+constexpr int kMaxStages = 6;                  // even: a stage always serves the same box of a unit
+constexpr int kMaxSlots = 4;                   // token operands in shared memory, with their scales in tensor memory
+constexpr int kSfCols = 16;                    // columns per slot: 4 + 4 of the two boxes, then the tokens' from 8 on
+constexpr int kAccCol = kMaxSlots * kSfCols;
+constexpr int kParts = 4;                      // most CTAs that share a tile of the first product
+// warps: 0 weight loads, 1 and 2 MMA issuers (one per box), 4-7 and 8-11 as each kernel needs them
+constexpr int kThreads = 384;
+constexpr int kBarBytes = 256;
+constexpr int kMostSmem = 113 * 1024;          // two CTAs per SM
+
+enum { kFp8 = 0, kBf16 = 1 };
+
+struct FewArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  const int32_t* sf;          // scale words of this kernel's routed weights [E][words][rows], and of the shared ones
+  const int32_t* sf_shared;
+  float* part;                // partial sums of the first product [kParts][R][2][I], [kParts][T][2][S]
+  float* part_shared;
+  const uint16_t* addend;
+  int64_t ldc;
+  uint16_t* z;
+  int64_t ldz;
+  int T, kr, E, R;            // R = T * kr
+  int K, I, S;
+  int nkb1;                   // K-blocks of the first product
+  int nkb2, nkb2_shared;      // of the second, per expert
+  int ctas1;                  // CTAs of the first kernel
+  int split, nbox;            // second kernel: CTAs per cluster, 128-row tiles per CTA
+  int stages, slots, slot_bytes;
+  int acc_stride;
+  uint32_t tmem_cols;
+  int tiled, withhold, vec4;
+  int* err;
+};
+
+struct Unit {                 // consecutive K-blocks of one expert (and, in the first kernel, of one tile)
+  int a, j, kb0, kb1;         // a: index of the chosen expert, the number of them for the shared one
+};
+
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// (names the registers of the loads that it completes, see tmem_wait_ld_regs)
+__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[8], uint32_t (&o)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Eight values f * scale -> E4M3 codes of their leading four bits and of 16 times what is left (exact in float32).
+__device__ __forceinline__ void split8(const float (&f)[8], float scale, uint2& hi, uint2& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = f[2 * i] * scale, b = f[2 * i + 1] * scale;
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3);
+    const float2 back = __half22float2(__half2(raw));
+    l[i] = __nv_cvt_float2_to_fp8x2(make_float2((a - back.x) * 16.f, (b - back.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// A block's exponent for split8, at least -122 so that the low term's is a scale too, and the factor 2**-e: NaN
+// where the block holds an infinity (which E4M3 lacks), as a NaN in the block is NaN without it.
+__device__ __forceinline__ int split_exponent(float amax, float& scale) {
+  const int e = max(block_exponent(amax), -122);
+  scale = amax <= FLT_MAX ? inv_pow2(e) : __uint_as_float(0x7FC00000u);
+  return e;
+}
+
+// Token operand of one K-block: row r of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint8_t* operand_at(uint8_t* slot, int row, int chunk) {
+  return slot + row * 128 + ((chunk ^ (row & 7)) << 4);
+}
+
+template <int FMT, int PHASE>
+__global__ void __launch_bounds__(kThreads, 2)
+    few_kernel(const __grid_constant__ CUtensorMap map_routed, const __grid_constant__ CUtensorMap map_shared,
+               const FewArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* slots = smem + p.stages * kBoxBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(slots + p.slots * p.slot_bytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tok_full = empty + kMaxStages;
+  uint64_t* tok_empty = tok_full + kMaxSlots;
+  uint64_t* acc_full = tok_empty + kMaxSlots;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* exps = reinterpret_cast<uint8_t*>(full) + kBarBytes;                 // [kMaxSlots][64] of the hi rows
+  int* group_cnt = reinterpret_cast<int*>(exps + kMaxSlots * 64);               // per 32 experts: chosen ones,
+  int* group_rows = group_cnt + 32;                                             // and their rows
+  uint2* chosen = reinterpret_cast<uint2*>(group_rows + 32);                    // tokens (bits); expert, first row << 16
+  float* share = reinterpret_cast<float*>(chosen + min(p.E, p.R) + 1);          // [R] p of each row
+  uint8_t* token = reinterpret_cast<uint8_t*>(share + p.R);                     // [R] token of each row
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cluster = PHASE == 2 ? static_cast<int>(blockIdx.x) / p.split : 0;
+  const int rank = PHASE == 2 ? static_cast<int>(blockIdx.x) - cluster * p.split : 0;
+  const int boxes = PHASE == 1 ? 2 : min(p.nbox, p.K / 128 - cluster * p.nbox);
+  constexpr int kConvWarps = PHASE == 1 ? 4 : 8;
+
+  if (tid == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(&tok_full[s], kConvWarps);
+      mbar_init(&tok_empty[s], boxes);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], boxes);
+      mbar_init(&acc_empty[s], 4);
+    }
+    mbar_init(done, boxes);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_routed);
+    if (p.S) tma_prefetch_desc(&map_shared);
+  }
+  // The first kernel lets the second one start once everything before both is complete, so that the second may read
+  // topk_ids, topk_weights and weights at once; only the partial sums (and z) wait for the first to end.
+  if (PHASE == 1) pdl_wait();
+  pdl_launch_dependents();
+
+  // ---------------------------------------------------------------- routing, in every CTA
+  // The stages, not yet in use, hold the tables: tokens and first row of every expert, ids and weights.
+  {
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem);
+    int* first = reinterpret_cast<int*>(mask + kMaxExperts);
+    int* ids = first + kMaxExperts;
+    float* w = reinterpret_cast<float*>(ids + kMaxTokens * kMaxKr);
+    for (int e = tid; e < p.E; e += kThreads) mask[e] = 0u;
+    __syncthreads();
+    for (int i = tid; i < p.R; i += kThreads) {
+      const int id = __ldcg(p.ids + i);
+      if (PHASE == 2) w[i] = __ldcg(p.weights + i);
+      ids[i] = id;
+      if (id >= p.E) {
+        if (PHASE == 1 && blockIdx.x == 0) raise_error(p.err, BSF_DEVERR_EXPERT_ID);
+      } else if (id >= 0) {
+        atomicOr(mask + id, 1u << (i / p.kr));
+      }
+    }
+    __syncthreads();
+    const int groups = (p.E + 31) >> 5;
+    for (int g = warp; g < groups; g += kThreads / 32) {
+      const uint32_t m = g * 32 + lane < p.E ? mask[g * 32 + lane] : 0u;
+      const int n = __reduce_add_sync(0xffffffffu, __popc(m));
+      const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
+      if (lane == 0) {
+        group_cnt[g] = __popc(some);
+        group_rows[g] = n;
+      }
+    }
+    __syncthreads();
+    for (int g = warp; g < groups; g += kThreads / 32) {
+      const int e = g * 32 + lane;
+      const uint32_t m = e < p.E ? mask[e] : 0u;
+      const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
+      int rows = __popc(m);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, rows, o);
+        if (lane >= o) rows += below;
+      }
+      rows -= __popc(m);
+      int at = __popc(some & ((1u << lane) - 1u));
+      for (int k = 0; k < g; ++k) {
+        rows += group_rows[k];
+        at += group_cnt[k];
+      }
+      if (m) {
+        chosen[at] = make_uint2(m, static_cast<uint32_t>(e) | static_cast<uint32_t>(rows) << 16);
+        first[e] = rows;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.R; i += kThreads) {
+      const int id = ids[i];
+      if (id < 0 || id >= p.E) continue;
+      const int t = i / p.kr;
+      const int row = first[id] + __popc(mask[id] & ((1u << t) - 1u));
+      token[row] = static_cast<uint8_t>(t);
+      if (PHASE == 2) {
+        // an expert named twice by a token is one row with both weights
+        float sum = 0.f;
+        bool earlier = false;
+        for (int k = t * p.kr; k < t * p.kr + p.kr; ++k) {
+          if (ids[k] != id) continue;
+          earlier |= k < i;
+          sum += w[k];
+        }
+        if (!earlier) share[row] = sum;
+      }
+    }
+  }
+  int nchosen = 0;
+  for (int g = 0; g < (p.E + 31) >> 5; ++g) nchosen += group_cnt[g];
+  const uint32_t everyone = p.T == 32 ? 0xffffffffu : (1u << p.T) - 1u;
+  if (tid == 0) chosen[nchosen] = make_uint2(everyone, 0u);
+  proxy_fence();                           // the tables' place is written by TMA next
+  __syncthreads();
+
+  const int tiles = p.I >> 7;              // 128-wide tiles of h per expert
+  int u0, u1, per = 1;                     // this CTA's K-blocks
+  {
+    const int routed = PHASE == 1 ? nchosen * tiles * p.nkb1 : nchosen * p.nkb2;
+    const int units = routed + (PHASE == 1 ? (p.S >> 7) * p.nkb1 : p.nkb2_shared);
+    const int units1 = PHASE == 1 ? units : (nchosen * tiles + (p.S >> 7)) * p.nkb1;
+    // (at least a third of a tile's K, so that at most kParts CTAs share one)
+    per = max((units1 + p.ctas1 - 1) / p.ctas1, (p.nkb1 + 2) / 3);
+    if (PHASE == 1) {
+      u0 = min(units, static_cast<int>(blockIdx.x) * per);
+      u1 = min(units, u0 + per);
+    } else {
+      u0 = static_cast<int>(static_cast<int64_t>(units) * rank / p.split);
+      u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / p.split);
+    }
+  }
+  auto unit_at = [&](int u) {
+    Unit w;
+    if (PHASE == 1) {
+      const int item = u / p.nkb1;
+      w.a = min(item / tiles, nchosen);
+      w.j = item - w.a * tiles;
+      w.kb0 = u - item * p.nkb1;
+      w.kb1 = min(p.nkb1, w.kb0 + u1 - u);
+    } else {
+      w.a = min(u / p.nkb2, nchosen);
+      w.j = 0;
+      w.kb0 = u - w.a * p.nkb2;
+      w.kb1 = min(w.a < nchosen ? p.nkb2 : p.nkb2_shared, w.kb0 + u1 - u);
+    }
+    return w;
+  };
+  // tokens padded to whole groups: rows of the hi terms (or of bf16 values), and columns of the MMA
+  auto padded = [&](int n) { return FMT == kFp8 ? (n + 7) & ~7 : (n + 15) & ~15; };
+  auto columns = [&](int n) { return FMT == kFp8 ? 2 * padded(n) : padded(n); };
+
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  // (the loads do not wait for tensor memory, which the first kernel may still hold)
+  if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  else asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+  tc_fence_after();
+  const uint32_t tmem_base = warp != 0 ? *tmem_slot : 0u;
+
+  bool have = false;                       // this warp may read the accumulators (second kernel)
+  if (warp == 0) {
+    // ------------------------------------------------------------ weight loads
+    if (lane == 0) {
+      const uint64_t once = l2_policy_evict_first();
+      uint32_t stage = 0, phase = 0;
+      int issued = 0;
+      bool ok = !p.withhold;
+      for (int u = u0; u < u1 && ok;) {
+        const Unit w = unit_at(u);
+        const bool shared = w.a == nchosen;
+        const CUtensorMap* map = shared ? &map_shared : &map_routed;
+        const int e = shared ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
+        const int width = shared ? p.S : p.I;                            // of h
+        const int row = PHASE == 1 ? e * 2 * width + w.j * 128 : e * p.K + cluster * p.nbox * 128;
+        const int step = PHASE == 1 ? width : 128;                       // rows from the first box to the second
+        const int nkb = PHASE == 1 ? p.nkb1 : shared ? p.nkb2_shared : p.nkb2;
+        for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
+          for (int b = 0; b < boxes; ++b) {
+            // (the second kernel's clock starts when the first kernel has ended)
+            if (PHASE == 2 && issued == p.stages) pdl_wait();
+            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
+            const int r = row + b * step;
+            mbar_arrive_expect_tx(&full[stage], kBoxBytes);
+            if (p.tiled)
+              tma_load_2d_hint(smem + stage * kBoxBytes, map, &full[stage], 0, r * nkb + kb * 128, once);
+            else
+              tma_load_2d_hint(smem + stage * kBoxBytes, map, &full[stage], kb * 128, r, once);
+            ++issued;
+            if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+          }
+        }
+        u += w.kb1 - w.kb0;
+      }
+      // no TMA write may be in flight when the CTA exits or reuses its stages
+      const int outstanding = issued < p.stages ? issued : p.stages;
+      for (int i = 0; i < outstanding; ++i) {
+        if (stage == 0) { stage = p.stages; phase ^= 1u; }
+        --stage;
+        wait_quiet(&full[stage], phase);
+      }
+    }
+    __syncwarp();
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers: one box of every unit each
+    const int b = warp - 1;
+    if (b < boxes && lane == 0) {
+      if (PHASE == 2) pdl_wait();
+      uint32_t stage = b, phase = 0, slot = 0, slot_phase = 0, set = 0, set_phase = 0;
+      bool ok = true, start = true;
+      for (int u = u0; u < u1 && ok;) {
+        const Unit w = unit_at(u);
+        const int n = columns(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
+        const uint32_t d = tmem_base + kAccCol + (2 * set + b) * p.acc_stride;
+        const uint32_t idesc = FMT == kFp8 ? idesc_mxf8_e4m3(128, n, 0, 0) : idesc_bf16(128, n);
+        if (PHASE == 1) {
+          start = true;
+          if (!mbar_wait(&acc_empty[set], set_phase ^ 1u, abort_flag, p.err)) break;
+        }
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(&tok_full[slot], slot_phase, abort_flag, p.err) ||
+              !mbar_wait(&full[stage], phase, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t adesc = smem_desc_k_sw128(smem_u32(smem + stage * kBoxBytes));
+          const uint64_t bdesc = smem_desc_k_sw128(smem_u32(slots + slot * p.slot_bytes));
+          const uint32_t sf = tmem_base + slot * kSfCols;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (FMT == kFp8)
+              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, sf + 4 * b, sf + 8, !start || k != 0);
+            else
+              mma_bf16(d, adesc + 2 * k, bdesc + 2 * k, idesc, !start || k != 0);
+          }
+          start = false;
+          tc_commit(&empty[stage]);
+          tc_commit(&tok_empty[slot]);
+          stage += boxes;                  // (an even number of stages: each stage keeps its issuer)
+          if (stage >= static_cast<uint32_t>(p.stages)) { stage -= p.stages; phase ^= 1u; }
+          if (++slot == static_cast<uint32_t>(p.slots)) { slot = 0; slot_phase ^= 1u; }
+        }
+        u += w.kb1 - w.kb0;
+        if (PHASE == 1 && ok) {
+          tc_commit(&acc_full[set]);
+          if (++set == 2) { set = 0; set_phase ^= 1u; }
+        }
+      }
+      if (PHASE == 2 && ok) tc_commit(&acc_full[0]);
+      // on every way out: tensor memory is released only after the issued MMAs are done
+      tc_commit(done);
+      wait_quiet(done, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 4 + kConvWarps) {
+    // ------------------------------------------------------------ token operands and scales of every K-block
+    constexpr int kLanes = FMT == kFp8 ? 16 : 8;             // lanes of eight values per token
+    constexpr int kPerRound = 32 * kConvWarps / kLanes;      // tokens at once
+    const int ct = tid - 128, sub = ct & (kLanes - 1), mine = ct / kLanes;
+    const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    uint32_t slot = 0, slot_phase = 0;
+    bool ok = true;
+    // the scale byte of a box: one word per row, but the same for the 128 rows of a block
+    auto scale_word = [&](const Unit& w, int kb, int b) -> uint32_t {
+      if (FMT != kFp8 || b >= boxes) return 0u;
+      const bool sh = w.a == nchosen;
+      const int width = sh ? p.S : p.I, e = sh ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
+      const int rows = PHASE == 1 ? 2 * width : p.K, inner = PHASE == 1 ? p.K : width;
+      const int row = PHASE == 1 ? b * width + w.j * 128 : (cluster * p.nbox + b) * 128;
+      const int64_t at = (static_cast<int64_t>(e) * ((inner + 511) >> 9) + (kb >> 2)) * rows + row;
+      return static_cast<uint32_t>(__ldg((sh ? p.sf_shared : p.sf) + at));
+    };
+    // eight values of token row `row` of the slot
+    auto store8 = [&](const float (&f)[8], int row, int hi_rows) {
+      uint8_t* to = slots + slot * p.slot_bytes;
+      if (FMT == kFp8) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float scale;
+        const int e = split_exponent(amax, scale);
+        uint2 hi, lo;
+        split8(f, scale, hi, lo);
+        if (row < hi_rows) {
+          *reinterpret_cast<uint2*>(operand_at(to, row, sub >> 1) + (sub & 1) * 8) = hi;
+          *reinterpret_cast<uint2*>(operand_at(to, hi_rows + row, sub >> 1) + (sub & 1) * 8) = lo;
+          if (sub == 0) exps[slot * 64 + row] = static_cast<uint8_t>(e + 127);
+        }
+      } else if (row < hi_rows) {
+        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      }
+    };
+    // hands the slot over once all warps have written it; false if one of them gave up
+    auto publish = [&](int hi_rows, uint32_t word0, uint32_t word1, int kb) -> bool {
+      proxy_fence();
+      if (FMT == kFp8) {
+        if (named_barrier_or(2, 32 * kConvWarps, !ok)) return false;
+        if (warp < 8) {
+          const uint32_t w0 = (word0 >> (8 * (kb & 3))) & 255u, w1 = (word1 >> (8 * (kb & 3))) & 255u;
+          const uint32_t sf = quad + slot * kSfCols;
+          const uint32_t w[8] = {w0, w0, w0, w0, w1, w1, w1, w1};
+          tmem_st_x8(sf, w);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = lane + 32 * c;
+            if (32 * c < 2 * hi_rows)
+              tmem_st_x1(sf + 8 + c, r < hi_rows ? exps[slot * 64 + r] : r < 2 * hi_rows ? exps[slot * 64 + r - hi_rows] - 4 : 127);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+      } else if (!ok) {
+        return false;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tok_full[slot]);
+      if (++slot == static_cast<uint32_t>(p.slots)) { slot = 0; slot_phase ^= 1u; }
+      return true;
+    };
+
+    if (PHASE == 1) {
+      // x, one load ahead: the next round's values (and scale words) are in flight while this one's are split
+      struct At {
+        Unit w;
+        int u, kb, round, n;
+      };
+      auto begin = [&](int u) {
+        At a;
+        a.u = u;
+        a.w = unit_at(min(u, max(u1 - 1, 0)));
+        a.kb = a.w.kb0;
+        a.round = 0;
+        a.n = __popc(chosen[a.w.a].x);
+        return a;
+      };
+      uint4 next = {};
+      uint32_t next0 = 0, next1 = 0;
+      auto load = [&](const At& a) {
+        const int j = a.round * kPerRound + mine;
+        next = make_uint4(0, 0, 0, 0);
+        if (j < a.n) {
+          const int t = a.w.a == nchosen ? j : token[(chosen[a.w.a].y >> 16) + j];
+          next = __ldg(reinterpret_cast<const uint4*>(p.x + t * p.ldx + a.kb * (kLanes * 8) + sub * 8));
+        }
+        if (a.round == 0) {
+          next0 = scale_word(a.w, a.kb, 0);
+          next1 = scale_word(a.w, a.kb, 1);
+        }
+      };
+      At at = begin(u0);
+      if (u0 < u1) load(at);
+      uint32_t word0 = 0, word1 = 0;
+      while (at.u < u1) {
+        const uint4 v = next;
+        const At now = at;
+        const int hi_rows = padded(now.n);
+        if (now.round == 0) {
+          word0 = next0;
+          word1 = next1;
+        }
+        const bool last = (now.round + 1) * kPerRound >= hi_rows;
+        if (!last) {
+          ++at.round;
+        } else {
+          at.round = 0;
+          ++at.u;
+          if (++at.kb == now.w.kb1) at = begin(at.u);
+        }
+        if (at.u < u1) load(at);
+        if (now.round == 0)
+          ok = wait_all(&tok_empty[slot], slot_phase ^ 1u, abort_flag, p.err);
+        float f[8];
+        bf16x8_to_float(v, f);
+        if (ok) store8(f, now.round * kPerRound + mine, hi_rows);
+        if (last && !publish(hi_rows, word0, word1, now.kb)) break;
+      }
+    } else {
+      // h from the first kernel's partial sums, at most kParts of each value, added in the order of the CTAs
+      pdl_wait();
+      const int hi_rows = padded(p.T);
+      for (int u = u0; u < u1 && ok;) {
+        const Unit w = unit_at(u);
+        const bool sh = w.a == nchosen;
+        const uint2 who = chosen[w.a];
+        const int width = sh ? p.S : p.I;
+        const int64_t part_step = static_cast<int64_t>(sh ? p.T : p.R) * 2 * width;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          const uint32_t word0 = scale_word(w, kb, 0), word1 = scale_word(w, kb, 1);
+          const int i = kb * (kLanes * 8) + sub * 8;                     // of h
+          const int item = w.a * tiles + (i >> 7);
+          const int parts = ((item + 1) * p.nkb1 - 1) / per - item * p.nkb1 / per + 1;
+          bool waited = false;
+          for (int base = 0; base < hi_rows; base += kPerRound) {
+            const int t = base + mine;
+            float f[8] = {};
+            if (t < p.T && (who.x >> t & 1u)) {
+              const int row = sh ? t : static_cast<int>(who.y >> 16) + __popc(who.x & ((1u << t) - 1u));
+              const float* at = (sh ? p.part_shared : p.part) + static_cast<int64_t>(row) * 2 * width + i;
+              float g[8] = {}, v[8] = {};
+#pragma unroll
+              for (int s = 0; s < kParts; ++s) {
+                if (s >= parts) break;
+                const float4 g0 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step));
+                const float4 g1 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step) + 1);
+                const float4 v0 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step + width));
+                const float4 v1 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step + width) + 1);
+                g[0] += g0.x, g[1] += g0.y, g[2] += g0.z, g[3] += g0.w, g[4] += g1.x, g[5] += g1.y, g[6] += g1.z, g[7] += g1.w;
+                v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w, v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
+              }
+              const float weight = sh ? 1.f : share[row];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[k] = __fdividef(g[k], 1.f + expf(-g[k])) * v[k] * weight;
+            }
+            if (!waited) ok = wait_all(&tok_empty[slot], slot_phase ^ 1u, abort_flag, p.err);
+            waited = true;
+            if (ok) store8(f, t, hi_rows);
+          }
+          if (!publish(hi_rows, word0, word1, kb)) { ok = false; break; }
+        }
+        u += w.kb1 - w.kb0;
+      }
+    }
+  } else if (PHASE == 1 && warp >= 8) {
+    // ------------------------------------------------------------ first kernel's sums: lane = row of the tile
+    const int q = warp & 3;
+    uint32_t set = 0, set_phase = 0;
+    bool ok = true;
+    for (int u = u0; u < u1;) {
+      const Unit w = unit_at(u);
+      const bool sh = w.a == nchosen;
+      const uint2 who = chosen[w.a];
+      const int n = __popc(who.x), hi_rows = padded(n);
+      const int width = sh ? p.S : p.I;
+      const int part = static_cast<int>(blockIdx.x) - (w.a * tiles + w.j) * p.nkb1 / per;
+      const int64_t row0 = static_cast<int64_t>(part) * (sh ? p.T : p.R) + (who.y >> 16);
+      float* to = (sh ? p.part_shared : p.part) + row0 * 2 * width + w.j * 128 + 32 * q + lane;
+      ok = ok && wait_all(&acc_full[set], set_phase, abort_flag, p.err);
+      tc_fence_after();
+      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 2 * set * p.acc_stride;
+      for (int b = 0; b < 2; ++b) {
+        for (int c = 0; c < hi_rows; c += 8) {
+          uint32_t r[8], o[8];
+          tmem_ld_x8(acc + b * p.acc_stride + c, r);
+          tmem_ld_x8(acc + b * p.acc_stride + (FMT == kFp8 ? hi_rows : 0) + c, o);
+          tmem_wait_ld_regs(r, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v = __uint_as_float(r[k]);
+            if (FMT == kFp8) v += __uint_as_float(o[k]);
+            // (where a wait ran out the sums are marked, so that z cannot look like an answer)
+            if (c + k < n) to[(static_cast<int64_t>(c + k) * 2 + b) * width] = ok ? v : __uint_as_float(0x7FC00000u);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[set]);
+      if (++set == 2) { set = 0; set_phase ^= 1u; }
+      u += w.kb1 - w.kb0;
+    }
+  }
+
+  if (PHASE == 1) {
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc(tmem_base, p.tmem_cols);
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- z: partials to shared memory, sum over the cluster
+  pdl_wait();                              // (every thread, before it stores)
+  float* sums = reinterpret_cast<float*>(smem);              // [T][boxes][128], in place of the consumed stages
+  if (warp >= 4) {
+    have = wait_all(&acc_full[0], 0, abort_flag, p.err) && *abort_flag == 0;
+    have = __all_sync(0xffffffffu, have);
+    tc_fence_after();
+    if (!have) {
+      // a wait that ran out anywhere in this CTA keeps all of its cluster from storing
+      if (lane == 0)
+        for (int s = 0; s < p.split; ++s) st_cluster_u32(map_rank(smem_u32(const_cast<int*>(abort_flag)), s), 1u);
+      __syncwarp();
+    } else if (const int b = (warp - 4) >> 2; b < boxes) {
+      const int q = warp & 3, hi_rows = padded(p.T);
+      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + b * p.acc_stride;
+      for (int c = 0; c < hi_rows; c += 8) {
+        uint32_t r[8], o[8];
+        tmem_ld_x8(acc + c, r);
+        tmem_ld_x8(acc + (FMT == kFp8 ? hi_rows : 0) + c, o);
+        tmem_wait_ld_regs(r, o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float v = __uint_as_float(r[k]);
+          if (FMT == kFp8) v += __uint_as_float(o[k]);
+          if (c + k < p.T) sums[((c + k) * boxes + b) * 128 + 32 * q + lane] = u0 < u1 ? v : 0.f;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+  if (*abort_flag == 0) {
+    const int quads = p.T * boxes * 32;                      // groups of four neighbouring values of z
+    const int i1 = quads * (rank + 1) / p.split;
+    const uint32_t mine = smem_u32(sums);
+    for (int i = quads * rank / p.split + tid; i < i1; i += kThreads) {
+      float4 v[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < p.split) v[s] = ld_cluster_f4(map_rank(mine, s) + i * 16);
+      float4 f = v[0];
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < p.split) f.x += v[s].x, f.y += v[s].y, f.z += v[s].z, f.w += v[s].w;
+      const int t = i / (boxes * 32), n = cluster * p.nbox * 128 + (i - t * boxes * 32) * 4;
+      if (p.vec4) {
+        if (p.addend) {
+          const uint2 c = *reinterpret_cast<const uint2*>(p.addend + t * p.ldc + n);
+          f.x += __uint_as_float(c.x << 16);
+          f.y += __uint_as_float(c.x & 0xFFFF0000u);
+          f.z += __uint_as_float(c.y << 16);
+          f.w += __uint_as_float(c.y & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(p.z + t * p.ldz + n) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+      } else {
+        const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float c = p.addend ? __uint_as_float(static_cast<uint32_t>(p.addend[t * p.ldc + n + k]) << 16) : 0.f;
+          p.z[t * p.ldz + n + k] = static_cast<uint16_t>(pack_bf16x2(e[k] + c, 0.f) & 0xFFFFu);
+        }
+      }
+    }
+  }
+  // a CTA's shared memory stays until every CTA of the cluster has read it
+  cluster_sync();
+}
+
+template <int FMT>
+bsf_status few_attributes() {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BSF_ERR_CUDA;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    const void* kernels[2] = {reinterpret_cast<const void*>(few_kernel<FMT, 1>),
+                              reinterpret_cast<const void*>(few_kernel<FMT, 2>)};
+    for (const void* k : kernels) {
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess ||
+          cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+              cudaSuccess)
+        return BSF_ERR_CUDA;
+    }
+    ready[dev].store(true, std::memory_order_release);
+  }
+  return BSF_OK;
+}
+
+uint32_t columns_of(int cols) { return cols <= 128 ? 128 : cols <= 256 ? 256 : 512; }
+
+int64_t part_floats(int64_t rows, int64_t width) { return kParts * rows * 2 * width; }
+
+bool few_sizes(int64_t T, int64_t kr, int64_t I, int64_t S) {
+  return T >= 0 && T <= kMaxTokens && kr >= 1 && kr <= kMaxKr && I >= 1 && I <= kMaxRowWidth && S >= 0 && S <= kMaxRowWidth;
+}
+
+// 16 KB boxes of weights [rows, inner bytes]
+bool make_weight_map(CUtensorMap* map, const void* w, int64_t rows, int64_t bytes, bool tiled) {
+  return tiled ? make_map(map, w, rows * (bytes / 128), 128, 128) : make_map(map, w, rows, bytes, 128);
+}
+
+template <int FMT>
+bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const void* w2, const int32_t* sf2,
+                      const void* w13_shared, const int32_t* sf13_shared, const void* w2_shared,
+                      const int32_t* sf2_shared, cudaStream_t s) {
+  const bsf_status st = few_attributes<FMT>();
+  if (st != BSF_OK) return st;
+  constexpr int kSize = FMT == kFp8 ? 1 : 2;
+  const int sms = sm_count();
+  a.nkb1 = a.K * kSize / 128;
+  a.nkb2 = a.I * kSize / 128;
+  a.nkb2_shared = a.S * kSize / 128;
+  a.ctas1 = sms;
+  const int rows = FMT == kFp8 ? 2 * ((a.T + 7) / 8 * 8) : (a.T + 15) / 16 * 16;
+  a.slot_bytes = (rows * 128 + 1023) / 1024 * 1024;
+  a.acc_stride = (rows + 31) / 32 * 32;
+  const int tables = (((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5 + 15) / 16 * 16;
+  const int fixed = 1024 + kBarBytes + kMaxSlots * 64 + 256 + tables;
+  a.slots = a.slot_bytes <= 2048 ? kMaxSlots : 3;
+  a.stages = (kMostSmem - fixed - a.slots * a.slot_bytes) / kBoxBytes;
+  a.stages = a.stages >= kMaxStages ? kMaxStages : a.stages / 2 * 2;
+  const size_t smem = fixed + a.slots * a.slot_bytes + a.stages * kBoxBytes;
+
+  // The second kernel: a CTA takes two 128-row tiles of W2 where that leaves enough CTAs to keep HBM busy (the token
+  // operand is formed once for both), a cluster as much of the contraction's split as it can.
+  const int tiles = a.K / 128;
+  a.nbox = (tiles + 1) / 2 * 8 >= 7 * sms / 10 ? 2 : 1;
+  const int clusters = (tiles + a.nbox - 1) / a.nbox;
+  const int64_t most = static_cast<int64_t>(a.E < a.R ? a.E : a.R) * a.nkb2 + a.nkb2_shared;   // K-blocks
+  a.split = 2 * sms / clusters;
+  if (a.split > 8) a.split = 8;
+  if (a.split > most) a.split = static_cast<int>(most);
+  if (a.split < 1) a.split = 1;
+
+  CUtensorMap m13, m2, s13, s2;
+  if (!make_weight_map(&m13, w13, static_cast<int64_t>(a.E) * 2 * a.I, static_cast<int64_t>(a.K) * kSize, a.tiled) ||
+      !make_weight_map(&m2, w2, static_cast<int64_t>(a.E) * a.K, static_cast<int64_t>(a.I) * kSize, a.tiled))
+    return BSF_ERR_CUDA;
+  s13 = m13;
+  s2 = m2;
+  if (a.S && (!make_weight_map(&s13, w13_shared, 2 * static_cast<int64_t>(a.S), static_cast<int64_t>(a.K) * kSize, a.tiled) ||
+              !make_weight_map(&s2, w2_shared, a.K, static_cast<int64_t>(a.S) * kSize, a.tiled)))
+    return BSF_ERR_CUDA;
+
+  a.sf = sf13;
+  a.sf_shared = sf13_shared;
+  a.tmem_cols = columns_of(kAccCol + 4 * a.acc_stride);
+  void* args1[] = {&m13, &s13, &a};
+  const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, smem, 0, s, args1);
+  if (first != BSF_OK) return first;
+  FewArgs b = a;
+  b.sf = sf2;
+  b.sf_shared = sf2_shared;
+  b.tmem_cols = columns_of(kAccCol + 2 * a.acc_stride);
+  void* args2[] = {&m2, &s2, &b};
+  return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, smem, b.split, s, args2);
+}
+
+}  // namespace
+}  // namespace bsf
+
+using namespace bsf;
+
+extern "C" size_t bsf_few_token_moe_workspace_bytes(int64_t T, int64_t kr, int64_t I, int64_t S) {
+  if (!few_sizes(T, kr, I, S)) return 0;
+  return static_cast<size_t>(part_floats(T * kr, I) + part_floats(T, S)) * 4 + 16;
+}
+
+extern "C" bsf_status bsf_few_token_moe(const void* x, int64_t T, int64_t K, int64_t ldx, const int32_t* topk_ids,
+                                        const float* topk_weights, int64_t kr, int64_t E, int64_t I, int weight_type,
+                                        const void* w13, const int32_t* sfb13, const void* w2, const int32_t* sfb2,
+                                        int64_t S, const void* w13_shared, const int32_t* sfb13_shared,
+                                        const void* w2_shared, const int32_t* sfb2_shared, const void* addend,
+                                        int64_t ldc, void* z, int64_t ldz, void* workspace, size_t workspace_bytes,
+                                        int flags, bsf_stream_t stream) {
+  if (T < 0 || K <= 0 || kr <= 0 || E <= 0 || I <= 0 || S < 0) return BSF_ERR_INVALID_ARGUMENT;
+  if (K % 128 || I % 128 || S % 128) return BSF_ERR_INVALID_ARGUMENT;
+  if (weight_type != BSF_TYPE_E4M3 && weight_type != BSF_TYPE_BF16) return BSF_ERR_INVALID_ARGUMENT;
+  if (flags & ~(BSF_B_TILED | BSF_DEBUG_WITHHOLD_LOADS)) return BSF_ERR_INVALID_ARGUMENT;
+  if (T > kMaxTokens || kr > kMaxKr || E > kMaxExperts || K > kMaxRowWidth / 2 || !few_sizes(T, kr, I, S))
+    return BSF_ERR_UNSUPPORTED;
+  if (T == 0) return BSF_OK;
+  const bool fp8 = weight_type == BSF_TYPE_E4M3;
+  if (!x || !topk_ids || !topk_weights || !w13 || !w2 || !z || !workspace) return BSF_ERR_INVALID_ARGUMENT;
+  if (fp8 && (!sfb13 || !sfb2)) return BSF_ERR_INVALID_ARGUMENT;
+  if (S && (!w13_shared || !w2_shared || (fp8 && (!sfb13_shared || !sfb2_shared)))) return BSF_ERR_INVALID_ARGUMENT;
+  if (ldx < K || ldz < K || (addend && ldc < K)) return BSF_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < bsf_few_token_moe_workspace_bytes(T, kr, I, S)) return BSF_ERR_INVALID_ARGUMENT;
+  if (!aligned16(x) || ldx % 8 || !aligned16(w13) || !aligned16(w2) || !aligned16(workspace) ||
+      (S && (!aligned16(w13_shared) || !aligned16(w2_shared))))
+    return BSF_ERR_MISALIGNED;
+  for (const void* q : {static_cast<const void*>(topk_ids), static_cast<const void*>(topk_weights),
+                        static_cast<const void*>(sfb13), static_cast<const void*>(sfb2),
+                        static_cast<const void*>(sfb13_shared), static_cast<const void*>(sfb2_shared)})
+    if (reinterpret_cast<uintptr_t>(q) & 3) return BSF_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(z) & 1) || (reinterpret_cast<uintptr_t>(addend) & 1)) return BSF_ERR_MISALIGNED;
+  if (ldx > kMaxRowWidth || ldz > kMaxRowWidth || (addend && ldc > kMaxRowWidth)) return BSF_ERR_UNSUPPORTED;
+  // weight rows x K-blocks are the boxes' coordinates, K-blocks over all CTAs the units: both 32-bit
+  const int64_t per_k = (fp8 ? K : 2 * K) / 128;
+  if (!fits_weights(E, 2 * I, 2 * K) || E * I + S > kMaxRows || 2 * (E * I + S) * per_k > INT32_MAX / 2)
+    return BSF_ERR_UNSUPPORTED;
+  FewArgs a = {};
+  a.err = device_error_ptr();
+  if (!a.err) return BSF_ERR_CUDA;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.part = static_cast<float*>(workspace);
+  a.part_shared = a.part + part_floats(T * kr, I);
+  a.addend = static_cast<const uint16_t*>(addend);
+  a.ldc = ldc;
+  a.z = static_cast<uint16_t*>(z);
+  a.ldz = ldz;
+  a.T = static_cast<int>(T);
+  a.kr = static_cast<int>(kr);
+  a.E = static_cast<int>(E);
+  a.R = static_cast<int>(T * kr);
+  a.K = static_cast<int>(K);
+  a.I = static_cast<int>(I);
+  a.S = static_cast<int>(S);
+  a.tiled = (flags & BSF_B_TILED) != 0;
+  a.withhold = (flags & BSF_DEBUG_WITHHOLD_LOADS) != 0;
+  a.vec4 = (reinterpret_cast<uintptr_t>(z) & 7) == 0 && ldz % 4 == 0 &&
+           (!addend || ((reinterpret_cast<uintptr_t>(addend) & 7) == 0 && ldc % 4 == 0));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return fp8 ? launch_few<kFp8>(a, w13, sfb13, w2, sfb2, w13_shared, sfb13_shared, w2_shared, sfb2_shared, s)
+             : launch_few<kBf16>(a, w13, sfb13, w2, sfb2, w13_shared, sfb13_shared, w2_shared, sfb2_shared, s);
+}

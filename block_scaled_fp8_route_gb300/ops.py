@@ -430,6 +430,7 @@ GATE_SIGMOID = 0x1
 GATE_GROUP_TOP2 = 0x2
 GATE_RENORMALISE = 0x4
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}       # BSF_TYPE_F32, BSF_TYPE_BF16
+TYPE_E4M3 = 2
 _SCORES = {"softmax": 0, "sigmoid": GATE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": GATE_GROUP_TOP2}
 
@@ -641,3 +642,103 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
     if status:
         _lib.check(status, "dense_gemm")
     return d
+
+
+def few_token_moe_workspace(T, kr, I, S=0, device="cuda"):
+    """Workspace of ``few_token_moe`` for these sizes (or smaller ones).  Calls that may overlap, on different
+    streams or in graphs that may run at the same time, need one each."""
+    n = _lib.load().bsf_few_token_moe_workspace_bytes(T, kr, I, S)
+    if n == 0:
+        raise ValueError(f"few_token_moe: expected T and kr of at most 32, got T = {T}, kr = {kr}, I = {I}, S = {S}")
+    return torch.empty(n, dtype=_U8, device=device)
+
+
+def _few_weights(w, sf, E, rows, inner, kind, what):
+    """Check one weight tensor (and its scale words) of ``few_token_moe``."""
+    shape = (rows, inner) if E is None else (E, rows, inner)
+    if kind == _BF16 and w.dtype == _U8:         # tile_weights gives bytes
+        shape = shape[:-1] + (2 * inner,)
+    elif w.dtype != kind:
+        _refuse(w, kind, None, what)
+    if w.shape != shape or not w.is_contiguous():
+        _refuse(w, w.dtype, shape, what)
+    if kind == _U8:
+        words = ((inner + 511) // 512, rows)
+        words = words if E is None else (E,) + words
+        if sf is None or sf.dtype != _I32 or sf.shape != words or not sf.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous int32 scale words of shape {words}, got "
+                             f"{None if sf is None else (sf.dtype, tuple(sf.shape))}")
+    elif sf is not None:
+        raise ValueError(f"{what}: bfloat16 weights have no scale words")
+
+
+def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, addend=None, z=None, workspace=None,
+                  flags=B_TILED, stream=None):
+    """A whole MoE layer for T <= 32 tokens in two kernels: x bf16 [T, K] (row stride a multiple of 8), topk_ids int32
+    and topk_weights float32 [T, kr] (``gate``; an id < 0 takes no expert) -> z bf16 [T, K] =
+    sum_k weight_k * W2_e (silu(gate_e x) * (up_e x)) (+ the shared expert's) (+ ``addend`` bf16 [T, K]).
+
+    Weights: w13 uint8 [E, 2 I, K] with sfb13, w2 uint8 [E, K, I] with sfb2 (``quantise_weight`` ->
+    ``prepare_weight_sf``, ``tile_weights``), or bf16 of these shapes (with ``B_TILED`` the bytes that
+    ``tile_weights`` gives) and None for both scales.  ``shared`` = (w13 [2 S, K], sfb13, w2 [K, S], sfb2) of an
+    expert that every token takes.  x is not quantised.  ``workspace`` from ``few_token_moe_workspace``, used by this
+    call alone until it is done (default: a new one)."""
+    T, K = _two_dims(x, "x")
+    if x.dtype != _BF16:
+        _refuse(x, _BF16, None, "x")
+    ldx = _row_stride(x, T, K, "x")
+    if w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError(f"expected w13 [E, 2 I, K] and w2 [E, K, I], got {tuple(w13.shape)} and {tuple(w2.shape)}")
+    E, I = w13.shape[0], w13.shape[1] // 2
+    kind = _BF16 if sfb13 is None else _U8
+    _few_weights(w13, sfb13, E, 2 * I, K, kind, "w13")
+    _few_weights(w2, sfb2, E, K, I, kind, "w2")
+    b13 = f13 = b2 = f2 = None
+    S = 0
+    if shared is not None:
+        b13, f13, b2, f2 = shared
+        if b13.dim() != 2 or b2.dim() != 2:
+            raise ValueError(f"shared: expected w13 [2 S, K] and w2 [K, S], got {tuple(b13.shape)} and {tuple(b2.shape)}")
+        S = b13.shape[0] // 2
+        _few_weights(b13, f13, None, 2 * S, K, kind, "shared w13")
+        _few_weights(b2, f2, None, K, S, kind, "shared w2")
+    if K % 128 or I % 128 or S % 128:
+        raise ValueError(f"expected K, I and S to be multiples of 128, got {K}, {I} and {S}")
+    kr = topk_ids.shape[-1]
+    if topk_ids.dtype != _I32 or topk_ids.shape != (T, kr) or not topk_ids.is_contiguous():
+        _refuse(topk_ids, _I32, (T, kr), "topk_ids")
+    if topk_weights.dtype != _F32 or topk_weights.shape != (T, kr) or not topk_weights.is_contiguous():
+        _refuse(topk_weights, _F32, (T, kr), "topk_weights")
+    out = (T, K)
+    if z is None:
+        z = _empty(out, _BF16, x, stream)
+    elif z.dtype != _BF16 or z.shape != out:
+        _refuse(z, _BF16, out, "z")
+    ldz = _row_stride(z, T, K, "z")
+    ldc = 0
+    if addend is not None:
+        if addend.dtype != _BF16 or addend.shape != out:
+            _refuse(addend, _BF16, out, "addend")
+        ldc = _row_stride(addend, T, K, "addend")
+    need = _lib.load().bsf_few_token_moe_workspace_bytes(T, kr, I, S)
+    if workspace is None:
+        workspace = _empty((max(need, 16),), _U8, x, stream)
+    elif workspace.dtype != _U8 or workspace.dim() != 1 or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace: expected at least {need} contiguous bytes, got {workspace.dtype} "
+                         f"{tuple(workspace.shape)}")
+    operands = (x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace)
+    device = x.get_device()
+    if (device < 0 or device != _current_device() or (stream is not None and stream.device_index != device)
+            or any(t is not None and t.get_device() != device for t in operands)):
+        _refuse_devices("x topk_ids topk_weights w13 sfb13 w2 sfb2 shared_w13 shared_sfb13 shared_w2 shared_sfb2 "
+                        "addend z workspace", operands, stream)
+    if stream is not None:
+        _used_on(stream, *operands)
+    at = [None if t is None else t.data_ptr() for t in operands]
+    status = _lib.load().bsf_few_token_moe(
+        at[0], T, K, ldx, at[1], at[2], kr, E, I, _TYPES[_BF16] if kind == _BF16 else TYPE_E4M3, at[3], at[4], at[5],
+        at[6], S, at[7], at[8], at[9], at[10], at[11], ldc, at[12], ldz, at[13], workspace.numel(), flags,
+        _current_stream(device) if stream is None else stream.cuda_stream)
+    if status:
+        _lib.check(status, "few_token_moe")
+    return z

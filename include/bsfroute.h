@@ -538,6 +538,7 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
 /* Element types of an argument that takes more than one. */
 #define BSF_TYPE_F32 0
 #define BSF_TYPE_BF16 1
+#define BSF_TYPE_E4M3 2
 
 /* bsf_gate flags. */
 #define BSF_GATE_SIGMOID 0x1     /* score = sigmoid(logit); otherwise softmax over the usable experts */
@@ -623,6 +624,54 @@ bsf_status bsf_swiglu_quantise(const void* y, int64_t T, int64_t K, int64_t ld, 
 bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, int64_t M, const uint8_t* b,
                           const int32_t* sfb, int64_t N, int64_t K, const void* addend, int64_t ldc, void* d,
                           int64_t ldd, int flags, bsf_stream_t stream);
+
+/*
+ * bsf_few_token_moe — a whole MoE layer for at most 32 tokens, from the chosen
+ * experts to the layer's output ("GEMM 执行方式" §4.2-§4.4), in two kernels:
+ *   z_t = BF16( sum_k topk_weights[t, k] * W2_e h_te  (+ shared) (+ addend) ),
+ *   h_te = silu(W13_e[gate rows] x_t) * (W13_e[up rows] x_t),  e = topk_ids[t, k]
+ * Weights are quantised, activations are not: x enters as bf16 and nothing in
+ * between is rounded to bf16 or FP8 as a whole.  (bsf_dispatch ... bsf_combine
+ * quantise x and h, so the two forms agree within FP8's error, not in bits.)
+ *   x             bf16 [T, K], row stride ldx >= K elements, ldx % 8 == 0.
+ *   topk_ids      int32 [T, kr]; a negative id takes no expert (a row of them
+ *                 gives zero, or the shared expert and the addend alone); ids >= E set
+ *                 BSF_DEVERR_EXPERT_ID and take none.  An expert that a token
+ *                 names twice counts with both weights.
+ *   topk_weights  fp32 [T, kr].
+ *   weight_type   BSF_TYPE_E4M3: w13 e4m3 [E, 2 I, K] (gate rows, then up
+ *                 rows), sfb13 int32 [E][ceil(K/512)][2 I], w2 e4m3 [E, K, I],
+ *                 sfb2 int32 [E][ceil(I/512)][K], as from bsf_quantise_weight
+ *                 and bsf_prepare_weight_sf: one scale per 128 x 128 block.
+ *                 BSF_TYPE_BF16: bf16 of the same shapes, no scales.
+ *   S, *_shared   an expert that every token takes with weight 1: the same
+ *                 with E = 1 and S in place of I; S == 0: none.
+ *   addend        bf16 [T, K], row stride ldc >= K, or NULL: added before the
+ *                 one rounding (for instance the residual stream).  It may be z.
+ *   z             bf16 [T, K], row stride ldz >= K (output).
+ *   workspace     bsf_few_token_moe_workspace_bytes() bytes, 16-byte aligned,
+ *                 any contents; used from the call's start on its stream to its
+ *                 end there, so calls that may overlap need one each.
+ * FP32 accumulation on the tensor cores; an E4M3 weight meets x as two E4M3
+ * terms, exact for values within 2^-14 of the largest of their 128 and off by
+ * at most 2^-21 of that largest below (h: also 2^-9 of its own size; bf16
+ * weights: h is rounded to bf16).  The weight topk_weights enters before that.  The order
+ * of all sums is fixed: results are bit-identical from run to run.  An infinity
+ * or NaN in x gives NaN in that token's z.
+ * T <= 32, kr <= 32, E <= 1024 (else BSF_ERR_UNSUPPORTED); K, I and S
+ * multiples of 128; 16-byte aligned x and weights; z and addend need only their element
+ * alignment (8 bytes and row strides of 4 elements are faster).  flags:
+ * BSF_B_TILED (all weights through bsf_tile_weights), BSF_DEBUG_WITHHOLD_LOADS.
+ * T == 0 is a no-op.  Asynchronous on stream.  A wait that runs out sets
+ * BSF_DEVERR_TIMEOUT; z is then NaN or not written.
+ */
+size_t bsf_few_token_moe_workspace_bytes(int64_t T, int64_t kr, int64_t I, int64_t S);
+bsf_status bsf_few_token_moe(const void* x, int64_t T, int64_t K, int64_t ldx, const int32_t* topk_ids,
+                             const float* topk_weights, int64_t kr, int64_t E, int64_t I, int weight_type,
+                             const void* w13, const int32_t* sfb13, const void* w2, const int32_t* sfb2, int64_t S,
+                             const void* w13_shared, const int32_t* sfb13_shared, const void* w2_shared,
+                             const int32_t* sfb2_shared, const void* addend, int64_t ldc, void* z, int64_t ldz,
+                             void* workspace, size_t workspace_bytes, int flags, bsf_stream_t stream);
 
 #ifdef __cplusplus
 }
