@@ -40,9 +40,9 @@ constexpr int kMaxKr = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kBoxBytes = 16384;               // 128 weight rows x 128 bytes
 constexpr int kMaxStages = 6;                  // even: a stage always serves the same box of a unit
-constexpr int kMaxSlots = 4;                   // token operands in shared memory, with their scales in tensor memory
-constexpr int kSfCols = 16;                    // columns per slot: 4 + 4 of the two boxes, then the tokens' from 8 on
-constexpr int kAccCol = kMaxSlots * kSfCols;
+constexpr int kMaxSlots = 4;                   // token operands in shared memory
+constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows, for one box
+constexpr int kAccCol = 64;                    // tensor memory: 4 columns of ones, 4 per slot and box of scales, sums
 constexpr int kParts = 4;                      // most CTAs that share a tile of the first product
 // warps: 0 weight loads, 1 and 2 MMA issuers (one per box), 4-7 and 8-11 as each kernel needs them
 constexpr int kThreads = 384;
@@ -71,7 +71,7 @@ struct FewArgs {
   int ctas1;                  // CTAs of the first kernel
   int split, nbox;            // second kernel: CTAs per cluster, 128-row tiles per CTA
   int stages, slots, slot_bytes;
-  int acc_stride;
+  int acc_stride, sets;       // columns of a sum; sets of them in the first kernel
   uint32_t tmem_cols;
   int tiled, withhold, vec4;
   int* err;
@@ -95,6 +95,14 @@ __device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[8], uint32_t (&o
                :
                : "memory");
 }
+// 32 rows of 16 bytes in shared memory -> four columns of tensor memory, the same in each of the four lane quadrants:
+// scale bytes, row r + 32 c of the operand in word c of row r.  The MMAs that the same thread issues next see them.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem_addr) {
+  uint64_t d = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);   // no swizzle
+  d |= static_cast<uint64_t>(128u >> 4) << 32;                      // stride: 8 rows x 16 bytes
+  d |= static_cast<uint64_t>(1u) << 46;                             // descriptor version (tcgen05)
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Eight values f * scale -> E4M3 codes of their leading four bits and of 16 times what is left (exact in float32).
@@ -112,10 +120,10 @@ __device__ __forceinline__ void split8(const float (&f)[8], float scale, uint2& 
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
-// A block's exponent for split8, at least -122 so that the low term's is a scale too, and the factor 2**-e: NaN
-// where the block holds an infinity (which E4M3 lacks), as a NaN in the block is NaN without it.
-__device__ __forceinline__ int split_exponent(float amax, float& scale) {
-  const int e = max(block_exponent(amax), -122);
+// A block's exponent for split8 and the factor 2**-e: NaN where the block holds an infinity (which E4M3 lacks), as a
+// NaN in the block is NaN without it.  At least `least`, so that the products' scales have an exponent.
+__device__ __forceinline__ int split_exponent(float amax, int least, float& scale) {
+  const int e = max(block_exponent(amax), least);
   scale = amax <= FLT_MAX ? inv_pow2(e) : __uint_as_float(0x7FC00000u);
   return e;
 }
@@ -136,13 +144,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* empty = full + kMaxStages;
   uint64_t* tok_full = empty + kMaxStages;
   uint64_t* tok_empty = tok_full + kMaxSlots;
-  uint64_t* acc_full = tok_empty + kMaxSlots;
+  uint64_t* acc_full = tok_empty + 8;              // (tok_empty: one for each warp that forms operands)
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* exps = reinterpret_cast<uint8_t*>(full) + kBarBytes;                 // [kMaxSlots][64] of the hi rows
-  int* group_cnt = reinterpret_cast<int*>(exps + kMaxSlots * 64);               // per 32 experts: chosen ones,
+  uint8_t* scales = reinterpret_cast<uint8_t*>(full) + kBarBytes;               // [slots][2 boxes][kSfBytes]
+  int* group_cnt = reinterpret_cast<int*>(scales + p.slots * 2 * kSfBytes);   // per 32 experts: chosen ones,
   int* group_rows = group_cnt + 32;                                             // and their rows
   uint2* chosen = reinterpret_cast<uint2*>(group_rows + 32);                    // tokens (bits); expert, first row << 16
   float* share = reinterpret_cast<float*>(chosen + min(p.E, p.R) + 1);          // [R] p of each row
@@ -153,16 +161,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rank = PHASE == 2 ? static_cast<int>(blockIdx.x) - cluster * p.split : 0;
   const int boxes = PHASE == 1 ? 2 : min(p.nbox, p.K / 128 - cluster * p.nbox);
   constexpr int kConvWarps = PHASE == 1 ? 4 : 8;
+  constexpr int kTerms = FMT == kFp8 || PHASE == 2 ? 2 : 1;
 
   if (tid == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(&tok_full[s], kConvWarps);
-      mbar_init(&tok_empty[s], boxes);
-    }
+    for (int s = 0; s < kMaxSlots; ++s) mbar_init(&tok_full[s], 1);
+    for (int s = 0; s < kConvWarps; ++s) mbar_init(&tok_empty[s], boxes);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], boxes);
       mbar_init(&acc_empty[s], 4);
@@ -254,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int g = 0; g < (p.E + 31) >> 5; ++g) nchosen += group_cnt[g];
   const uint32_t everyone = p.T == 32 ? 0xffffffffu : (1u << p.T) - 1u;
   if (tid == 0) chosen[nchosen] = make_uint2(everyone, 0u);
+  if (FMT == kFp8)                         // every row has a scale, whether or not it has values
+    for (int i = tid; i < p.slots * 2 * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
   proxy_fence();                           // the tables' place is written by TMA next
   __syncthreads();
 
@@ -289,9 +298,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     return w;
   };
-  // tokens padded to whole groups: rows of the hi terms (or of bf16 values), and columns of the MMA
-  auto padded = [&](int n) { return FMT == kFp8 ? (n + 7) & ~7 : (n + 15) & ~15; };
-  auto columns = [&](int n) { return FMT == kFp8 ? 2 * padded(n) : padded(n); };
+  // tokens padded to whole groups; the operand has so many rows for each term of a value
+  auto padded = [&](int n) { return kTerms == 2 ? (n + 7) & ~7 : (n + 15) & ~15; };
 
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
@@ -304,6 +312,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   else asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
   tc_fence_after();
   const uint32_t tmem_base = warp != 0 ? *tmem_slot : 0u;
+  if (FMT == kFp8 && warp != 0) {          // scales of the weight rows: one (a block's own goes to the tokens' rows)
+    if (warp >= 4 && warp < 8) {
+      tmem_st_x4(tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16), 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    asm volatile("bar.sync 2, %0;" ::"n"(kThreads - 32) : "memory");
+    tc_fence_after();
+  }
 
   bool have = false;                       // this warp may read the accumulators (second kernel)
   if (warp == 0) {
@@ -353,11 +370,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int b = warp - 1;
     if (b < boxes && lane == 0) {
       if (PHASE == 2) pdl_wait();
-      uint32_t stage = b, phase = 0, slot = 0, slot_phase = 0, set = 0, set_phase = 0;
+      uint32_t stage = b, phase = 0, slot = 0, slot_phase = 0, former = 0, set = 0, set_phase = 0;
       bool ok = true, start = true;
       for (int u = u0; u < u1 && ok;) {
         const Unit w = unit_at(u);
-        const int n = columns(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
+        const int n = kTerms * padded(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
         const uint32_t d = tmem_base + kAccCol + (2 * set + b) * p.acc_stride;
         const uint32_t idesc = FMT == kFp8 ? idesc_mxf8_e4m3(128, n, 0, 0) : idesc_bf16(128, n);
         if (PHASE == 1) {
@@ -373,17 +390,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           tc_fence_after();
           const uint64_t adesc = smem_desc_k_sw128(smem_u32(smem + stage * kBoxBytes));
           const uint64_t bdesc = smem_desc_k_sw128(smem_u32(slots + slot * p.slot_bytes));
-          const uint32_t sf = tmem_base + slot * kSfCols;
+          const uint32_t sf = tmem_base + 4 + (2 * slot + b) * 4;
+          if (FMT == kFp8) copy_scales(sf, smem_u32(scales + (2 * slot + b) * kSfBytes));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (FMT == kFp8)
-              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, sf + 4 * b, sf + 8, !start || k != 0);
+              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem_base, sf, !start || k != 0);
             else
               mma_bf16(d, adesc + 2 * k, bdesc + 2 * k, idesc, !start || k != 0);
           }
           start = false;
           tc_commit(&empty[stage]);
-          tc_commit(&tok_empty[slot]);
+          tc_commit(&tok_empty[former]);
+          if (++former == kConvWarps) former = 0;
           stage += boxes;                  // (an even number of stages: each stage keeps its issuer)
           if (stage >= static_cast<uint32_t>(p.stages)) { stage -= p.stages; phase ^= 1u; }
           if (++slot == static_cast<uint32_t>(p.slots)) { slot = 0; slot_phase ^= 1u; }
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         u += w.kb1 - w.kb0;
         if (PHASE == 1 && ok) {
           tc_commit(&acc_full[set]);
-          if (++set == 2) { set = 0; set_phase ^= 1u; }
+          if (++set == static_cast<uint32_t>(p.sets)) { set = 0; set_phase ^= 1u; }
         }
       }
       if (PHASE == 2 && ok) tc_commit(&acc_full[0]);
@@ -401,25 +420,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 4 + kConvWarps) {
-    // ------------------------------------------------------------ token operands and scales of every K-block
+    // ------------------------------------------------------------ token operands and scales
+    // One warp per K-block: what forms an operand is a chain of latencies (values, a maximum, codes, fences) several
+    // times as long as a unit's share of HBM, so as many of them as there are warps are under way at once.
     constexpr int kLanes = FMT == kFp8 ? 16 : 8;             // lanes of eight values per token
-    constexpr int kPerRound = 32 * kConvWarps / kLanes;      // tokens at once
-    const int ct = tid - 128, sub = ct & (kLanes - 1), mine = ct / kLanes;
-    const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    uint32_t slot = 0, slot_phase = 0;
-    bool ok = true;
-    // the scale byte of a box: one word per row, but the same for the 128 rows of a block
-    auto scale_word = [&](const Unit& w, int kb, int b) -> uint32_t {
-      if (FMT != kFp8 || b >= boxes) return 0u;
+    constexpr int kAtOnce = 32 / kLanes;                     // tokens at once
+    const int cw = warp - 4, sub = lane & (kLanes - 1), mine = lane / kLanes;
+    // exponent of a box's scale (the words of a block's 128 rows are the same)
+    auto scale_word = [&](const Unit& w, int b) -> uint32_t {
+      if (FMT != kFp8 || b >= boxes) return 0x7F7F7F7Fu;
       const bool sh = w.a == nchosen;
       const int width = sh ? p.S : p.I, e = sh ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
       const int rows = PHASE == 1 ? 2 * width : p.K, inner = PHASE == 1 ? p.K : width;
       const int row = PHASE == 1 ? b * width + w.j * 128 : (cluster * p.nbox + b) * 128;
-      const int64_t at = (static_cast<int64_t>(e) * ((inner + 511) >> 9) + (kb >> 2)) * rows + row;
+      const int64_t at = (static_cast<int64_t>(e) * ((inner + 511) >> 9) + (w.kb0 >> 2)) * rows + row;
       return static_cast<uint32_t>(__ldg((sh ? p.sf_shared : p.sf) + at));
     };
-    // eight values of token row `row` of the slot
-    auto store8 = [&](const float (&f)[8], int row, int hi_rows) {
+    // this lane's eight values of token row `row` of a slot whose terms are `rows` apart
+    auto store8 = [&](const float (&f)[8], int slot, bool valid, int row, int rows, int e0, int e1) {
       uint8_t* to = slots + slot * p.slot_bytes;
       if (FMT == kFp8) {
         float amax = 0.f;
@@ -428,147 +446,133 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale;
-        const int e = split_exponent(amax, scale);
+        const int e = split_exponent(amax, -122 - min(0, min(e0, e1)), scale);
         uint2 hi, lo;
         split8(f, scale, hi, lo);
-        if (row < hi_rows) {
+        if (valid) {
           *reinterpret_cast<uint2*>(operand_at(to, row, sub >> 1) + (sub & 1) * 8) = hi;
-          *reinterpret_cast<uint2*>(operand_at(to, hi_rows + row, sub >> 1) + (sub & 1) * 8) = lo;
-          if (sub == 0) exps[slot * 64 + row] = static_cast<uint8_t>(e + 127);
+          *reinterpret_cast<uint2*>(operand_at(to, rows + row, sub >> 1) + (sub & 1) * 8) = lo;
+          if (sub < 4) {                   // lane 0: hi of box 0, 1: hi of box 1, 2 and 3: lo, 2**-4 of it
+            const int r = sub & 2 ? rows + row : row;
+            const int byte = min(e + (sub & 1 ? e1 : e0) + 127 - (sub & 2 ? 4 : 0), 254);
+            *reinterpret_cast<uint32_t*>(scales + (2 * slot + (sub & 1)) * kSfBytes + (r & 31) * 16 + (r >> 5) * 4) =
+                static_cast<uint32_t>(byte);
+          }
         }
-      } else if (row < hi_rows) {
-        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) =
-            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      } else if (valid) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+          if (kTerms == 2)
+            lo[i] = pack_bf16x2(f[2 * i] - __uint_as_float(hi[i] << 16), f[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+        }
+        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (kTerms == 2) *reinterpret_cast<uint4*>(operand_at(to, rows + row, sub)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     };
-    // hands the slot over once all warps have written it; false if one of them gave up
-    auto publish = [&](int hi_rows, uint32_t word0, uint32_t word1, int kb) -> bool {
+    auto exponent = [](uint32_t word, int kb) { return static_cast<int>((word >> (8 * (kb & 3))) & 255u) - 127; };
+    auto publish = [&](int slot) {
       proxy_fence();
-      if (FMT == kFp8) {
-        if (named_barrier_or(2, 32 * kConvWarps, !ok)) return false;
-        if (warp < 8) {
-          const uint32_t w0 = (word0 >> (8 * (kb & 3))) & 255u, w1 = (word1 >> (8 * (kb & 3))) & 255u;
-          const uint32_t sf = quad + slot * kSfCols;
-          const uint32_t w[8] = {w0, w0, w0, w0, w1, w1, w1, w1};
-          tmem_st_x8(sf, w);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = lane + 32 * c;
-            if (32 * c < 2 * hi_rows)
-              tmem_st_x1(sf + 8 + c, r < hi_rows ? exps[slot * 64 + r] : r < 2 * hi_rows ? exps[slot * 64 + r - hi_rows] - 4 : 127);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-      } else if (!ok) {
-        return false;
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&tok_full[slot]);
-      if (++slot == static_cast<uint32_t>(p.slots)) { slot = 0; slot_phase ^= 1u; }
-      return true;
+    };
+    // K-block i takes the slot of K-block i - slots, whose end has a barrier by the warp that formed it: this warp has
+    // seen the one before there complete, when it formed block i - kConvWarps, and the one after cannot be,
+    // so a parity says which.
+    auto wait_slot = [&](int i) {
+      const int before = i - p.slots;
+      return before < 0 || wait_all(&tok_empty[before % kConvWarps], (before / kConvWarps) & 1, abort_flag, p.err);
     };
 
     if (PHASE == 1) {
-      // x, one load ahead: the next round's values (and scale words) are in flight while this one's are split
-      struct At {
-        Unit w;
-        int u, kb, round, n;
-      };
-      auto begin = [&](int u) {
-        At a;
-        a.u = u;
-        a.w = unit_at(min(u, max(u1 - 1, 0)));
-        a.kb = a.w.kb0;
-        a.round = 0;
-        a.n = __popc(chosen[a.w.a].x);
-        return a;
-      };
-      uint4 next = {};
-      uint32_t next0 = 0, next1 = 0;
-      auto load = [&](const At& a) {
-        const int j = a.round * kPerRound + mine;
-        next = make_uint4(0, 0, 0, 0);
-        if (j < a.n) {
-          const int t = a.w.a == nchosen ? j : token[(chosen[a.w.a].y >> 16) + j];
-          next = __ldg(reinterpret_cast<const uint4*>(p.x + t * p.ldx + a.kb * (kLanes * 8) + sub * 8));
+      // x: the loads of up to kBatch rounds are in flight while the warp waits for its slot
+      constexpr int kBatch = 4;
+      for (int i = cw; u0 + i < u1; i += kConvWarps) {
+        const Unit w = unit_at(u0 + i);
+        const uint2 who = chosen[w.a];
+        const int n = __popc(who.x), slot = i % p.slots, rows = padded(n);
+        const uint8_t* list = token + (who.y >> 16);
+        const bool sh = w.a == nchosen;
+        const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
+        const uint16_t* from = p.x + w.kb0 * (kLanes * 8) + sub * 8;
+        bool ok = true;
+        for (int j0 = 0; j0 < n && ok; j0 += kBatch * kAtOnce) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int j = j0 + k * kAtOnce + mine;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (j < n) v[k] = __ldg(reinterpret_cast<const uint4*>(from + (sh ? j : list[j]) * p.ldx));
+          }
+          if (j0 == 0) ok = wait_slot(i);
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int row = j0 + k * kAtOnce + mine;
+            if (j0 + k * kAtOnce >= n) break;
+            float f[8];
+            bf16x8_to_float(v[k], f);
+            store8(f, slot, row < rows, row, rows, exponent(word0, w.kb0), exponent(word1, w.kb0));
+          }
         }
-        if (a.round == 0) {
-          next0 = scale_word(a.w, a.kb, 0);
-          next1 = scale_word(a.w, a.kb, 1);
-        }
-      };
-      At at = begin(u0);
-      if (u0 < u1) load(at);
-      uint32_t word0 = 0, word1 = 0;
-      while (at.u < u1) {
-        const uint4 v = next;
-        const At now = at;
-        const int hi_rows = padded(now.n);
-        if (now.round == 0) {
-          word0 = next0;
-          word1 = next1;
-        }
-        const bool last = (now.round + 1) * kPerRound >= hi_rows;
-        if (!last) {
-          ++at.round;
-        } else {
-          at.round = 0;
-          ++at.u;
-          if (++at.kb == now.w.kb1) at = begin(at.u);
-        }
-        if (at.u < u1) load(at);
-        if (now.round == 0)
-          ok = wait_all(&tok_empty[slot], slot_phase ^ 1u, abort_flag, p.err);
-        float f[8];
-        bf16x8_to_float(v, f);
-        if (ok) store8(f, now.round * kPerRound + mine, hi_rows);
-        if (last && !publish(hi_rows, word0, word1, now.kb)) break;
+        if (!ok) break;
+        publish(slot);
       }
     } else {
-      // h from the first kernel's partial sums, at most kParts of each value, added in the order of the CTAs
+      // h from the first kernel's partial sums, at most kParts of each value, added in the order of the CTAs; tokens
+      // that did not choose the expert get zeros
       pdl_wait();
-      const int hi_rows = padded(p.T);
-      for (int u = u0; u < u1 && ok;) {
-        const Unit w = unit_at(u);
+      const int rows = padded(p.T);
+      for (int i = cw; u0 + i < u1; i += kConvWarps) {
+        const Unit w = unit_at(u0 + i);
         const bool sh = w.a == nchosen;
         const uint2 who = chosen[w.a];
+        const int n = __popc(who.x), slot = i % p.slots;
         const int width = sh ? p.S : p.I;
+        const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
         const int64_t part_step = static_cast<int64_t>(sh ? p.T : p.R) * 2 * width;
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          const uint32_t word0 = scale_word(w, kb, 0), word1 = scale_word(w, kb, 1);
-          const int i = kb * (kLanes * 8) + sub * 8;                     // of h
-          const int item = w.a * tiles + (i >> 7);
-          const int parts = ((item + 1) * p.nkb1 - 1) / per - item * p.nkb1 / per + 1;
-          bool waited = false;
-          for (int base = 0; base < hi_rows; base += kPerRound) {
-            const int t = base + mine;
-            float f[8] = {};
-            if (t < p.T && (who.x >> t & 1u)) {
-              const int row = sh ? t : static_cast<int>(who.y >> 16) + __popc(who.x & ((1u << t) - 1u));
-              const float* at = (sh ? p.part_shared : p.part) + static_cast<int64_t>(row) * 2 * width + i;
-              float g[8] = {}, v[8] = {};
+        const int at = w.kb0 * (kLanes * 8) + sub * 8;                   // of h
+        const int item = w.a * tiles + (at >> 7);
+        const int parts = ((item + 1) * p.nkb1 - 1) / per - item * p.nkb1 / per + 1;
+        bool ok = true;
+        for (int j0 = 0; j0 < n && ok; j0 += kAtOnce) {
+          const int j = j0 + mine;
+          int t = 0;
+          float g[8] = {}, v[8] = {};
+          float weight = 1.f;
+          if (j < n) {
+            const int row = sh ? j : static_cast<int>(who.y >> 16) + j;
+            t = sh ? j : token[row];
+            weight = sh ? 1.f : share[row];
+            const float* from = (sh ? p.part_shared : p.part) + static_cast<int64_t>(row) * 2 * width + at;
 #pragma unroll
-              for (int s = 0; s < kParts; ++s) {
-                if (s >= parts) break;
-                const float4 g0 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step));
-                const float4 g1 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step) + 1);
-                const float4 v0 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step + width));
-                const float4 v1 = __ldcg(reinterpret_cast<const float4*>(at + s * part_step + width) + 1);
-                g[0] += g0.x, g[1] += g0.y, g[2] += g0.z, g[3] += g0.w, g[4] += g1.x, g[5] += g1.y, g[6] += g1.z, g[7] += g1.w;
-                v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w, v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
-              }
-              const float weight = sh ? 1.f : share[row];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) f[k] = __fdividef(g[k], 1.f + expf(-g[k])) * v[k] * weight;
+            for (int s = 0; s < kParts; ++s) {
+              if (s >= parts) break;
+              const float4 g0 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step));
+              const float4 g1 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step) + 1);
+              const float4 v0 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step + width));
+              const float4 v1 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step + width) + 1);
+              g[0] += g0.x, g[1] += g0.y, g[2] += g0.z, g[3] += g0.w, g[4] += g1.x, g[5] += g1.y, g[6] += g1.z, g[7] += g1.w;
+              v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w, v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
             }
-            if (!waited) ok = wait_all(&tok_empty[slot], slot_phase ^ 1u, abort_flag, p.err);
-            waited = true;
-            if (ok) store8(f, t, hi_rows);
           }
-          if (!publish(hi_rows, word0, word1, kb)) { ok = false; break; }
+          if (j0 == 0) {
+            ok = wait_slot(i);
+            if (!ok) break;
+            uint8_t* to = slots + slot * p.slot_bytes;
+            for (int r = lane >> 3; r < rows; r += 4) {
+              if (who.x >> r & 1u) continue;
+              *reinterpret_cast<uint4*>(operand_at(to, r, lane & 7)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(operand_at(to, rows + r, lane & 7)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.f + expf(-g[k])) * v[k] * weight;
+          store8(g, slot, j < n, t, rows, exponent(word0, w.kb0), exponent(word1, w.kb0));
         }
-        u += w.kb1 - w.kb0;
+        if (!ok) break;
+        publish(slot);
       }
     }
   } else if (PHASE == 1 && warp >= 8) {
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Unit w = unit_at(u);
       const bool sh = w.a == nchosen;
       const uint2 who = chosen[w.a];
-      const int n = __popc(who.x), hi_rows = padded(n);
+      const int n = __popc(who.x), rows = padded(n);
       const int width = sh ? p.S : p.I;
       const int part = static_cast<int>(blockIdx.x) - (w.a * tiles + w.j) * p.nkb1 / per;
       const int64_t row0 = static_cast<int64_t>(part) * (sh ? p.T : p.R) + (who.y >> 16);
@@ -589,15 +593,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 2 * set * p.acc_stride;
       for (int b = 0; b < 2; ++b) {
-        for (int c = 0; c < hi_rows; c += 8) {
+        for (int c = 0; c < rows; c += 8) {
           uint32_t r[8], o[8];
           tmem_ld_x8(acc + b * p.acc_stride + c, r);
-          tmem_ld_x8(acc + b * p.acc_stride + (FMT == kFp8 ? hi_rows : 0) + c, o);
+          tmem_ld_x8(acc + b * p.acc_stride + (kTerms - 1) * rows + c, o);
           tmem_wait_ld_regs(r, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float v = __uint_as_float(r[k]);
-            if (FMT == kFp8) v += __uint_as_float(o[k]);
+            if (kTerms == 2) v += __uint_as_float(o[k]);
             // (where a wait ran out the sums are marked, so that z cannot look like an answer)
             if (c + k < n) to[(static_cast<int64_t>(c + k) * 2 + b) * width] = ok ? v : __uint_as_float(0x7FC00000u);
           }
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[set]);
-      if (++set == 2) { set = 0; set_phase ^= 1u; }
+      if (++set == static_cast<uint32_t>(p.sets)) { set = 0; set_phase ^= 1u; }
       u += w.kb1 - w.kb0;
     }
   }
@@ -634,17 +638,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int s = 0; s < p.split; ++s) st_cluster_u32(map_rank(smem_u32(const_cast<int*>(abort_flag)), s), 1u);
       __syncwarp();
     } else if (const int b = (warp - 4) >> 2; b < boxes) {
-      const int q = warp & 3, hi_rows = padded(p.T);
+      const int q = warp & 3, rows = padded(p.T);
       const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + b * p.acc_stride;
-      for (int c = 0; c < hi_rows; c += 8) {
+      for (int c = 0; c < rows; c += 8) {
         uint32_t r[8], o[8];
         tmem_ld_x8(acc + c, r);
-        tmem_ld_x8(acc + (FMT == kFp8 ? hi_rows : 0) + c, o);
+        tmem_ld_x8(acc + rows + c, o);
         tmem_wait_ld_regs(r, o);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          float v = __uint_as_float(r[k]);
-          if (FMT == kFp8) v += __uint_as_float(o[k]);
+          const float v = __uint_as_float(r[k]) + __uint_as_float(o[k]);
           if (c + k < p.T) sums[((c + k) * boxes + b) * 128 + 32 * q + lane] = u0 < u1 ? v : 0.f;
         }
       }
@@ -737,12 +740,12 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   a.nkb2 = a.I * kSize / 128;
   a.nkb2_shared = a.S * kSize / 128;
   a.ctas1 = sms;
-  const int rows = FMT == kFp8 ? 2 * ((a.T + 7) / 8 * 8) : (a.T + 15) / 16 * 16;
+  const int rows = 2 * ((a.T + 7) / 8 * 8);      // of two terms (one term of bf16 takes no more)
   a.slot_bytes = (rows * 128 + 1023) / 1024 * 1024;
   a.acc_stride = (rows + 31) / 32 * 32;
   const int tables = (((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5 + 15) / 16 * 16;
-  const int fixed = 1024 + kBarBytes + kMaxSlots * 64 + 256 + tables;
-  a.slots = a.slot_bytes <= 2048 ? kMaxSlots : 3;
+  a.slots = a.slot_bytes <= 2048 ? kMaxSlots : 2;
+  const int fixed = 1024 + kBarBytes + a.slots * 2 * kSfBytes + 256 + tables;
   a.stages = (kMostSmem - fixed - a.slots * a.slot_bytes) / kBoxBytes;
   a.stages = a.stages >= kMaxStages ? kMaxStages : a.stages / 2 * 2;
   const size_t smem = fixed + a.slots * a.slot_bytes + a.stages * kBoxBytes;
@@ -770,7 +773,8 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
 
   a.sf = sf13;
   a.sf_shared = sf13_shared;
-  a.tmem_cols = columns_of(kAccCol + 4 * a.acc_stride);
+  a.sets = 2;
+  a.tmem_cols = columns_of(kAccCol + 2 * a.sets * a.acc_stride);
   void* args1[] = {&m13, &s13, &a};
   const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, smem, 0, s, args1);
   if (first != BSF_OK) return first;
