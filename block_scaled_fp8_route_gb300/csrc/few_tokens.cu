@@ -24,6 +24,7 @@
 //   each term holds 4, so the split is exact down to 2**-14 of the block's largest value and off by at most
 //   2**-21 of that below; a float32 h is off by at most 2**-9 of its size or 2**-21 of the block's largest.  The weights
 //   go from HBM to the tensor core without passing a register.
+#include <algorithm>
 #include <cfloat>
 
 #include "cluster.cuh"
@@ -39,15 +40,16 @@ constexpr int kMaxTokens = 32;
 constexpr int kMaxKr = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kBoxBytes = 16384;               // 128 weight rows x 128 bytes
-constexpr int kMaxStages = 6;                  // even: a stage always serves the same box of a unit
-constexpr int kMaxSlots = 4;                   // token operands in shared memory
-constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows, for one box
-constexpr int kAccCol = 64;                    // tensor memory: 4 columns of ones, 4 per slot and box of scales, sums
+constexpr int kMaxStages = 4;                  // a stage: two boxes, the token operand that both meet, its scales
+constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows: words 0, 1 for box 0, 2, 3 for box 1
+constexpr int kAccCol = 64;                    // tensor memory: 4 columns of ones, 4 per stage and box of scales, sums
 constexpr int kParts = 4;                      // most CTAs that share a tile of the first product
-// warps: 0 weight loads, 1 and 2 MMA issuers (one per box), 4-7 and 8-11 as each kernel needs them
+// warps: 0 and 3 weight loads, 1 and 2 MMA issuers (one per box each), 4-7 and 8-11 as each kernel needs them
 constexpr int kThreads = 384;
-constexpr int kBarBytes = 256;
-constexpr int kMostSmem = 113 * 1024;          // two CTAs per SM
+constexpr int kBarBytes = 384;                // barriers 232, two words, 32 words of groups
+constexpr int kSmem = 113 * 1024;              // two CTAs per SM
+constexpr int kMostSmem = 227 * 1024;
+constexpr int kMaxSplit = 16;
 
 enum { kFp8 = 0, kBf16 = 1 };
 
@@ -70,7 +72,7 @@ struct FewArgs {
   int nkb2, nkb2_shared;      // of the second, per expert
   int ctas1;                  // CTAs of the first kernel
   int split, nbox;            // second kernel: CTAs per cluster, 128-row tiles per CTA
-  int stages, slots, slot_bytes;
+  int stages, operand_bytes;
   int acc_stride, sets;       // columns of a sum; sets of them in the first kernel
   uint32_t tmem_cols;
   int tiled, withhold, vec4;
@@ -139,20 +141,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                const FewArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* slots = smem + p.stages * kBoxBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slots + p.slots * p.slot_bytes);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* tok_full = empty + kMaxStages;
-  uint64_t* tok_empty = tok_full + kMaxSlots;
-  uint64_t* acc_full = tok_empty + 8;              // (tok_empty: one for each warp that forms operands)
+  const int stage_bytes = 2 * kBoxBytes + p.operand_bytes;
+  uint8_t* scales = smem + p.stages * stage_bytes;                              // [stages][kSfBytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + p.stages * kSfBytes);   // per stage and box
+  uint64_t* empty = full + 2 * kMaxStages;                                      // per stage and box
+  uint64_t* formed = empty + 2 * kMaxStages;                                    // one for each warp that forms operands
+  uint64_t* acc_full = formed + 8;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* scales = reinterpret_cast<uint8_t*>(full) + kBarBytes;               // [slots][2 boxes][kSfBytes]
-  int* group_cnt = reinterpret_cast<int*>(scales + p.slots * 2 * kSfBytes);   // per 32 experts: chosen ones,
-  int* group_rows = group_cnt + 32;                                             // and their rows
-  uint2* chosen = reinterpret_cast<uint2*>(group_rows + 32);                    // tokens (bits); expert, first row << 16
+  uint32_t* groups_of = tmem_slot + 2;                                          // per 32 experts: chosen ones, rows << 16
+  uint2* chosen = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(full) + kBarBytes);   // tokens (bits); expert, first row << 16
   float* share = reinterpret_cast<float*>(chosen + min(p.E, p.R) + 1);          // [R] p of each row
   uint8_t* token = reinterpret_cast<uint8_t*>(share + p.R);                     // [R] token of each row
 
@@ -164,12 +164,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kTerms = FMT == kFp8 || PHASE == 2 ? 2 : 1;
 
   if (tid == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < 2 * kMaxStages; ++s) {
+      mbar_init(&full[s], 2);              // its load, and the warp that formed the operand
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kMaxSlots; ++s) mbar_init(&tok_full[s], 1);
-    for (int s = 0; s < kConvWarps; ++s) mbar_init(&tok_empty[s], boxes);
+    for (int s = 0; s < kConvWarps; ++s) mbar_init(&formed[s], boxes);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], boxes);
       mbar_init(&acc_empty[s], 4);
@@ -182,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // The first kernel lets the second one start once everything before both is complete, so that the second may read
   // topk_ids, topk_weights and weights at once; only the partial sums (and z) wait for the first to end.
+  for (int e = tid; e < p.E; e += kThreads) reinterpret_cast<uint32_t*>(smem)[e] = 0u;      // (the masks below)
   if (PHASE == 1) pdl_wait();
   pdl_launch_dependents();
 
@@ -192,7 +192,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     int* first = reinterpret_cast<int*>(mask + kMaxExperts);
     int* ids = first + kMaxExperts;
     float* w = reinterpret_cast<float*>(ids + kMaxTokens * kMaxKr);
-    for (int e = tid; e < p.E; e += kThreads) mask[e] = 0u;
     __syncthreads();
     for (int i = tid; i < p.R; i += kThreads) {
       const int id = __ldcg(p.ids + i);
@@ -210,10 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t m = g * 32 + lane < p.E ? mask[g * 32 + lane] : 0u;
       const int n = __reduce_add_sync(0xffffffffu, __popc(m));
       const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
-      if (lane == 0) {
-        group_cnt[g] = __popc(some);
-        group_rows[g] = n;
-      }
+      if (lane == 0) groups_of[g] = static_cast<uint32_t>(__popc(some)) | static_cast<uint32_t>(n) << 16;
     }
     __syncthreads();
     for (int g = warp; g < groups; g += kThreads / 32) {
@@ -229,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       rows -= __popc(m);
       int at = __popc(some & ((1u << lane) - 1u));
       for (int k = 0; k < g; ++k) {
-        rows += group_rows[k];
-        at += group_cnt[k];
+        rows += static_cast<int>(groups_of[k] >> 16);
+        at += static_cast<int>(groups_of[k] & 0xFFFFu);
       }
       if (m) {
         chosen[at] = make_uint2(m, static_cast<uint32_t>(e) | static_cast<uint32_t>(rows) << 16);
@@ -258,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   int nchosen = 0;
-  for (int g = 0; g < (p.E + 31) >> 5; ++g) nchosen += group_cnt[g];
+  for (int g = 0; g < (p.E + 31) >> 5; ++g) nchosen += static_cast<int>(groups_of[g] & 0xFFFFu);
   const uint32_t everyone = p.T == 32 ? 0xffffffffu : (1u << p.T) - 1u;
   if (tid == 0) chosen[nchosen] = make_uint2(everyone, 0u);
   if (FMT == kFp8)                         // every row has a scale, whether or not it has values
-    for (int i = tid; i < p.slots * 2 * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
+    for (int i = tid; i < p.stages * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
   proxy_fence();                           // the tables' place is written by TMA next
   __syncthreads();
 
@@ -307,25 +303,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncwarp();
   tc_fence_before();
-  // (the loads do not wait for tensor memory, which the first kernel may still hold)
-  if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-  else asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-  tc_fence_after();
-  const uint32_t tmem_base = warp != 0 ? *tmem_slot : 0u;
-  if (FMT == kFp8 && warp != 0) {          // scales of the weight rows: one (a block's own goes to the tokens' rows)
-    if (warp >= 4 && warp < 8) {
-      tmem_st_x4(tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16), 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-      tmem_wait_st();
-      tc_fence_before();
+  // (the loads and the operands do not wait for tensor memory, which the first kernel may still hold)
+  if (warp == 1 || warp == 2 || warp >= 8) {
+    asm volatile("bar.sync 1, %0;" ::"n"(6 * 32) : "memory");
+    if (FMT == kFp8) {                     // scales of the weight rows: one (a block's own goes to the tokens' rows)
+      if (warp >= 8) {
+        tc_fence_after();
+        tmem_st_x4(*tmem_slot + (static_cast<uint32_t>(32 * (warp & 3)) << 16), 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu,
+                   0x7F7F7F7Fu);
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      asm volatile("bar.sync 2, %0;" ::"n"(6 * 32) : "memory");
     }
-    asm volatile("bar.sync 2, %0;" ::"n"(kThreads - 32) : "memory");
     tc_fence_after();
   }
+  const volatile uint32_t* tmem_at = tmem_slot;      // (read by the warps above; by the others after a later barrier)
 
   bool have = false;                       // this warp may read the accumulators (second kernel)
-  if (warp == 0) {
+  // Each box of a K-block has a loading and an issuing thread of its own: a load with its waits takes a thread about 300
+  // cycles, four MMAs with theirs 800, where two boxes' share of HBM is 1400, and less while stages are catching up.
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ weight loads
-    if (lane == 0) {
+    const int b = warp == 0 ? 0 : 1;
+    if (lane == 0 && b < boxes) {
       const uint64_t once = l2_policy_evict_first();
       uint32_t stage = 0, phase = 0;
       int issued = 0;
@@ -336,41 +337,42 @@ __global__ void __launch_bounds__(kThreads, 2)
         const CUtensorMap* map = shared ? &map_shared : &map_routed;
         const int e = shared ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
         const int width = shared ? p.S : p.I;                            // of h
-        const int row = PHASE == 1 ? e * 2 * width + w.j * 128 : e * p.K + cluster * p.nbox * 128;
-        const int step = PHASE == 1 ? width : 128;                       // rows from the first box to the second
+        const int row = PHASE == 1 ? (2 * e + b) * width + w.j * 128 : e * p.K + (cluster * p.nbox + b) * 128;
         const int nkb = PHASE == 1 ? p.nkb1 : shared ? p.nkb2_shared : p.nkb2;
-        for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
-          for (int b = 0; b < boxes; ++b) {
-            // (the second kernel's clock starts when the first kernel has ended)
-            if (PHASE == 2 && issued == p.stages) pdl_wait();
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
-            const int r = row + b * step;
-            mbar_arrive_expect_tx(&full[stage], kBoxBytes);
-            if (p.tiled)
-              tma_load_2d_hint(smem + stage * kBoxBytes, map, &full[stage], 0, r * nkb + kb * 128, once);
-            else
-              tma_load_2d_hint(smem + stage * kBoxBytes, map, &full[stage], kb * 128, r, once);
-            ++issued;
-            if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
-          }
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          // (the second kernel's clock starts when the first kernel has ended)
+          if (PHASE == 2 && issued == p.stages) pdl_wait();
+          uint64_t* bar = &full[2 * stage + b];
+          if (!mbar_wait(&empty[2 * stage + b], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
+          // the stage's operand may be formed anew, too
+          if (issued >= p.stages) mbar_arrive(&formed[(issued - p.stages) & (kConvWarps - 1)]);
+          mbar_arrive_expect_tx(bar, kBoxBytes);
+          uint8_t* to = smem + stage * stage_bytes + b * kBoxBytes;
+          if (p.tiled)
+            tma_load_2d_hint(to, map, bar, 0, row * nkb + kb * 128, once);
+          else
+            tma_load_2d_hint(to, map, bar, kb * 128, row, once);
+          ++issued;
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
         }
         u += w.kb1 - w.kb0;
       }
       // no TMA write may be in flight when the CTA exits or reuses its stages
-      const int outstanding = issued < p.stages ? issued : p.stages;
+      const int outstanding = min(issued, p.stages);
       for (int i = 0; i < outstanding; ++i) {
         if (stage == 0) { stage = p.stages; phase ^= 1u; }
         --stage;
-        wait_quiet(&full[stage], phase);
+        wait_quiet(&full[2 * stage + b], phase);
       }
     }
     __syncwarp();
   } else if (warp <= 2) {
-    // ------------------------------------------------------------ MMA issuers: one box of every unit each
+    // ------------------------------------------------------------ MMA issuers
     const int b = warp - 1;
-    if (b < boxes && lane == 0) {
+    if (lane == 0 && b < boxes) {
+      const uint32_t tmem_base = *tmem_at;
       if (PHASE == 2) pdl_wait();
-      uint32_t stage = b, phase = 0, slot = 0, slot_phase = 0, former = 0, set = 0, set_phase = 0;
+      uint32_t stage = 0, phase = 0, set = 0, set_phase = 0;
       bool ok = true, start = true;
       for (int u = u0; u < u1 && ok;) {
         const Unit w = unit_at(u);
@@ -382,30 +384,23 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!mbar_wait(&acc_empty[set], set_phase ^ 1u, abort_flag, p.err)) break;
         }
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait(&tok_full[slot], slot_phase, abort_flag, p.err) ||
-              !mbar_wait(&full[stage], phase, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
+          if (!mbar_wait(&full[2 * stage + b], phase, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t adesc = smem_desc_k_sw128(smem_u32(smem + stage * kBoxBytes));
-          const uint64_t bdesc = smem_desc_k_sw128(smem_u32(slots + slot * p.slot_bytes));
-          const uint32_t sf = tmem_base + 4 + (2 * slot + b) * 4;
-          if (FMT == kFp8) copy_scales(sf, smem_u32(scales + (2 * slot + b) * kSfBytes));
+          const uint8_t* at = smem + stage * stage_bytes;
+          const uint64_t adesc = smem_desc_k_sw128(smem_u32(at + b * kBoxBytes));
+          const uint64_t bdesc = smem_desc_k_sw128(smem_u32(at + 2 * kBoxBytes));
+          const uint32_t sf = tmem_base + 4 + (2 * stage + b) * 4;
+          if (FMT == kFp8) copy_scales(sf, smem_u32(scales + stage * kSfBytes));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (FMT == kFp8)
-              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem_base, sf, !start || k != 0);
+              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem_base, sf + 2 * b, !start || k != 0);
             else
               mma_bf16(d, adesc + 2 * k, bdesc + 2 * k, idesc, !start || k != 0);
           }
           start = false;
-          tc_commit(&empty[stage]);
-          tc_commit(&tok_empty[former]);
-          if (++former == kConvWarps) former = 0;
-          stage += boxes;                  // (an even number of stages: each stage keeps its issuer)
-          if (stage >= static_cast<uint32_t>(p.stages)) { stage -= p.stages; phase ^= 1u; }
-          if (++slot == static_cast<uint32_t>(p.slots)) { slot = 0; slot_phase ^= 1u; }
+          tc_commit(&empty[2 * stage + b]);
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
         }
         u += w.kb1 - w.kb0;
         if (PHASE == 1 && ok) {
@@ -436,9 +431,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int64_t at = (static_cast<int64_t>(e) * ((inner + 511) >> 9) + (w.kb0 >> 2)) * rows + row;
       return static_cast<uint32_t>(__ldg((sh ? p.sf_shared : p.sf) + at));
     };
-    // this lane's eight values of token row `row` of a slot whose terms are `rows` apart
-    auto store8 = [&](const float (&f)[8], int slot, bool valid, int row, int rows, int e0, int e1) {
-      uint8_t* to = slots + slot * p.slot_bytes;
+    // This lane's eight values of a token as they go into an operand: the terms' codes (or bf16 values), and the
+    // exponent of their block.
+    struct Terms {
+      uint32_t hi[4], lo[4];
+      int e;
+    };
+    auto terms_of = [&](const float (&f)[8], int e0, int e1) {
+      Terms r;
+      r.e = 0;
       if (FMT == kFp8) {
         float amax = 0.f;
 #pragma unroll
@@ -446,52 +447,58 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale;
-        const int e = split_exponent(amax, -122 - min(0, min(e0, e1)), scale);
+        r.e = split_exponent(amax, -122 - min(0, min(e0, e1)), scale);
         uint2 hi, lo;
         split8(f, scale, hi, lo);
-        if (valid) {
-          *reinterpret_cast<uint2*>(operand_at(to, row, sub >> 1) + (sub & 1) * 8) = hi;
-          *reinterpret_cast<uint2*>(operand_at(to, rows + row, sub >> 1) + (sub & 1) * 8) = lo;
-          if (sub < 4) {                   // lane 0: hi of box 0, 1: hi of box 1, 2 and 3: lo, 2**-4 of it
-            const int r = sub & 2 ? rows + row : row;
-            const int byte = min(e + (sub & 1 ? e1 : e0) + 127 - (sub & 2 ? 4 : 0), 254);
-            *reinterpret_cast<uint32_t*>(scales + (2 * slot + (sub & 1)) * kSfBytes + (r & 31) * 16 + (r >> 5) * 4) =
-                static_cast<uint32_t>(byte);
-          }
-        }
-      } else if (valid) {
-        uint32_t hi[4], lo[4];
+        r.hi[0] = hi.x, r.hi[1] = hi.y, r.lo[0] = lo.x, r.lo[1] = lo.y;
+      } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          hi[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+          r.hi[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
           if (kTerms == 2)
-            lo[i] = pack_bf16x2(f[2 * i] - __uint_as_float(hi[i] << 16), f[2 * i + 1] - __uint_as_float(hi[i] & 0xFFFF0000u));
+            r.lo[i] = pack_bf16x2(f[2 * i] - __uint_as_float(r.hi[i] << 16), f[2 * i + 1] - __uint_as_float(r.hi[i] & 0xFFFF0000u));
         }
-        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (kTerms == 2) *reinterpret_cast<uint4*>(operand_at(to, rows + row, sub)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      return r;
+    };
+    // ... as row `row` of a stage's operand whose terms are `rows` apart
+    auto put = [&](const Terms& r, int stage, int row, int rows, int e0, int e1) {
+      uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
+      if (FMT == kFp8) {
+        *reinterpret_cast<uint2*>(operand_at(to, row, sub >> 1) + (sub & 1) * 8) = make_uint2(r.hi[0], r.hi[1]);
+        *reinterpret_cast<uint2*>(operand_at(to, rows + row, sub >> 1) + (sub & 1) * 8) = make_uint2(r.lo[0], r.lo[1]);
+        if (sub < 4) {                     // lane 0: hi for box 0, 1: hi for box 1, 2 and 3: lo, 2**-4 of it
+          const int at = sub & 2 ? rows + row : row;
+          const int byte = min(r.e + (sub & 1 ? e1 : e0) + 127 - (sub & 2 ? 4 : 0), 254);
+          *reinterpret_cast<uint32_t*>(scales + stage * kSfBytes + (at & 31) * 16 + (sub & 1) * 8 + (at >> 5) * 4) =
+              static_cast<uint32_t>(byte);
+        }
+      } else {
+        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) = make_uint4(r.hi[0], r.hi[1], r.hi[2], r.hi[3]);
+        if (kTerms == 2) *reinterpret_cast<uint4*>(operand_at(to, rows + row, sub)) = make_uint4(r.lo[0], r.lo[1], r.lo[2], r.lo[3]);
       }
     };
     auto exponent = [](uint32_t word, int kb) { return static_cast<int>((word >> (8 * (kb & 3))) & 255u) - 127; };
-    auto publish = [&](int slot) {
+    // K-block i takes the stage of K-block i - stages.  Its end is told (by the loading threads, who wait for it
+    // anyway) on a barrier of the warp that formed it: this warp has seen the one before there complete, when it
+    // formed K-block i - kConvWarps, and the one after cannot be yet (stages <= kConvWarps), so a parity says which.
+    auto wait_stage = [&](int i) {
+      const int before = i - p.stages;
+      return before < 0 || wait_all(&formed[before & (kConvWarps - 1)], (before / kConvWarps) & 1, abort_flag, p.err);
+    };
+    auto publish = [&](int stage) {
       proxy_fence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tok_full[slot]);
-    };
-    // K-block i takes the slot of K-block i - slots, whose end has a barrier by the warp that formed it: this warp has
-    // seen the one before there complete, when it formed block i - kConvWarps, and the one after cannot be,
-    // so a parity says which.
-    auto wait_slot = [&](int i) {
-      const int before = i - p.slots;
-      return before < 0 || wait_all(&tok_empty[before % kConvWarps], (before / kConvWarps) & 1, abort_flag, p.err);
+      if (lane < boxes) mbar_arrive(&full[2 * stage + lane]);
     };
 
     if (PHASE == 1) {
-      // x: the loads of up to kBatch rounds are in flight while the warp waits for its slot
+      // x: the loads of up to kBatch rounds are in flight at once, and while the warp waits for its stage
       constexpr int kBatch = 4;
       for (int i = cw; u0 + i < u1; i += kConvWarps) {
         const Unit w = unit_at(u0 + i);
         const uint2 who = chosen[w.a];
-        const int n = __popc(who.x), slot = i % p.slots, rows = padded(n);
+        const int n = __popc(who.x), stage = i % p.stages, rows = padded(n);
         const uint8_t* list = token + (who.y >> 16);
         const bool sh = w.a == nchosen;
         const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
@@ -505,32 +512,44 @@ __global__ void __launch_bounds__(kThreads, 2)
             v[k] = make_uint4(0, 0, 0, 0);
             if (j < n) v[k] = __ldg(reinterpret_cast<const uint4*>(from + (sh ? j : list[j]) * p.ldx));
           }
-          if (j0 == 0) ok = wait_slot(i);
-          if (!ok) break;
+          const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int row = j0 + k * kAtOnce + mine;
-            if (j0 + k * kAtOnce >= n) break;
+            if (row - mine >= n) break;
             float f[8];
             bf16x8_to_float(v[k], f);
-            store8(f, slot, row < rows, row, rows, exponent(word0, w.kb0), exponent(word1, w.kb0));
+            const Terms r = terms_of(f, e0, e1);
+            if (j0 + k == 0) ok = wait_stage(i);
+            if (!ok) break;
+            if (row < rows) put(r, stage, row, rows, e0, e1);
           }
         }
         if (!ok) break;
-        publish(slot);
+        publish(stage);
       }
     } else {
       // h from the first kernel's partial sums, at most kParts of each value, added in the order of the CTAs; tokens
       // that did not choose the expert get zeros
+      Unit w = {};
+      uint32_t word0 = 0, word1 = 0;
+      if (u0 + cw < u1) {                  // (there may be no K-block at all, nor scales)
+        w = unit_at(u0 + cw);
+        word0 = scale_word(w, 0);
+        word1 = scale_word(w, 1);
+      }
       pdl_wait();
       const int rows = padded(p.T);
       for (int i = cw; u0 + i < u1; i += kConvWarps) {
-        const Unit w = unit_at(u0 + i);
+        if (i != cw) {
+          w = unit_at(u0 + i);
+          word0 = scale_word(w, 0);
+          word1 = scale_word(w, 1);
+        }
         const bool sh = w.a == nchosen;
         const uint2 who = chosen[w.a];
-        const int n = __popc(who.x), slot = i % p.slots;
+        const int n = __popc(who.x), stage = i % p.stages;
         const int width = sh ? p.S : p.I;
-        const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
         const int64_t part_step = static_cast<int64_t>(sh ? p.T : p.R) * 2 * width;
         const int at = w.kb0 * (kLanes * 8) + sub * 8;                   // of h
         const int item = w.a * tiles + (at >> 7);
@@ -547,37 +566,53 @@ __global__ void __launch_bounds__(kThreads, 2)
             weight = sh ? 1.f : share[row];
             const float* from = (sh ? p.part_shared : p.part) + static_cast<int64_t>(row) * 2 * width + at;
 #pragma unroll
-            for (int s = 0; s < kParts; ++s) {
+            for (int s = 0; s < kParts; s += 2) {                        // two parts' loads at once
               if (s >= parts) break;
-              const float4 g0 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step));
-              const float4 g1 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step) + 1);
-              const float4 v0 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step + width));
-              const float4 v1 = __ldcg(reinterpret_cast<const float4*>(from + s * part_step + width) + 1);
-              g[0] += g0.x, g[1] += g0.y, g[2] += g0.z, g[3] += g0.w, g[4] += g1.x, g[5] += g1.y, g[6] += g1.z, g[7] += g1.w;
-              v[0] += v0.x, v[1] += v0.y, v[2] += v0.z, v[3] += v0.w, v[4] += v1.x, v[5] += v1.y, v[6] += v1.z, v[7] += v1.w;
-            }
-          }
-          if (j0 == 0) {
-            ok = wait_slot(i);
-            if (!ok) break;
-            uint8_t* to = slots + slot * p.slot_bytes;
-            for (int r = lane >> 3; r < rows; r += 4) {
-              if (who.x >> r & 1u) continue;
-              *reinterpret_cast<uint4*>(operand_at(to, r, lane & 7)) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(operand_at(to, rows + r, lane & 7)) = make_uint4(0, 0, 0, 0);
+              const float* f0 = from + s * part_step;
+              const float* f1 = s + 1 < parts ? f0 + part_step : f0;
+              float4 a[4], c[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) a[k] = __ldcg(reinterpret_cast<const float4*>(f0 + (k >> 1) * width) + (k & 1));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) c[k] = __ldcg(reinterpret_cast<const float4*>(f1 + (k >> 1) * width) + (k & 1));
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                g[4 * k] += a[k].x, g[4 * k + 1] += a[k].y, g[4 * k + 2] += a[k].z, g[4 * k + 3] += a[k].w;
+                v[4 * k] += a[2 + k].x, v[4 * k + 1] += a[2 + k].y, v[4 * k + 2] += a[2 + k].z, v[4 * k + 3] += a[2 + k].w;
+              }
+              if (s + 1 < parts) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  g[4 * k] += c[k].x, g[4 * k + 1] += c[k].y, g[4 * k + 2] += c[k].z, g[4 * k + 3] += c[k].w;
+                  v[4 * k] += c[2 + k].x, v[4 * k + 1] += c[2 + k].y, v[4 * k + 2] += c[2 + k].z, v[4 * k + 3] += c[2 + k].w;
+                }
+              }
             }
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.f + expf(-g[k])) * v[k] * weight;
-          store8(g, slot, j < n, t, rows, exponent(word0, w.kb0), exponent(word1, w.kb0));
+          const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
+          const Terms r = terms_of(g, e0, e1);
+          if (j0 == 0) {
+            ok = wait_stage(i);
+            if (!ok) break;
+            uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
+            for (int z = lane >> 3; z < rows; z += 4) {
+              if (who.x >> z & 1u) continue;
+              *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (j < n) put(r, stage, t, rows, e0, e1);
         }
         if (!ok) break;
-        publish(slot);
+        publish(stage);
       }
     }
   } else if (PHASE == 1 && warp >= 8) {
     // ------------------------------------------------------------ first kernel's sums: lane = row of the tile
     const int q = warp & 3;
+    const uint32_t tmem_base = *tmem_at;
     uint32_t set = 0, set_phase = 0;
     bool ok = true;
     for (int u = u0; u < u1;) {
@@ -620,13 +655,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     if (warp == 1) {
       tc_fence_after();
-      tmem_dealloc(tmem_base, p.tmem_cols);
+      tmem_dealloc(*tmem_at, p.tmem_cols);
     }
     return;
   }
 
   // ---------------------------------------------------------------- z: partials to shared memory, sum over the cluster
   pdl_wait();                              // (every thread, before it stores)
+  __syncthreads();                         // (the place of the accumulators is known to all warps)
+  const uint32_t tmem_base = *tmem_at;
   float* sums = reinterpret_cast<float*>(smem);              // [T][boxes][128], in place of the consumed stages
   if (warp >= 4) {
     have = wait_all(&acc_full[0], 0, abort_flag, p.err) && *abort_flag == 0;
@@ -664,14 +701,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int i1 = quads * (rank + 1) / p.split;
     const uint32_t mine = smem_u32(sums);
     for (int i = quads * rank / p.split + tid; i < i1; i += kThreads) {
-      float4 v[8];
+      float4 f = {};
+      for (int s0 = 0; s0 < p.split; s0 += 8) {              // in rank order, eight loads at once
+        float4 v[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (s < p.split) v[s] = ld_cluster_f4(map_rank(mine, s) + i * 16);
-      float4 f = v[0];
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < p.split) v[s] = ld_cluster_f4(map_rank(mine, s0 + s) + i * 16);
 #pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < p.split) f.x += v[s].x, f.y += v[s].y, f.z += v[s].z, f.w += v[s].w;
+        for (int s = 0; s < 8; ++s)
+          if (s0 + s < p.split) f.x += v[s].x, f.y += v[s].y, f.z += v[s].z, f.w += v[s].w;
+      }
       const int t = i / (boxes * 32), n = cluster * p.nbox * 128 + (i - t * boxes * 32) * 4;
       if (p.vec4) {
         if (p.addend) {
@@ -696,22 +735,40 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_sync();
 }
 
+// Once per device: shared memory, clusters of up to kMaxSplit CTAs, and how many clusters of each size run at once.
+struct FewLimits {
+  std::atomic<int> clusters[kMaxSplit + 1];
+  std::atomic<bool> ready;
+};
 template <int FMT>
-bsf_status few_attributes() {
-  static std::atomic<bool> ready[64];
+bsf_status few_limits(const FewLimits** out) {
+  static FewLimits limits[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BSF_ERR_CUDA;
-  if (!ready[dev].load(std::memory_order_acquire)) {
+  FewLimits& l = limits[dev];
+  if (!l.ready.load(std::memory_order_acquire)) {    // (racing first calls store the same values)
     const void* kernels[2] = {reinterpret_cast<const void*>(few_kernel<FMT, 1>),
                               reinterpret_cast<const void*>(few_kernel<FMT, 2>)};
-    for (const void* k : kernels) {
+    for (const void* k : kernels)
       if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess ||
           cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
               cudaSuccess)
         return BSF_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernels[1], cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return BSF_ERR_CUDA;
+    for (int i = 1; i <= kMaxSplit; ++i) {
+      DependentLaunch launch(i, kThreads, kSmem, nullptr, i);
+      launch.cfg.numAttrs = 1;                       // the cluster alone
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernels[1], &launch.cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      l.clusters[i].store(n, std::memory_order_relaxed);
     }
-    ready[dev].store(true, std::memory_order_release);
+    l.ready.store(true, std::memory_order_release);
   }
+  *out = &l;
   return BSF_OK;
 }
 
@@ -732,7 +789,8 @@ template <int FMT>
 bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const void* w2, const int32_t* sf2,
                       const void* w13_shared, const int32_t* sf13_shared, const void* w2_shared,
                       const int32_t* sf2_shared, cudaStream_t s) {
-  const bsf_status st = few_attributes<FMT>();
+  const FewLimits* limits;
+  const bsf_status st = few_limits<FMT>(&limits);
   if (st != BSF_OK) return st;
   constexpr int kSize = FMT == kFp8 ? 1 : 2;
   const int sms = sm_count();
@@ -741,25 +799,25 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   a.nkb2_shared = a.S * kSize / 128;
   a.ctas1 = sms;
   const int rows = 2 * ((a.T + 7) / 8 * 8);      // of two terms (one term of bf16 takes no more)
-  a.slot_bytes = (rows * 128 + 1023) / 1024 * 1024;
+  a.operand_bytes = (rows * 128 + 1023) / 1024 * 1024;
   a.acc_stride = (rows + 31) / 32 * 32;
   const int tables = (((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5 + 15) / 16 * 16;
-  a.slots = a.slot_bytes <= 2048 ? kMaxSlots : 2;
-  const int fixed = 1024 + kBarBytes + a.slots * 2 * kSfBytes + 256 + tables;
-  a.stages = (kMostSmem - fixed - a.slots * a.slot_bytes) / kBoxBytes;
-  a.stages = a.stages >= kMaxStages ? kMaxStages : a.stages / 2 * 2;
-  const size_t smem = fixed + a.slots * a.slot_bytes + a.stages * kBoxBytes;
+  const int fixed = 1024 + kBarBytes + tables, stage_bytes = 2 * kBoxBytes + a.operand_bytes + kSfBytes;
+  a.stages = (kSmem - fixed) / stage_bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const size_t smem = fixed + a.stages * stage_bytes;
+  const int stages2 = std::min((kSmem - fixed) / stage_bytes, kMaxStages);
 
-  // The second kernel: a CTA takes two 128-row tiles of W2 where that leaves enough CTAs to keep HBM busy (the token
-  // operand is formed once for both), a cluster as much of the contraction's split as it can.
+  // The second kernel: a CTA takes two 128-row tiles of W2 (the token operand is formed once for both), and the
+  // contraction is split as far as all clusters still run at once, two CTAs per SM (the runtime's count is for one):
+  // K 4096 takes clusters of 12 (16 tokens: 202 us, of 8 209, of 16 224), K 2048 of 16 (bf16, 7 tokens: 98 us, of 8 110).
   const int tiles = a.K / 128;
-  a.nbox = (tiles + 1) / 2 * 8 >= 7 * sms / 10 ? 2 : 1;
+  a.nbox = 2;
   const int clusters = (tiles + a.nbox - 1) / a.nbox;
   const int64_t most = static_cast<int64_t>(a.E < a.R ? a.E : a.R) * a.nkb2 + a.nkb2_shared;   // K-blocks
-  a.split = 2 * sms / clusters;
-  if (a.split > 8) a.split = 8;
-  if (a.split > most) a.split = static_cast<int>(most);
-  if (a.split < 1) a.split = 1;
+  a.split = 1;
+  for (int i = 2; i <= kMaxSplit && i <= most; ++i)
+    if (2 * limits->clusters[i].load(std::memory_order_relaxed) >= clusters) a.split = i;
 
   CUtensorMap m13, m2, s13, s2;
   if (!make_weight_map(&m13, w13, static_cast<int64_t>(a.E) * 2 * a.I, static_cast<int64_t>(a.K) * kSize, a.tiled) ||
@@ -773,17 +831,18 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
 
   a.sf = sf13;
   a.sf_shared = sf13_shared;
-  a.sets = 2;
+  a.sets = kAccCol + 4 * a.acc_stride <= 256 ? 2 : 1;       // (two CTAs share an SM's tensor memory)
   a.tmem_cols = columns_of(kAccCol + 2 * a.sets * a.acc_stride);
   void* args1[] = {&m13, &s13, &a};
   const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, smem, 0, s, args1);
   if (first != BSF_OK) return first;
   FewArgs b = a;
+  b.stages = stages2;
   b.sf = sf2;
   b.sf_shared = sf2_shared;
   b.tmem_cols = columns_of(kAccCol + 2 * a.acc_stride);
   void* args2[] = {&m2, &s2, &b};
-  return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, smem, b.split, s, args2);
+  return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, fixed + stages2 * stage_bytes, b.split, s, args2);
 }
 
 }  // namespace
