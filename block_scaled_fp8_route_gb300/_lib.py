@@ -66,6 +66,8 @@ SIGNATURES = {
     "bsf_few_token_moe_workspace_bytes": (_size, [_i64, _i64, _i64, _i64]),
     "bsf_few_token_moe": (_c_int, [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _c_int, _p, _p, _p, _p, _i64, _p, _p,
                                    _p, _p, _p, _i64, _p, _i64, _p, _size, _c_int, _p]),
+    "bsf_linear": (_c_int, [_p, _c_int, _i64, _i64, _i64, _p, _i64, _i64, _p, _c_int, _c_int, _p, _i64, _p, _c_int,
+                            _i64, _c_int, _p]),
     "bsf_dense_gemm": (_c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p]),
 }
 

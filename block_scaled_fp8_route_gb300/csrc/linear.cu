@@ -1,0 +1,845 @@
+// Matrix product of unquantised operands with bias, activation and residual in its epilogue, sm_103a:
+//
+//   Y[t, n] = act( sum_k X[t, k] W[n, k] + b[n] ) + R[t, n]
+//
+// X and W both bf16 or both fp16, FP32 accumulation, Y in bf16, fp16 or float32.  Among others it gives the router's
+// logits ("GEMM 执行方式" (rainlin-net) §4.2 takes the top-k of them as given) and the projections around an
+// MoE block, added to the residual stream.
+//
+// As in the dense FP8 product, weights are the MMA's M = 128 rows (256 in a CTA pair) and tokens its N, and the
+// forms are chosen by the time each would take (choose_plan):
+//
+// * Split (few tokens, or few tiles).  A tile's K is split over a cluster of CTAs, which exchange their
+//   FP32 partials through distributed shared memory and add them in rank order: no atomics, no workspace, the same
+//   bits every run.  Bias, activation and residual are applied to the sum, once per element.
+// * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 256 tokens with one cta_group::2 MMA per 16 K;
+//   two accumulators let a tile's epilogue run under the next tile's MMAs.
+#include "cluster.cuh"
+#include "common.cuh"
+#include "host_utils.h"
+#include "tma_map.h"
+
+#include <cuda_fp16.h>
+
+namespace bsf {
+namespace {
+
+constexpr int kTileW = 128;                     // weight rows per tile and CTA
+constexpr int kBlockK = 64;                     // K per block: rows of 128 bytes
+constexpr int kRowBytes = 128;
+constexpr int kMaxTok = 128;                    // split: tokens per tile
+constexpr int kMaxIssuers = 2;
+constexpr int kThreads = 32 * (1 + kMaxIssuers + 4);   // split: loads, issuers, four warps for the accumulators
+constexpr int kMaxStages = 12;
+constexpr int kBarBytes = 512;
+constexpr int kSmemBytes = 227 * 1024;
+constexpr int kHalfSmemBytes = 112 * 1024;      // two CTAs per SM
+
+struct Epilogue {
+  const void* bias;
+  const void* residual;      // of the type of y
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int bias_type, act;
+  int wide;                  // neighbouring elements of y (and the residual) are aligned together: 4 (split), 2 (pairs)
+};
+
+struct SplitArgs {
+  Epilogue e;
+  int M, N, nkb;
+  int chunks, per;           // token chunks per weight tile, tokens of a full chunk (multiple of 16)
+  int split, stages;
+  int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between their accumulators
+  uint32_t tmem_cols, idesc;
+  int withhold;              // BSF_DEBUG_WITHHOLD_LOADS, in the last CTA of each cluster
+  int* err;
+};
+
+__device__ __forceinline__ float load_as_float(const void* p, int64_t i, int type) {
+  if (type == BSF_TYPE_F32) return __ldg(static_cast<const float*>(p) + i);
+  const uint16_t v = __ldg(static_cast<const uint16_t*>(p) + i);
+  return type == BSF_TYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+
+// Values of OUT, two in a word where it has 16 bits.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (OUT == BSF_TYPE_BF16) return pack_bf16x2(a, b);
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int OUT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (OUT == BSF_TYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// y may be the residual itself, so the residual is read with plain loads.
+template <int OUT>
+__device__ __forceinline__ float residual_at(const Epilogue& e, int64_t i) {
+  if (OUT == BSF_TYPE_F32) return static_cast<const float*>(e.residual)[i];
+  return unpack2<OUT>(static_cast<const uint16_t*>(e.residual)[i]).x;
+}
+template <int OUT>
+__device__ __forceinline__ void store_at(const Epilogue& e, int64_t i, float v) {
+  if (OUT == BSF_TYPE_F32) static_cast<float*>(e.y)[i] = v;
+  else static_cast<uint16_t*>(e.y)[i] = static_cast<uint16_t>(pack2<OUT>(v, 0.f));
+}
+
+// Each activation of N values, in float32 within a few units in the last place of it (relative: the tails of gelu
+// and of the sigmoids are not differences).  A quotient by more than 2**126 is 0, where the exact one is below 2**-119.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  switch (act) {
+    case BSF_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];            // (NaN stays)
+      break;
+    case BSF_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.f + expf(-v[i]));
+      break;
+    case BSF_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
+      break;
+    case BSF_ACT_GELU_TANH:             // 0.5 v (1 + tanh(u)) = v / (1 + exp(-2 u)), u = sqrt(2 / pi) (v + 0.044715 v^3)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u2 = v[i] * (1.5957691216057308f + 0.07135481627364643f * v[i] * v[i]);
+        v[i] = __fdividef(v[i], 1.f + expf(-u2));
+      }
+      break;
+    case BSF_ACT_SIGMOID:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(1.f, 1.f + expf(-v[i]));
+      break;
+    default:
+      break;
+  }
+}
+
+// Tokens [j0, j1) of a tile: their S partials part[token][weight row], one in each CTA of the cluster, summed in
+// rank order, through the epilogue and stored.  A thread takes items (token, four weight rows) and has the loads of U
+// of them in flight.
+template <int OUT, int S, int U>
+__device__ __forceinline__ void sum_and_store(const SplitArgs& p, uint32_t part, int n0, int tok0, int j0, int j1) {
+  uint32_t base[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) base[s] = map_rank(part, s);
+  const Epilogue& e = p.e;
+  for (int i0 = threadIdx.x + j0 * 32; i0 < j1 * 32; i0 += U * kThreads) {
+    float4 v[U][S];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * kThreads, j1 * 32 - 1);     // (past the end: the last item again, not stored)
+#pragma unroll
+      for (int s = 0; s < S; ++s) v[u][s] = ld_cluster_f4(base[s] + i * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= j1 * 32) break;
+      float f[4] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w};
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        f[0] += v[u][s].x;
+        f[1] += v[u][s].y;
+        f[2] += v[u][s].z;
+        f[3] += v[u][s].w;
+      }
+      const int n = n0 + (i & 31) * 4;
+      if (n >= p.N) continue;
+      const int64_t row = tok0 + (i >> 5);
+      if (e.bias) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (n + x < p.N) f[x] += load_as_float(e.bias, n + x, e.bias_type);
+      }
+      activate(f, e.act);
+      if (e.wide && n + 4 <= p.N) {
+        if (OUT == BSF_TYPE_F32) {
+          float* to = static_cast<float*>(e.y) + row * e.ldy + n;
+          if (e.residual) {
+            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + row * e.ldr + n);
+            f[0] += r.x, f[1] += r.y, f[2] += r.z, f[3] += r.w;
+          }
+          *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+          uint16_t* to = static_cast<uint16_t*>(e.y) + row * e.ldy + n;
+          if (e.residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.residual) + row * e.ldr + n);
+            const float2 a = unpack2<OUT>(r.x), b = unpack2<OUT>(r.y);
+            f[0] += a.x, f[1] += a.y, f[2] += b.x, f[3] += b.y;
+          }
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]));
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (n + x >= p.N) break;
+          const float r = e.residual ? residual_at<OUT>(e, row * e.ldr + n + x) : 0.f;
+          store_at<OUT>(e, row * e.ldy + n + x, f[x] + r);
+        }
+      }
+    }
+  }
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads, 2)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                        const SplitArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = (kTileW + p.per) * kRowBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
+  const int nt = tile / p.chunks, chunk = tile - nt * p.chunks;
+  const int tok0 = chunk * p.per;
+  const int ntok = min(p.per, p.M - tok0);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, p.issuers);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_w);
+    tma_prefetch_desc(&tmap_x);
+  }
+  pdl_launch_dependents();
+  // Dependent launch: while the preceding kernel drains, the first stages of the weights are pulled into L2 (what
+  // that kernel may still write is written in L2, too).  No global memory is loaded or stored before it has completed.
+  if (threadIdx.x == 0)
+    for (int kb = kb0; kb < min(kb1, kb0 + p.stages); ++kb) tma_prefetch_l2(&tmap_w, kb * kBlockK, nt * kTileW);
+  pdl_wait();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  // (the loading warp, whose own thread initialised the barriers, does not wait for the others)
+  if (warp != 0) asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  else asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+  tc_fence_after();
+  const uint32_t tmem_base = warp != 0 ? *tmem_slot : 0u;
+
+  bool have = false;                       // this warp may read the accumulators
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1 && !(p.withhold && rank == p.split - 1); ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) break;
+        uint8_t* dst = smem + stage * stage_bytes;
+        mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        tma_load_2d(dst, &tmap_w, &full[stage], kb * kBlockK, nt * kTileW);
+        tma_load_2d(dst + kTileW * kRowBytes, &tmap_x, &full[stage], kb * kBlockK, tok0);
+        ++issued;
+        if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+      }
+      // no TMA write may be in flight when the CTA exits or reuses its stages
+      const int outstanding = min(issued, p.stages);
+      for (int j = 0; j < outstanding; ++j) {
+        if (stage == 0) { stage = p.stages; phase ^= 1u; }
+        --stage;
+        wait_quiet(&full[stage], phase);
+      }
+    }
+    __syncwarp();
+  } else if (warp <= kMaxIssuers) {
+    // ------------------------------------------------------------ MMA issuers
+    // Issuer i takes the K-blocks (kb - kb0) % issuers == i into an accumulator of its own: four narrow MMAs with
+    // their wait and commit keep a thread busy longer than the loads of a block take.
+    const int me = warp - 1;
+    if (me < p.issuers && lane == 0) {
+      const uint32_t d_tmem = tmem_base + me * p.acc_stride;
+      uint32_t stage = me, phase = 0;      // (stages are a multiple of issuers: a stage keeps its issuer)
+      bool first = true;
+      for (int kb = kb0 + me; kb < kb1; kb += p.issuers) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint8_t* src = smem + stage * stage_bytes;
+        const uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
+        const uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + kTileW * kRowBytes));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_bf16(d_tmem, adesc + 2 * k, bdesc + 2 * k, p.idesc, !first || k != 0);
+        first = false;
+        tc_commit(&empty[stage]);
+        stage += p.issuers;
+        if (stage >= static_cast<uint32_t>(p.stages)) { stage -= p.stages; phase ^= 1u; }
+      }
+      // commits on every way out: TMEM is released only after the issued MMAs are done
+      tc_commit(acc_full);
+      wait_quiet(acc_full, 0);
+    }
+    __syncwarp();
+  } else {
+    have = wait_all(acc_full, 0, abort_flag, p.err) && *abort_flag == 0;
+    have = __all_sync(0xffffffffu, have);
+    tc_fence_after();
+    // A wait that ran out anywhere in this CTA ends here, and keeps all of its cluster from storing.
+    if (!have) {
+      if (lane == 0)
+        for (int s = 0; s < p.split; ++s) st_cluster_u32(map_rank(smem_u32(const_cast<int*>(abort_flag)), s), 1u);
+      __syncwarp();
+    }
+  }
+
+  // ---------------------------------------------------------------- partial to shared memory, sum, store
+  // part[token][weight row] takes the place of the stages, which have all been consumed.
+  if (have) {
+    const int q = warp & 3;
+    const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    float* part = reinterpret_cast<float*>(smem) + 32 * q + lane;
+    for (int c0 = 0; c0 < ntok; c0 += 32) {      // (whole chunks: the rows past ntok are not read)
+      uint32_t r[32], o[32];
+      tmem_ld_x32(quad + c0, r);
+      if (p.issuers == 2) tmem_ld_x32(quad + p.acc_stride + c0, o);
+      tmem_wait_ld_regs(r);
+      if (p.issuers == 2) {
+        tmem_wait_ld_regs(o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[(c0 + j) * kTileW] = __uint_as_float(r[j]);
+    }
+  }
+  tc_fence_before();
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+  if (*abort_flag == 0) {
+    const int j0 = ntok * rank / p.split, j1 = ntok * (rank + 1) / p.split, n0 = nt * kTileW;
+    const uint32_t part = smem_u32(smem);
+    switch (p.split) {
+      case 1: sum_and_store<OUT, 1, 4>(p, part, n0, tok0, j0, j1); break;
+      case 2: sum_and_store<OUT, 2, 4>(p, part, n0, tok0, j0, j1); break;
+      case 4: sum_and_store<OUT, 4, 2>(p, part, n0, tok0, j0, j1); break;
+      default: sum_and_store<OUT, 8, 1>(p, part, n0, tok0, j0, j1); break;
+    }
+  }
+  // a CTA's shared memory stays until every CTA of the cluster has read it
+  if (p.split > 1) cluster_sync();
+}
+
+// ---------------------------------------------------------------- CTA pairs: 256 x up to 256 output tiles
+constexpr int kPairW = 256;                                // weight rows of a tile (MMA M), 128 per CTA
+constexpr int kPairMaxTok = 256;                           // tokens of a tile (MMA N), half staged by each CTA
+constexpr int kPairMaxStages = 6;                          // a stage is two K-blocks of both operands
+// warps: 0 weight loads, 1 waiter, 2 and 3 token loads and MMA issuer, 4-11 epilogue, 12 second issuer
+constexpr int kPairWaiter = 1, kPairTokLoads = 2, kPairIssuer = 3, kPairIssuer2 = 12;
+constexpr int kPairBarBytes = 256;
+
+struct PairArgs {
+  Epilogue e;
+  int M, N, nkb;
+  int tiles_m, tiles_n;      // token tiles, weight tiles
+  int tok, acc_cols;         // tokens of a tile (a multiple of 16); columns of an accumulator
+  int accs, stages;          // accumulators (of every issuer), stages
+  uint32_t idesc;
+  int withhold;
+  int* err;
+};
+
+// Executed by the whole warp, issued by the lane whose `lead` is non-zero.
+__device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// 32 tokens of one weight row per lane -> y.  Two neighbouring lanes exchange halves, so that a lane holds two
+// neighbouring rows of one token (16-bit types).
+template <int OUT>
+__device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], float bias, int64_t row, int rows, int n, int N) {
+  const int odd = n & 1;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] += bias;
+  activate(v, e.act);
+  if (OUT == BSF_TYPE_F32 || !e.wide) {
+    if (n >= N) return;
+    if (e.residual) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < rows) v[j] += residual_at<OUT>(e, (row + j) * e.ldr + n);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < rows) store_at<OUT>(e, (row + j) * e.ldy + n, v[j]);
+    return;
+  }
+  // (N is even, so both rows of a word exist or neither does)
+  uint32_t w[16];
+  if (e.residual) {
+    const uint16_t* from = static_cast<const uint16_t*>(e.residual) + (row + odd) * e.ldr + (n & ~1);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      w[j] = 0u;
+      if (2 * j + odd < rows && n < N) w[j] = *reinterpret_cast<const uint32_t*>(from + 2 * j * e.ldr);
+    }
+  }
+  uint16_t* to = static_cast<uint16_t*>(e.y) + (row + odd) * e.ldy + (n & ~1);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float v0 = v[2 * j], v1 = v[2 * j + 1];
+    const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+    v0 = odd ? x : v0;
+    v1 = odd ? v1 : x;
+    if (e.residual) {
+      const float2 r = unpack2<OUT>(w[j]);
+      v0 += r.x;
+      v1 += r.y;
+    }
+    if (2 * j + odd < rows && n < N) *reinterpret_cast<uint32_t*>(to + 2 * j * e.ldy) = pack2<OUT>(v0, v1);
+  }
+}
+
+template <int OUT, int kIssuers>
+__global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                       const PairArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int half_tok = p.tok >> 1;
+  // a stage: 128 weight rows of two K-blocks, then half of the tile's tokens of the same two
+  const int tok_bytes = half_tok * kRowBytes;
+  const int stage_bytes = 2 * (kTileW * kRowBytes + tok_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);          // used in rank 0
+  uint64_t* empty = full + kPairMaxStages;
+  uint64_t* acc_full = empty + kPairMaxStages;
+  uint64_t* acc_empty = acc_full + 2;                                                   // used in rank 0
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int total = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < p.accs; ++s) {
+      mbar_init(&acc_full[s], kIssuers);
+      mbar_init(&acc_empty[s], 16);
+    }
+    mbar_init(mma_done, kIssuers);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_w);
+    tma_prefetch_desc(&tmap_x);
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == kPairIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();                           // barriers of both CTAs are initialised
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t set_cols = kIssuers * p.acc_cols;          // of a set of accumulators, one per issuer
+
+  if (warp == 0 || warp == kPairTokLoads) {
+    // ------------------------------------------------------------ loads (each CTA its halves), a warp per operand
+    // (where K has an odd number of blocks the last stage's second half is loaded, as zeros, but not multiplied)
+    if (lane == 0) {
+      const bool weights = warp == 0;
+      uint32_t stage = 0, phase = 0;
+      int issued = 0;
+      bool ok = !p.withhold;
+      for (int t = pair; t < total && ok; t += npairs) {
+        const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+        const int row = weights ? (tn * 2 + static_cast<int>(rank)) * kTileW : tm * p.tok + static_cast<int>(rank) * half_tok;
+        const CUtensorMap* map = weights ? &tmap_w : &tmap_x;
+        const int offset = weights ? 0 : 2 * kTileW * kRowBytes, block = weights ? kTileW * kRowBytes : tok_bytes;
+        for (int kb = 0; kb < p.nkb; kb += 2) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
+          const uint32_t bar = map_rank(smem_u32(&full[stage]), 0);
+          uint8_t* dst = smem + stage * stage_bytes + offset;
+          if (weights && rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
+          pair_load_2d(dst, map, bar, kb * kBlockK, row);
+          pair_load_2d(dst + block, map, bar, (kb + 1) * kBlockK, row);
+          ++issued;
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (rank == 0) {
+        // both CTAs' loads complete on these barriers; rank 1 waits for rank 0 at the last cluster barrier
+        const int outstanding = min(issued, p.stages);
+        for (int j = 0; j < outstanding; ++j) {
+          if (stage == 0) { stage = p.stages; phase ^= 1u; }
+          --stage;
+          wait_quiet(&full[stage], phase);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPairIssuer || warp >= kPairIssuer2) {
+    // ------------------------------------------------------------ MMA issuers (rank 0)
+    // An issuing thread reads no shared memory between stages: the waiter warp does every wait and hands each stage
+    // over through a named barrier whose OR-reduced predicate carries an abort.  With two issuers the stages of
+    // a tile go to them in turn, each into an accumulator of its own (narrow tiles are bound by the issue of MMAs).
+    const int me = warp == kPairIssuer ? 0 : 1;
+    if (rank == 0) {
+      const uint32_t lead = lane == 0;
+      uint32_t stage = 0, acc = 0;                     // stage: of the tile's next two K-blocks, whoever takes them
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        const uint32_t d_tmem = tmem_base + acc * set_cols + me * p.acc_cols;
+        uint32_t first = 1;
+        for (int kb = 0; kb < p.nkb; kb += 2) {
+          if (kIssuers == 1 || ((kb >> 1) & 1) == me) {
+            if (named_barrier_or(1 + me, 64, false)) { ok = false; break; }
+            tc_fence_after();
+            const uint8_t* src = smem + stage * stage_bytes;
+            uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
+            uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + 2 * kTileW * kRowBytes));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pair_mma_f16(d_tmem, adesc + 2 * k, bdesc + 2 * k, p.idesc, k == 0 ? first ^ 1u : 1u, lead);
+            first = 0;
+            if (kb + 1 < p.nkb) {
+              adesc += kTileW * kRowBytes >> 4;
+              bdesc += tok_bytes >> 4;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) pair_mma_f16(d_tmem, adesc + 2 * k, bdesc + 2 * k, p.idesc, 1, lead);
+            }
+            pair_commit(&empty[stage], lead);
+          }
+          if (++stage == static_cast<uint32_t>(p.stages)) stage = 0;
+        }
+        if (!ok) break;
+        pair_commit(&acc_full[acc], lead);
+        if (++acc == static_cast<uint32_t>(p.accs)) acc = 0;
+      }
+      pair_commit(mma_done, lead);
+      if (lane == 0) wait_quiet(mma_done, 0);
+    }
+    __syncwarp();
+  } else if (warp == kPairWaiter) {
+    // ------------------------------------------------------------ waiter (rank 0): the issuers' waits, in their order
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool good = true;
+      int t = pair, kb = 0;
+      while (t < total) {
+        good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
+        for (kb = 0; kb < p.nkb; kb += 2) {
+          if (good) good = wait_all(&full[stage], phase, abort_flag, p.err);
+          if (!good) break;
+          named_barrier_or(kIssuers == 1 ? 1 : 1 + ((kb >> 1) & 1), 64, false);
+          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+        }
+        if (!good) break;
+        if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
+        t += npairs;
+      }
+      if (!good) {
+        // the issuer of this stage is at its barrier or on its way to it, and so is the other one if any later
+        // stage is its own (with two issuers every tile has stages of both)
+        const int me = kIssuers == 1 ? 0 : (kb >> 1) & 1;
+        named_barrier_or(1 + me, 64, true);
+        if (kIssuers == 2 && (kb + 2 < p.nkb || t + npairs < total)) named_barrier_or(2 - me, 64, true);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue: lane = weight row, 32 tokens at a time
+    // two warps share a quadrant's tokens
+    const int q = warp & 3, ew = warp - 4;
+    const int nc = (p.tok + 31) >> 5, c_first = ew < 4 ? 0 : (nc + 1) >> 1, c_last = ew < 4 ? (nc + 1) >> 1 : nc;
+    uint32_t acc = 0, acc_phase = 0;
+    for (int t = pair; t < total; t += npairs) {
+      const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+      const int n = tn * kPairW + static_cast<int>(rank) * kTileW + 32 * q + lane;
+      const int64_t tok0 = static_cast<int64_t>(tm) * p.tok;
+      const int rows = min(p.tok, p.M - static_cast<int>(tok0));
+      const float bias = p.e.bias && n < p.N ? load_as_float(p.e.bias, n, p.e.bias_type) : 0.f;
+      if (!wait_all(&acc_full[acc], acc_phase, abort_flag, p.err)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * set_cols;
+      if (c_first == c_last) {              // (a tile of 32 tokens has nothing for the second warp)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
+      }
+      for (int c = c_first; c < c_last; ++c) {
+        uint32_t r[32];
+        float v[32];
+        tmem_ld_x32(taddr + 32 * c, r);
+        tmem_wait_ld_regs(r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        if (kIssuers == 2) {
+          tmem_ld_x32(taddr + p.acc_cols + 32 * c, r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+        }
+        if (c == c_last - 1) {              // the accumulator's last columns are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
+        }
+        if (32 * c < rows) finish<OUT>(p.e, v, bias, tok0 + 32 * c, min(32, rows - 32 * c), n, p.N);
+      }
+      if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
+    }
+    // the issuers' last commits have reached this CTA's barriers too, so none arrives after it exits
+    if (warp == 4 && lane == 0) wait_quiet(mma_done, 0);
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync();                           // no load, MMA or remote arrival of the pair is outstanding
+  if (warp == kPairIssuer) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+  }
+}
+
+// 2-D tensor of 16-bit elements [rows, cols] (row pitch ld elements), box {64 cols, box_rows}, 128-byte swizzle; what
+// lies past the edges reads as zeros.
+bool make_map_16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {kBlockK, box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// kind::f16, FP32 accumulator, both operands of the same type (0 fp16, 1 bf16), K-major
+uint32_t idesc_16(bool bf16, int m, int n) {
+  const uint32_t type = bf16 ? 1u : 0u;
+  return 1u << 4 | type << 7 | type << 10 | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
+}
+
+template <int OUT>
+const void* kernel_of(int form) {                  // 0 split, 1 and 2 pairs with so many issuers
+  return form == 0   ? reinterpret_cast<const void*>(linear_split_kernel<OUT>)
+         : form == 1 ? reinterpret_cast<const void*>(linear_pair_kernel<OUT, 1>)
+                     : reinterpret_cast<const void*>(linear_pair_kernel<OUT, 2>);
+}
+const void* kernel_of(int out, int form) {
+  return out == BSF_TYPE_F32    ? kernel_of<BSF_TYPE_F32>(form)
+         : out == BSF_TYPE_BF16 ? kernel_of<BSF_TYPE_BF16>(form)
+                                : kernel_of<BSF_TYPE_F16>(form);
+}
+
+// Once per device: all kernels may use all shared memory, and the number of CTAs of the split kernel that run at
+// once, one per SM, in clusters of 1, 2, 4 and 8 (a cluster lives in one GPC, so 8 leave SMs idle).
+struct LinearLimits {
+  std::atomic<int> ctas[4];
+  std::atomic<bool> ready;
+};
+bsf_status linear_limits(const LinearLimits** out) {
+  static LinearLimits limits[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return BSF_ERR_CUDA;
+  LinearLimits& l = limits[dev];
+  if (!l.ready.load(std::memory_order_acquire)) {      // (racing first calls store the same values)
+    for (int type : {BSF_TYPE_F32, BSF_TYPE_BF16, BSF_TYPE_F16})
+      for (int form = 0; form < 3; ++form) {
+        const void* k = kernel_of(type, form);
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+                cudaSuccess)
+          return BSF_ERR_CUDA;
+      }
+    for (int i = 0; i < 4; ++i) {
+      DependentLaunch launch(8u << i, kThreads, kSmemBytes, nullptr, 1u << i);
+      launch.cfg.numAttrs = 1;                           // the cluster alone
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel_of(BSF_TYPE_F32, 0), &launch.cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return BSF_ERR_CUDA;
+      }
+      l.ctas[i].store(n << i, std::memory_order_relaxed);
+    }
+    l.ready.store(true, std::memory_order_release);
+  }
+  *out = &l;
+  return BSF_OK;
+}
+
+// Which kernel a product takes, by the time each would need (nanoseconds).
+struct Plan {
+  bool pair;
+  int tok;                  // pairs: tokens per tile; split: most tokens per tile
+  int split;
+};
+Plan choose_plan(int64_t M, int64_t N, int64_t nkb, const LinearLimits& limits) {
+  const int64_t ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
+  Plan best = {false, 64, 1};
+  int64_t least = INT64_MAX;
+  for (int tok = 64; tok <= kMaxTok; tok += 64) {
+    if (tok > 64 && M <= 64) break;
+    const int64_t chunks = (M + tok - 1) / tok, per = ((M + chunks - 1) / chunks + 15) / 16 * 16;
+    for (int i = 0; i < 4; ++i) {
+      const int64_t split = int64_t(1) << i, ctas = ntn * chunks * split;
+      if (i > 0 && (nkb < 2 * split || ctas > 2 * sms)) break;
+      const int64_t at_once = limits.ctas[i].load(std::memory_order_relaxed), kbs = (nkb + split - 1) / split;
+      const int64_t load = (ctas + at_once - 1) / at_once;              // CTAs of the busiest SM
+      int64_t ns = 3100 + 6 * per + (i > 0 ? 400 + 400 * i : 0);
+      if (per > 64)         // one CTA per SM: it cannot start under its predecessor
+        ns += 800 + load * kbs * 270 + (load - 1) * 4700;
+      else                  // two CTAs on an SM share its 120 bytes a nanosecond from L2
+        ns += kbs * (load / 2 * (273 + 32 * per / 15) + load % 2 * 270) + (load - 1) * 1150;
+      if (ns < least) {
+        least = ns;
+        best = {false, tok, static_cast<int>(split)};
+      }
+    }
+  }
+  for (int tok = kPairMaxTok; tok >= 64; tok -= 16) {
+    const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
+    const int64_t multiply = (tok <= kMaxTok ? 40 : 36) * tok / 16, issue = tok <= kMaxTok ? 320 : 470;
+    const int64_t ns = 4600 + waves * ((nkb + 1) / 2 * (issue > multiply ? issue : multiply) + 13 * tok);
+    if (ns < least) {
+      least = ns;
+      best = {true, tok, 1};
+    }
+  }
+  return best;
+}
+
+size_t size_of(int type) { return type == BSF_TYPE_F32 ? 4 : 2; }
+bool known(int type) { return type == BSF_TYPE_F32 || type == BSF_TYPE_BF16 || type == BSF_TYPE_F16; }
+
+}  // namespace
+}  // namespace bsf
+
+using namespace bsf;
+
+extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, int64_t ldx, const void* w, int64_t N,
+                                 int64_t ldw, const void* bias, int bias_type, int activation, const void* residual,
+                                 int64_t ldr, void* y, int y_type, int64_t ldy, int flags, bsf_stream_t stream) {
+  if (T < 0 || N <= 0 || K <= 0) return BSF_ERR_INVALID_ARGUMENT;
+  if ((type != BSF_TYPE_BF16 && type != BSF_TYPE_F16) || !known(y_type) || (bias && !known(bias_type)))
+    return BSF_ERR_INVALID_ARGUMENT;
+  if (activation < BSF_ACT_NONE || activation > BSF_ACT_SIGMOID) return BSF_ERR_INVALID_ARGUMENT;
+  if (flags & ~BSF_DEBUG_WITHHOLD_LOADS) return BSF_ERR_INVALID_ARGUMENT;
+  if (T == 0) return BSF_OK;
+  if (!x || !w || !y) return BSF_ERR_INVALID_ARGUMENT;
+  if (ldx < K || ldw < K || ldy < N || (residual && ldr < N)) return BSF_ERR_INVALID_ARGUMENT;
+  const size_t ysize = size_of(y_type);
+  if (!aligned16(x) || !aligned16(w) || ldx % 8 || ldw % 8 || reinterpret_cast<uintptr_t>(y) % ysize ||
+      reinterpret_cast<uintptr_t>(residual) % ysize || (bias && reinterpret_cast<uintptr_t>(bias) % size_of(bias_type)))
+    return BSF_ERR_MISALIGNED;
+  if (!fits_rows(T, ldx) || !fits_rows(T, ldy) || (residual && ldr > kMaxRowWidth) || N > kMaxRowWidth ||
+      ldw > kMaxRowWidth || T > kMaxRows - 256)
+    return BSF_ERR_UNSUPPORTED;
+  const int64_t ntn = (N + kTileW - 1) / kTileW, nkb = (K + kBlockK - 1) / kBlockK;
+  int* err = device_error_ptr();
+  if (!err) return BSF_ERR_CUDA;
+  const bool withhold = (flags & BSF_DEBUG_WITHHOLD_LOADS) != 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const LinearLimits* limits;
+  const bsf_status st = linear_limits(&limits);
+  if (st != BSF_OK) return st;
+  const Plan plan = choose_plan(T, N, nkb, *limits);
+  Epilogue e;
+  e.bias = bias;
+  e.residual = residual;
+  e.ldr = ldr;
+  e.y = y;
+  e.ldy = ldy;
+  e.bias_type = bias_type;
+  e.act = activation;
+  const int64_t group = plan.pair ? 2 : 4;             // elements stored together
+  e.wide = reinterpret_cast<uintptr_t>(y) % (group * ysize) == 0 && ldy % group == 0 &&
+           (!residual || (reinterpret_cast<uintptr_t>(residual) % (group * ysize) == 0 && ldr % group == 0)) &&
+           (!plan.pair || N % 2 == 0);
+  CUtensorMap map_w, map_x;
+  if (!make_map_16(&map_w, w, N, K, ldw, kTileW)) return BSF_ERR_CUDA;
+
+  if (plan.pair) {
+    const int tok = plan.tok;
+    const int64_t tiles_m = (T + tok - 1) / tok, tiles_n = (ntn + 1) / 2, tiles = tiles_m * tiles_n;
+    if (tiles > INT32_MAX) return BSF_ERR_UNSUPPORTED;
+    PairArgs p;
+    p.e = e;
+    p.M = static_cast<int>(T);
+    p.N = static_cast<int>(N);
+    p.nkb = static_cast<int>(nkb);
+    p.tiles_m = static_cast<int>(tiles_m);
+    p.tiles_n = static_cast<int>(tiles_n);
+    p.tok = tok;
+    p.acc_cols = (tok + 31) / 32 * 32;
+    // (each issuer needs a stage of every tile)
+    const int issuers = tok <= kMaxTok && nkb > 2 ? 2 : 1;
+    p.accs = 2;                                        // (2 x 2 x 128 or 2 x 256 columns)
+    p.idesc = idesc_16(type == BSF_TYPE_BF16, kPairW, tok);
+    p.withhold = withhold;
+    p.err = err;
+    const int stage_bytes = 2 * (kTileW + tok / 2) * kRowBytes;
+    p.stages = (kSmemBytes - 1024 - kPairBarBytes) / stage_bytes;
+    if (p.stages > kPairMaxStages) p.stages = kPairMaxStages;
+    if (!make_map_16(&map_x, x, T, K, ldx, tok / 2)) return BSF_ERR_CUDA;
+    const int64_t pairs = sm_count() / 2, used = tiles < pairs ? tiles : pairs;
+    void* args[] = {&map_w, &map_x, &p};
+    return launch_cluster(kernel_of(y_type, issuers), static_cast<unsigned>(2 * used), 32 * (11 + issuers), kSmemBytes, 2, s,
+                          args);
+  }
+
+  const int64_t chunks = (T + plan.tok - 1) / plan.tok, tiles = ntn * chunks;
+  if (tiles * plan.split > INT32_MAX) return BSF_ERR_UNSUPPORTED;
+  SplitArgs p;
+  p.e = e;
+  p.M = static_cast<int>(T);
+  p.N = static_cast<int>(N);
+  p.nkb = static_cast<int>(nkb);
+  p.chunks = static_cast<int>(chunks);
+  // equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * tok < T)
+  p.per = static_cast<int>(((T + chunks - 1) / chunks + 15) / 16 * 16);
+  p.split = plan.split;
+  const int stage_bytes = (kTileW + p.per) * kRowBytes;
+  const size_t smem = p.per <= 64 ? kHalfSmemBytes : kSmemBytes;
+  p.stages = (static_cast<int>(smem) - 1024 - kBarBytes) / stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.acc_stride = (p.per + 31) / 32 * 32;
+  // (an issuer without a K-block would leave its accumulator unwritten)
+  p.issuers = nkb / p.split >= kMaxIssuers ? kMaxIssuers : 1;
+  p.stages = p.stages / p.issuers * p.issuers;
+  const int cols = p.issuers * p.acc_stride;
+  p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+  p.idesc = idesc_16(type == BSF_TYPE_BF16, kTileW, p.per);
+  p.withhold = withhold;
+  p.err = err;
+  if (!make_map_16(&map_x, x, T, K, ldx, p.per)) return BSF_ERR_CUDA;
+  void* args[] = {&map_w, &map_x, &p};
+  return launch_cluster(kernel_of(y_type, 0), static_cast<unsigned>(tiles * p.split), kThreads, smem,
+                        static_cast<unsigned>(p.split), s, args);
+}

@@ -430,7 +430,9 @@ GATE_SIGMOID = 0x1
 GATE_GROUP_TOP2 = 0x2
 GATE_RENORMALISE = 0x4
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}       # BSF_TYPE_F32, BSF_TYPE_BF16
-TYPE_E4M3 = 2
+TYPE_E4M3 = 2                                        # BSF_TYPE_E4M3
+_LINEAR_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 3}       # BSF_TYPE_F32, _BF16, _F16
+_ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 _SCORES = {"softmax": 0, "sigmoid": GATE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": GATE_GROUP_TOP2}
 
@@ -742,3 +744,58 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
     if status:
         _lib.check(status, "few_token_moe")
     return z
+
+
+def linear(x, w, bias=None, activation=None, residual=None, out=None, out_dtype=None, flags=0, stream=None):
+    """act(x w^T + bias) + residual: x [T, K] and w [N, K] both bf16 or both fp16 (row strides multiples of 8) -> out
+    [T, N] of ``out_dtype`` float32, bf16 or fp16 (default: that of ``out``, else x's).  ``bias`` [N] of any of the
+    three types, ``activation`` None, "relu", "silu", "gelu", "gelu_tanh" or "sigmoid", ``residual`` [T, N] of the
+    output's type (it may be ``out``).  One rounding, of the float32 result."""
+    T, K = _two_dims(x, "x")
+    N, Kw = _two_dims(w, "w")
+    kind = x.dtype
+    if kind not in (_BF16, torch.float16):
+        raise ValueError(f"x: expected bfloat16 or float16, got {kind}")
+    if w.dtype != kind or Kw != K:
+        raise ValueError(f"w: expected {kind} [N, {K}], got {w.dtype} {tuple(w.shape)}")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r}: expected one of {[a for a in _ACTIVATIONS if a]}")
+    if out_dtype is None:
+        out_dtype = kind if out is None else out.dtype
+    y_type = _LINEAR_TYPES.get(out_dtype)
+    if y_type is None:
+        raise ValueError(f"out: expected float32, bfloat16 or float16, got {out_dtype}")
+    ldx, ldw = _row_stride(x, T, K, "x"), _row_stride(w, N, K, "w")
+    shape = (T, N)
+    if out is None:
+        out = _empty(shape, out_dtype, x, stream)
+    elif out.dtype != out_dtype or out.shape != shape:
+        _refuse(out, out_dtype, shape, "out")
+    ldy = _row_stride(out, T, N, "out")
+    ldr = bias_type = 0
+    if bias is not None:
+        bias_type = _LINEAR_TYPES.get(bias.dtype)
+        if bias_type is None:
+            raise ValueError(f"bias: expected float32, bfloat16 or float16, got {bias.dtype}")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            _refuse(bias, bias.dtype, (N,), "bias")
+    if residual is not None:
+        if residual.dtype != out_dtype or residual.shape != shape:
+            _refuse(residual, out_dtype, shape, "residual")
+        ldr = _row_stride(residual, T, N, "residual")
+    device = x.get_device()
+    if (device < 0 or w.get_device() != device or out.get_device() != device
+            or (bias is not None and bias.get_device() != device)
+            or (residual is not None and residual.get_device() != device)
+            or device != _current_device() or (stream is not None and stream.device_index != device)):
+        _refuse_devices("x w bias residual out", (x, w, bias, residual, out), stream)
+    if stream is not None:
+        _used_on(stream, x, w, bias, residual, out)
+    status = _lib.load().bsf_linear(
+        x.data_ptr(), _LINEAR_TYPES[kind], T, K, ldx, w.data_ptr(), N, ldw, None if bias is None else bias.data_ptr(),
+        bias_type, act, None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), y_type, ldy, flags,
+        _current_stream(device) if stream is None else stream.cuda_stream)
+    if status:
+        _lib.check(status, "linear")
+    return out

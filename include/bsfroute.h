@@ -539,6 +539,7 @@ bsf_status bsf_grouped_gemm_f32sf_masked(const uint8_t* a, const float* sfa, int
 #define BSF_TYPE_F32 0
 #define BSF_TYPE_BF16 1
 #define BSF_TYPE_E4M3 2
+#define BSF_TYPE_F16 3
 
 /* bsf_gate flags. */
 #define BSF_GATE_SIGMOID 0x1     /* score = sigmoid(logit); otherwise softmax over the usable experts */
@@ -672,6 +673,39 @@ bsf_status bsf_few_token_moe(const void* x, int64_t T, int64_t K, int64_t ldx, c
                              const void* w13_shared, const int32_t* sfb13_shared, const void* w2_shared,
                              const int32_t* sfb2_shared, const void* addend, int64_t ldc, void* z, int64_t ldz,
                              void* workspace, size_t workspace_bytes, int flags, bsf_stream_t stream);
+
+/* bsf_linear activations. */
+#define BSF_ACT_NONE 0
+#define BSF_ACT_RELU 1
+#define BSF_ACT_SILU 2       /* v / (1 + exp(-v)) */
+#define BSF_ACT_GELU 3       /* v / 2 (1 + erf(v / sqrt 2)) */
+#define BSF_ACT_GELU_TANH 4  /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+#define BSF_ACT_SIGMOID 5    /* 1 / (1 + exp(-v)) */
+
+/*
+ * bsf_linear — Y[t, n] = act( sum_k X[t, k] W[n, k] + bias[n] ) + R[t, n] on
+ * unquantised operands: the router's logits, a projection added to the
+ * residual stream, a layer of a dense network.
+ *   x         [T, K], row stride ldx >= K elements; w [N, K], row stride ldw
+ *             >= K; both of `type` BSF_TYPE_BF16 or BSF_TYPE_F16.
+ *   bias      [N] of bias_type BSF_TYPE_F32, BF16 or F16, or NULL.
+ *   residual  [T, N] of y's type, row stride ldr >= N, or NULL: added after
+ *             the activation.  It may be y itself.
+ *   y         [T, N] (output) of y_type BSF_TYPE_F32, BF16 or F16, row stride
+ *             ldy >= N; nothing else is written.
+ * FP32 accumulation on the tensor cores; bias, activation and residual in
+ * float32 on the sum, then one rounding (to nearest even) to y's type.  The order
+ * of sums is fixed: results are bit-identical from run to run.  Infinities
+ * and NaN go through the arithmetic as they are.  x and w 16-byte aligned, ldx
+ * and ldw multiples of 8 (K may be any number); y, residual and bias need only
+ * their element alignment (four elements together are faster).  flags: 0, or
+ * BSF_DEBUG_WITHHOLD_LOADS as for the other products.  T == 0 is a no-op.  No
+ * workspace; asynchronous on stream.  A wait that runs out sets
+ * BSF_DEVERR_TIMEOUT.
+ */
+bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, int64_t ldx, const void* w, int64_t N,
+                      int64_t ldw, const void* bias, int bias_type, int activation, const void* residual, int64_t ldr,
+                      void* y, int y_type, int64_t ldy, int flags, bsf_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,4 +29,4 @@ values the pages print, closed forms, library routines or brute force, except
 the GPU-internal FP32 accumulation order, which is outside the oracle.
 """
 
-from . import formats, quantise, route, gemm, combine, checks, nvfp4, bf16, f32sf, gate, swiglu, block, few_tokens  # noqa: F401
+from . import formats, quantise, route, gemm, combine, checks, nvfp4, bf16, f32sf, gate, swiglu, block, few_tokens, linear  # noqa: F401
