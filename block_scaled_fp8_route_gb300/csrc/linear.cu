@@ -86,8 +86,34 @@ __device__ __forceinline__ void store_at(const Epilogue& e, int64_t i, float v) 
   else static_cast<uint16_t*>(e.y)[i] = static_cast<uint16_t>(pack2<OUT>(v, 0.f));
 }
 
-// Each activation of N values, in float32 within a few units in the last place of it (relative: the tails of gelu
-// and of the sigmoids are not differences).  A quotient by more than 2**126 is 0, where the exact one is below 2**-119.
+__device__ __forceinline__ float exp2_approx(float x) {      // 2**x to 2 units in the last place (0 below 2**-126)
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// exp(x) with a rounded argument: off by |x| 2**-24 of it
+__device__ __forceinline__ float exp_of(float x) { return exp2_approx(x * 1.4426950408889634f); }
+
+// erfc(|v| / sqrt 2) / 2: with x = |v| / sqrt 2, exp(-x^2) times a polynomial in t = 1 / (1 + 0.3021286 x), a minimax
+// fit (Lawson's iteration) of erfc(x) exp(x^2) on 0 .. 14 relative to it, off by 2.9e-8.  erfcf would be 2.5 times as
+// many instructions, and a tile's epilogue is not always hidden behind other tiles' products.
+__device__ __forceinline__ float half_erfc(float a) {
+  const float t = __fdividef(1.f, fmaf(a, 0.21363720167f, 1.f));
+  float q = -0.11995414206527316f;
+  q = fmaf(q, t, 0.4315029982598405f);
+  q = fmaf(q, t, -0.4179198212295966f);
+  q = fmaf(q, t, 0.4548883512025796f);
+  q = fmaf(q, t, -0.03962212128188006f);
+  q = fmaf(q, t, 0.19541278265418394f);
+  q = fmaf(q, t, 0.15392502081132817f);
+  q = fmaf(q, t, 0.1713477909787805f);
+  q = fmaf(q, t, 0.17041911225827286f);
+  return 0.5f * t * q * exp2_approx(a * a * -0.72134752044448170f);
+}
+
+// Each activation of N values, in float32 within a few units in the last place of it plus what a rounded argument of
+// exp makes (relative: the tails of gelu and of the sigmoids are not differences).  A quotient by more than 2**126 is 0,
+// where the exact one is below 2**-119.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
@@ -97,22 +123,25 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
       break;
     case BSF_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.f + expf(-v[i]));
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.f + exp_of(-v[i]));
       break;
-    case BSF_ACT_GELU:
+    case BSF_ACT_GELU:                  // max(v, 0) - |v| erfc(|v| / sqrt 2) / 2, whose second term is 0 from 20 on
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
+      for (int i = 0; i < N; ++i) {
+        const float a = fminf(fabsf(v[i]), 20.f);
+        v[i] = fmaf(-a, half_erfc(a), v[i] < 0.f ? 0.f : v[i]);
+      }
       break;
     case BSF_ACT_GELU_TANH:             // 0.5 v (1 + tanh(u)) = v / (1 + exp(-2 u)), u = sqrt(2 / pi) (v + 0.044715 v^3)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float u2 = v[i] * (1.5957691216057308f + 0.07135481627364643f * v[i] * v[i]);
-        v[i] = __fdividef(v[i], 1.f + expf(-u2));
+        v[i] = __fdividef(v[i], 1.f + exp_of(-u2));
       }
       break;
     case BSF_ACT_SIGMOID:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __fdividef(1.f, 1.f + expf(-v[i]));
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(1.f, 1.f + exp_of(-v[i]));
       break;
     default:
       break;
@@ -342,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ---------------------------------------------------------------- CTA pairs: 256 x up to 256 output tiles
 constexpr int kPairW = 256;                                // weight rows of a tile (MMA M), 128 per CTA
 constexpr int kPairMaxTok = 256;                           // tokens of a tile (MMA N), half staged by each CTA
-constexpr int kPairMaxStages = 6;                          // a stage is two K-blocks of both operands
+constexpr int kPairMaxStages = 8;                          // a stage is one or two K-blocks of both operands
+constexpr int kSegment = 1024;                             // values of K that a float32 output's sum takes at once
 // warps: 0 weight loads, 1 waiter, 2 and 3 token loads and MMA issuer, 4-11 epilogue, 12 second issuer
 constexpr int kPairWaiter = 1, kPairTokLoads = 2, kPairIssuer = 3, kPairIssuer2 = 12;
 constexpr int kPairBarBytes = 256;
@@ -352,7 +382,8 @@ struct PairArgs {
   int M, N, nkb;
   int tiles_m, tiles_n;      // token tiles, weight tiles
   int tok, acc_cols;         // tokens of a tile (a multiple of 16); columns of an accumulator
-  int accs, stages;          // accumulators (of every issuer), stages
+  int stages, blocks;        // stages, K-blocks in one (2: the barriers of narrow tiles cost as much as their MMAs)
+  int nst, segments;         // stages of a tile; runs of them with a sum of their own
   uint32_t idesc;
   int withhold;
   int* err;
@@ -369,6 +400,9 @@ __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, u
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
 }
+
+// One past the last stage of segment i.
+__device__ __forceinline__ int segment_end(const PairArgs& p, int i) { return p.nst * (i + 1) / p.segments; }
 
 // 32 tokens of one weight row per lane -> y.  Two neighbouring lanes exchange halves, so that a lane holds two
 // neighbouring rows of one token (16-bit types).
@@ -423,9 +457,9 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int half_tok = p.tok >> 1;
-  // a stage: 128 weight rows of two K-blocks, then half of the tile's tokens of the same two
+  // a stage: 128 weight rows of its K-blocks, then half of the tile's tokens of the same
   const int tok_bytes = half_tok * kRowBytes;
-  const int stage_bytes = 2 * (kTileW * kRowBytes + tok_bytes);
+  const int stage_bytes = p.blocks * (kTileW * kRowBytes + tok_bytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);          // used in rank 0
   uint64_t* empty = full + kPairMaxStages;
   uint64_t* acc_full = empty + kPairMaxStages;
@@ -444,7 +478,7 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < p.accs; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], kIssuers);
       mbar_init(&acc_empty[s], 16);
     }
@@ -470,7 +504,7 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
 
   if (warp == 0 || warp == kPairTokLoads) {
     // ------------------------------------------------------------ loads (each CTA its halves), a warp per operand
-    // (where K has an odd number of blocks the last stage's second half is loaded, as zeros, but not multiplied)
+    // (where a stage is two K-blocks and K has an odd number the last one's second half is zeros, and not multiplied)
     if (lane == 0) {
       const bool weights = warp == 0;
       uint32_t stage = 0, phase = 0;
@@ -480,14 +514,14 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
         const int tm = t % p.tiles_m, tn = t / p.tiles_m;
         const int row = weights ? (tn * 2 + static_cast<int>(rank)) * kTileW : tm * p.tok + static_cast<int>(rank) * half_tok;
         const CUtensorMap* map = weights ? &tmap_w : &tmap_x;
-        const int offset = weights ? 0 : 2 * kTileW * kRowBytes, block = weights ? kTileW * kRowBytes : tok_bytes;
-        for (int kb = 0; kb < p.nkb; kb += 2) {
+        const int offset = weights ? 0 : p.blocks * kTileW * kRowBytes, block = weights ? kTileW * kRowBytes : tok_bytes;
+        for (int kb = 0; kb < p.nkb; kb += p.blocks) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
           const uint32_t bar = map_rank(smem_u32(&full[stage]), 0);
           uint8_t* dst = smem + stage * stage_bytes + offset;
           if (weights && rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
           pair_load_2d(dst, map, bar, kb * kBlockK, row);
-          pair_load_2d(dst + block, map, bar, (kb + 1) * kBlockK, row);
+          if (p.blocks == 2) pair_load_2d(dst + block, map, bar, (kb + 1) * kBlockK, row);
           ++issued;
           if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
         }
@@ -511,23 +545,30 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
     const int me = warp == kPairIssuer ? 0 : 1;
     if (rank == 0) {
       const uint32_t lead = lane == 0;
-      uint32_t stage = 0, acc = 0;                     // stage: of the tile's next two K-blocks, whoever takes them
+      uint32_t stage = 0, acc = 0;                     // stage: of the tile's next K-blocks, whoever takes them
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
-        const uint32_t d_tmem = tmem_base + acc * set_cols + me * p.acc_cols;
         uint32_t first = 1;
-        for (int kb = 0; kb < p.nkb; kb += 2) {
-          if (kIssuers == 1 || ((kb >> 1) & 1) == me) {
+        int segment = 0, end = segment_end(p, 0);
+        for (int st = 0; st < p.nst; ++st) {
+          if (OUT == BSF_TYPE_F32 && st == end) {
+            pair_commit(&acc_full[acc], lead);
+            acc ^= 1u;
+            first = 1;
+            end = segment_end(p, ++segment);
+          }
+          if (kIssuers == 1 || (st & 1) == me) {
             if (named_barrier_or(1 + me, 64, false)) { ok = false; break; }
             tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * set_cols + me * p.acc_cols;
             const uint8_t* src = smem + stage * stage_bytes;
             uint64_t adesc = smem_desc_k_sw128(smem_u32(src));
-            uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + 2 * kTileW * kRowBytes));
+            uint64_t bdesc = smem_desc_k_sw128(smem_u32(src + p.blocks * kTileW * kRowBytes));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               pair_mma_f16(d_tmem, adesc + 2 * k, bdesc + 2 * k, p.idesc, k == 0 ? first ^ 1u : 1u, lead);
             first = 0;
-            if (kb + 1 < p.nkb) {
+            if (p.blocks == 2 && 2 * st + 1 < p.nkb) {
               adesc += kTileW * kRowBytes >> 4;
               bdesc += tok_bytes >> 4;
 #pragma unroll
@@ -539,7 +580,7 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
         }
         if (!ok) break;
         pair_commit(&acc_full[acc], lead);
-        if (++acc == static_cast<uint32_t>(p.accs)) acc = 0;
+        acc ^= 1u;
       }
       pair_commit(mma_done, lead);
       if (lane == 0) wait_quiet(mma_done, 0);
@@ -550,25 +591,29 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool good = true;
-      int t = pair, kb = 0;
+      int t = pair, st = 0;
       while (t < total) {
-        good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
-        for (kb = 0; kb < p.nkb; kb += 2) {
+        int segment = 0, end = 0;
+        for (st = 0; st < p.nst; ++st) {
+          if (st == end) {
+            good = wait_cluster_all(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.err);
+            if ((acc ^= 1u) == 0u) acc_phase ^= 1u;
+            end = segment_end(p, segment++);
+          }
           if (good) good = wait_all(&full[stage], phase, abort_flag, p.err);
           if (!good) break;
-          named_barrier_or(kIssuers == 1 ? 1 : 1 + ((kb >> 1) & 1), 64, false);
+          named_barrier_or(kIssuers == 1 ? 1 : 1 + (st & 1), 64, false);
           if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
         }
         if (!good) break;
-        if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
         t += npairs;
       }
       if (!good) {
         // the issuer of this stage is at its barrier or on its way to it, and so is the other one if any later
         // stage is its own (with two issuers every tile has stages of both)
-        const int me = kIssuers == 1 ? 0 : (kb >> 1) & 1;
+        const int me = kIssuers == 1 ? 0 : st & 1;
         named_barrier_or(1 + me, 64, true);
-        if (kIssuers == 2 && (kb + 2 < p.nkb || t + npairs < total)) named_barrier_or(2 - me, 64, true);
+        if (kIssuers == 2 && (st + 1 < p.nst || t + npairs < total)) named_barrier_or(2 - me, 64, true);
       }
     }
   } else {
@@ -583,35 +628,65 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
       const int64_t tok0 = static_cast<int64_t>(tm) * p.tok;
       const int rows = min(p.tok, p.M - static_cast<int>(tok0));
       const float bias = p.e.bias && n < p.N ? load_as_float(p.e.bias, n, p.e.bias_type) : 0.f;
-      if (!wait_all(&acc_full[acc], acc_phase, abort_flag, p.err)) break;
+      bool ok = wait_all(&acc_full[acc], acc_phase, abort_flag, p.err);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * set_cols;
-      if (c_first == c_last) {              // (a tile of 32 tokens has nothing for the second warp)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
-      }
-      for (int c = c_first; c < c_last; ++c) {
-        uint32_t r[32];
-        float v[32];
-        tmem_ld_x32(taddr + 32 * c, r);
-        tmem_wait_ld_regs(r);
+      const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+      if constexpr (OUT == BSF_TYPE_F32) {
+        // The tensor core cuts the running sum off rather than rounding it, so an error grows with the number of terms
+        // (8192 x 256 x 7168 in one sum per issuer: 3.8e-6 of the result); sums of kSegment values are added here.
+        float v[2][32] = {};
+        for (int s = 0; ok && s < p.segments; ++s) {
+          if (s > 0) ok = wait_all(&acc_full[acc], acc_phase, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (kIssuers == 2) {
-          tmem_ld_x32(taddr + p.acc_cols + 32 * c, r);
-          tmem_wait_ld_regs(r);
+          for (int i = 0; i < 2; ++i) {
+            if (c_first + i >= c_last) break;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
-        }
-        if (c == c_last - 1) {              // the accumulator's last columns are in registers
+            for (int b = 0; b < kIssuers; ++b) {
+              uint32_t r[32];
+              tmem_ld_x32(quad + acc * set_cols + b * p.acc_cols + 32 * (c_first + i), r);
+              tmem_wait_ld_regs(r);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[i][j] += __uint_as_float(r[j]);
+            }
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
+          if ((acc ^= 1u) == 0u) acc_phase ^= 1u;
         }
-        if (32 * c < rows) finish<OUT>(p.e, v, bias, tok0 + 32 * c, min(32, rows - 32 * c), n, p.N);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = 32 * (c_first + i);
+          if (c_first + i < c_last && c < rows) finish<OUT>(p.e, v[i], bias, tok0 + c, min(32, rows - c), n, p.N);
+        }
+      } else {
+        const uint32_t taddr = quad + acc * set_cols;
+        for (int c = c_first; c < c_last; ++c) {
+          uint32_t r[32];
+          float v[32];
+          tmem_ld_x32(taddr + 32 * c, r);
+          tmem_wait_ld_regs(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          if (kIssuers == 2) {
+            tmem_ld_x32(taddr + p.acc_cols + 32 * c, r);
+            tmem_wait_ld_regs(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+          }
+          if (c == c_last - 1) {              // the accumulator's last columns are in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
+          }
+          if (32 * c < rows) finish<OUT>(p.e, v, bias, tok0 + 32 * c, min(32, rows - 32 * c), n, p.N);
+        }
+        if ((acc ^= 1u) == 0u) acc_phase ^= 1u;
       }
-      if (++acc == static_cast<uint32_t>(p.accs)) { acc = 0; acc_phase ^= 1u; }
     }
     // the issuers' last commits have reached this CTA's barriers too, so none arrives after it exits
     if (warp == 4 && lane == 0) wait_quiet(mma_done, 0);
@@ -700,7 +775,7 @@ struct Plan {
   int tok;                  // pairs: tokens per tile; split: most tokens per tile
   int split;
 };
-Plan choose_plan(int64_t M, int64_t N, int64_t nkb, const LinearLimits& limits) {
+Plan choose_plan(int64_t M, int64_t N, int64_t nkb, bool f32, const LinearLimits& limits) {
   const int64_t ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
   Plan best = {false, 64, 1};
   int64_t least = INT64_MAX;
@@ -723,7 +798,7 @@ Plan choose_plan(int64_t M, int64_t N, int64_t nkb, const LinearLimits& limits) 
       }
     }
   }
-  for (int tok = kPairMaxTok; tok >= 64; tok -= 16) {
+  for (int tok = f32 ? kMaxTok : kPairMaxTok; tok >= 64; tok -= 16) {      // (float32 sums live in registers)
     const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
     const int64_t multiply = (tok <= kMaxTok ? 40 : 36) * tok / 16, issue = tok <= kMaxTok ? 320 : 470;
     const int64_t ns = 4600 + waves * ((nkb + 1) / 2 * (issue > multiply ? issue : multiply) + 13 * tok);
@@ -769,7 +844,7 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   const LinearLimits* limits;
   const bsf_status st = linear_limits(&limits);
   if (st != BSF_OK) return st;
-  const Plan plan = choose_plan(T, N, nkb, *limits);
+  const Plan plan = choose_plan(T, N, nkb, y_type == BSF_TYPE_F32, *limits);
   Epilogue e;
   e.bias = bias;
   e.residual = residual;
@@ -800,11 +875,14 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
     p.acc_cols = (tok + 31) / 32 * 32;
     // (each issuer needs a stage of every tile)
     const int issuers = tok <= kMaxTok && nkb > 2 ? 2 : 1;
-    p.accs = 2;                                        // (2 x 2 x 128 or 2 x 256 columns)
+    // (two sets of accumulators: 2 x 2 x 128 or 2 x 256 columns)
+    p.blocks = issuers == 2 ? 2 : 1;
+    p.nst = static_cast<int>((nkb + p.blocks - 1) / p.blocks);
+    p.segments = y_type == BSF_TYPE_F32 ? (p.nst * p.blocks * kBlockK + kSegment - 1) / kSegment : 1;
     p.idesc = idesc_16(type == BSF_TYPE_BF16, kPairW, tok);
     p.withhold = withhold;
     p.err = err;
-    const int stage_bytes = 2 * (kTileW + tok / 2) * kRowBytes;
+    const int stage_bytes = p.blocks * (kTileW + tok / 2) * kRowBytes;
     p.stages = (kSmemBytes - 1024 - kPairBarBytes) / stage_bytes;
     if (p.stages > kPairMaxStages) p.stages = kPairMaxStages;
     if (!make_map_16(&map_x, x, T, K, ldx, tok / 2)) return BSF_ERR_CUDA;
