@@ -20,6 +20,7 @@
 #include "tma_map.h"
 
 #include <cuda_fp16.h>
+#include <math.h>
 
 namespace bsf {
 namespace {
@@ -360,7 +361,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     switch (p.split) {
       case 1: sum_and_store<OUT, 1, 4>(p, part, n0, tok0, j0, j1); break;
       case 2: sum_and_store<OUT, 2, 4>(p, part, n0, tok0, j0, j1); break;
+      case 3: sum_and_store<OUT, 3, 2>(p, part, n0, tok0, j0, j1); break;
       case 4: sum_and_store<OUT, 4, 2>(p, part, n0, tok0, j0, j1); break;
+      case 5: sum_and_store<OUT, 5, 1>(p, part, n0, tok0, j0, j1); break;
+      case 6: sum_and_store<OUT, 6, 1>(p, part, n0, tok0, j0, j1); break;
+      case 7: sum_and_store<OUT, 7, 1>(p, part, n0, tok0, j0, j1); break;
       default: sum_and_store<OUT, 8, 1>(p, part, n0, tok0, j0, j1); break;
     }
   }
@@ -734,9 +739,10 @@ const void* kernel_of(int out, int form) {
 }
 
 // Once per device: all kernels may use all shared memory, and the number of CTAs of the split kernel that run at
-// once, one per SM, in clusters of 1, 2, 4 and 8 (a cluster lives in one GPC, so 8 leave SMs idle).
+// once, one per SM, in clusters of 1 .. kMaxSplit (a cluster lives in one GPC, so some sizes leave SMs idle).
+constexpr int kMaxSplit = 8;
 struct LinearLimits {
-  std::atomic<int> ctas[4];
+  std::atomic<int> ctas[kMaxSplit + 1];
   std::atomic<bool> ready;
 };
 bsf_status linear_limits(const LinearLimits** out) {
@@ -753,15 +759,15 @@ bsf_status linear_limits(const LinearLimits** out) {
                 cudaSuccess)
           return BSF_ERR_CUDA;
       }
-    for (int i = 0; i < 4; ++i) {
-      DependentLaunch launch(8u << i, kThreads, kSmemBytes, nullptr, 1u << i);
+    for (int i = 1; i <= kMaxSplit; ++i) {
+      DependentLaunch launch(8u * i, kThreads, kSmemBytes, nullptr, i);
       launch.cfg.numAttrs = 1;                           // the cluster alone
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, kernel_of(BSF_TYPE_F32, 0), &launch.cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         return BSF_ERR_CUDA;
       }
-      l.ctas[i].store(n << i, std::memory_order_relaxed);
+      l.ctas[i].store(n * i, std::memory_order_relaxed);
     }
     l.ready.store(true, std::memory_order_release);
   }
@@ -769,39 +775,49 @@ bsf_status linear_limits(const LinearLimits** out) {
   return BSF_OK;
 }
 
-// Which kernel a product takes, by the time each would need (nanoseconds).
+// Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 1800 products
+// of 1 .. 8192 tokens, 16 .. 8192 weight rows and K of 64 .. 8192, drawn by their logarithms, with weights that come from
+// HBM, each timed in every form that could win (20000 in all).  The choice is 0.8 % above the best form on average, at
+// worst 38 % (2694 x 23 x 1528, in tiles of 64 tokens over 6 CTAs instead of 128 over 5); with K over 1, 2, 4 or
+// 8 CTAs alone it would be 2.8 %.  Both sides: 256 x 4096 x 4096 takes 17.3 us split and 18.5 in pairs, 1024 x 256 x
+// 7168 11.3 and 21, 777 x 4100 x 1416 34 and 15.7.
 struct Plan {
   bool pair;
   int tok;                  // pairs: tokens per tile; split: most tokens per tile
   int split;
 };
-Plan choose_plan(int64_t M, int64_t N, int64_t nkb, bool f32, const LinearLimits& limits) {
-  const int64_t ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
+Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, const LinearLimits& limits) {
+  const int64_t nkb = (K + kBlockK - 1) / kBlockK, ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
+  const double read = 2.0 * K * (M + N) / 7221;        // of both operands from HBM
   Plan best = {false, 64, 1};
-  int64_t least = INT64_MAX;
+  double least = 1e300;
   for (int tok = 64; tok <= kMaxTok; tok += 64) {
     if (tok > 64 && M <= 64) break;
     const int64_t chunks = (M + tok - 1) / tok, per = ((M + chunks - 1) / chunks + 15) / 16 * 16;
-    for (int i = 0; i < 4; ++i) {
-      const int64_t split = int64_t(1) << i, ctas = ntn * chunks * split;
-      if (i > 0 && (nkb < 2 * split || ctas > 2 * sms)) break;
-      const int64_t at_once = limits.ctas[i].load(std::memory_order_relaxed), kbs = (nkb + split - 1) / split;
-      const int64_t load = (ctas + at_once - 1) / at_once;              // CTAs of the busiest SM
-      int64_t ns = 3100 + 6 * per + (i > 0 ? 400 + 400 * i : 0);
-      if (per > 64)         // one CTA per SM: it cannot start under its predecessor
-        ns += 800 + load * kbs * 270 + (load - 1) * 4700;
-      else                  // two CTAs on an SM share its 120 bytes a nanosecond from L2
-        ns += kbs * (load / 2 * (273 + 32 * per / 15) + load % 2 * 270) + (load - 1) * 1150;
+    for (int split = 1; split <= kMaxSplit; ++split) {
+      const int64_t ctas = ntn * chunks * split, kbs = (nkb + split - 1) / split;
+      if (split > 1 && (nkb < 2 * split || ctas > 2 * sms)) break;
+      const int64_t at_once = limits.ctas[split].load(std::memory_order_relaxed);
+      const int64_t load = (ctas + at_once - 1) / at_once;            // CTAs of the busiest SM
+      const double once = 89 * per / sqrt(double(split)) + (split > 1 ? 513 + 53 * split : 0);
+      // tiles of more than 64 tokens have an SM to themselves, others share one two at a time
+      const double busy = per > 64 ? load * (once + kbs * (206 + 0.55 * per))
+                                   : load / 2 * (once + 702.0 * kbs) + load % 2 * (once + 282.0 * kbs);
+      const double ns = 2558 + (busy > read ? busy : read);
       if (ns < least) {
         least = ns;
-        best = {false, tok, static_cast<int>(split)};
+        best = {false, tok, split};
       }
     }
   }
   for (int tok = f32 ? kMaxTok : kPairMaxTok; tok >= 64; tok -= 16) {      // (float32 sums live in registers)
     const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
-    const int64_t multiply = (tok <= kMaxTok ? 40 : 36) * tok / 16, issue = tok <= kMaxTok ? 320 : 470;
-    const int64_t ns = 4600 + waves * ((nkb + 1) / 2 * (issue > multiply ? issue : multiply) + 13 * tok);
+    const bool narrow = tok <= kMaxTok;
+    // a K-block: by the issuing threads, or by the tensor cores and L2
+    const double issue = narrow ? 143 : 261, multiply = narrow ? 105 + 1.5 * tok : 317 + 0.25 * tok;
+    const double loop = (narrow ? (nkb + 1) / 2 * 2 : nkb) * (issue > multiply ? issue : multiply);
+    const double store = tok * (f32 ? 15.0 : 10.4), busy = waves * (loop > 1456 + store ? loop : 1456 + store);
+    const double ns = 3920 + (busy > read ? busy : read) + store;
     if (ns < least) {
       least = ns;
       best = {true, tok, 1};
@@ -844,7 +860,7 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   const LinearLimits* limits;
   const bsf_status st = linear_limits(&limits);
   if (st != BSF_OK) return st;
-  const Plan plan = choose_plan(T, N, nkb, y_type == BSF_TYPE_F32, *limits);
+  const Plan plan = choose_plan(T, N, K, y_type == BSF_TYPE_F32, *limits);
   Epilogue e;
   e.bias = bias;
   e.residual = residual;
