@@ -98,18 +98,21 @@ __device__ __forceinline__ float exp_of(float x) { return exp2_approx(x * 1.4426
 // erfc(|v| / sqrt 2) / 2: with x = |v| / sqrt 2, exp(-x^2) times a polynomial in t = 1 / (1 + 0.3021286 x), a minimax
 // fit (Lawson's iteration) of erfc(x) exp(x^2) on 0 .. 14 relative to it, off by 2.9e-8.  erfcf would be 2.5 times as
 // many instructions, and a tile's epilogue is not always hidden behind other tiles' products.
-__device__ __forceinline__ float half_erfc(float a) {
-  const float t = __fdividef(1.f, fmaf(a, 0.21363720167f, 1.f));
-  float q = -0.11995414206527316f;
-  q = fmaf(q, t, 0.4315029982598405f);
-  q = fmaf(q, t, -0.4179198212295966f);
-  q = fmaf(q, t, 0.4548883512025796f);
-  q = fmaf(q, t, -0.03962212128188006f);
-  q = fmaf(q, t, 0.19541278265418394f);
-  q = fmaf(q, t, 0.15392502081132817f);
-  q = fmaf(q, t, 0.1713477909787805f);
-  q = fmaf(q, t, 0.17041911225827286f);
-  return 0.5f * t * q * exp2_approx(a * a * -0.72134752044448170f);
+// In pairs: one packed instruction takes the place of two.
+__device__ __forceinline__ float2 half_erfc(float a, float b) {
+  const float t0 = __fdividef(1.f, fmaf(a, 0.21363720167f, 1.f)), t1 = __fdividef(1.f, fmaf(b, 0.21363720167f, 1.f));
+  constexpr float c[8] = {0.17041911225827286f,  0.1713477909787805f, 0.15392502081132817f,  0.19541278265418394f,
+                          -0.03962212128188006f, 0.4548883512025796f, -0.4179198212295966f, 0.4315029982598405f};
+  float q0 = -0.11995414206527316f, q1 = q0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    float d0 = c[i], d1 = c[i];
+    fma2_f32(d0, d1, q0, q1, t0, t1);
+    q0 = d0;
+    q1 = d1;
+  }
+  return make_float2(0.5f * t0 * q0 * exp2_approx(a * a * -0.72134752044448170f),
+                     0.5f * t1 * q1 * exp2_approx(b * b * -0.72134752044448170f));
 }
 
 // Each activation of N values, in float32 within a few units in the last place of it plus what a rounded argument of
@@ -128,9 +131,11 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
       break;
     case BSF_ACT_GELU:                  // max(v, 0) - |v| erfc(|v| / sqrt 2) / 2, whose second term is 0 from 20 on
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float a = fminf(fabsf(v[i]), 20.f);
-        v[i] = fmaf(-a, half_erfc(a), v[i] < 0.f ? 0.f : v[i]);
+      for (int i = 0; i < N; i += 2) {
+        const float a = fminf(fabsf(v[i]), 20.f), b = fminf(fabsf(v[i + 1]), 20.f);
+        const float2 e = half_erfc(a, b);
+        v[i] = fmaf(-a, e.x, v[i] < 0.f ? 0.f : v[i]);
+        v[i + 1] = fmaf(-b, e.y, v[i + 1] < 0.f ? 0.f : v[i + 1]);
       }
       break;
     case BSF_ACT_GELU_TANH:             // 0.5 v (1 + tanh(u)) = v / (1 + exp(-2 u)), u = sqrt(2 / pi) (v + 0.044715 v^3)
