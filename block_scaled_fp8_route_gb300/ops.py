@@ -430,6 +430,7 @@ GATE_SIGMOID = 0x1
 GATE_GROUP_TOP2 = 0x2
 GATE_RENORMALISE = 0x4
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}       # BSF_TYPE_F32, BSF_TYPE_BF16
+FEW_TOKENS = 32                                      # most tokens of few_token_moe
 TYPE_E4M3 = 2                                        # BSF_TYPE_E4M3
 _LINEAR_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 3}       # BSF_TYPE_F32, _BF16, _F16
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}

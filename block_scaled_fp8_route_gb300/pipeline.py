@@ -255,13 +255,21 @@ class MoEBlock:
     ``w13_bf16`` [E, 2 I, K] holds each expert's gate rows and then its up rows, ``w2_bf16`` [E, K, I] its
     down projection (K and I multiples of 128); ``shared`` = (w13 [2 S, K], w2 [K, S]) of the always-active
     expert, S any multiple of 8.  The other keyword arguments are those of ``ops.gate`` that say how to choose
-    (``score``, ``bias``, ``groups``, ``kept_groups``, ``group_score``, ``renormalise``, ``scale``).  Every step
-    is a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be captured."""
+    (``score``, ``bias``, ``groups``, ``kept_groups``, ``group_score``, ``renormalise``, ``scale``).
 
+    ``router`` = its weights bf16 [E, K], or (weights, bias float32 [E]): the logits are then a product of the block's
+    own (``ops.linear``, float32).  ``few_tokens=True`` (T <= 32) runs everything after the gate as
+    ``ops.few_token_moe``, two kernels that leave x and the hidden values unquantised: closer to the weights' own
+    result than the chain, not bit-equal to it.
+
+    Every step is a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be
+    captured.  Steps of one object share its buffers and must not overlap."""
+
+    few_tokens, router = False, None
     _GATE_ARGS = {"score", "bias", "groups", "kept_groups", "group_score", "renormalise", "scale"}
 
     def __init__(self, E, kr, T, K, I, w13_bf16, w2_bf16, shared=None, layout=ops.CONTIGUOUS, align_or_max_m=128,
-                 device="cuda", expected_m=0, **gate):
+                 device="cuda", expected_m=0, few_tokens=False, router=None, **gate):
         if tuple(w13_bf16.shape) != (E, 2 * I, K) or tuple(w2_bf16.shape) != (E, K, I):
             raise ValueError(f"expected w13 {(E, 2 * I, K)} and w2 {(E, K, I)}, got {tuple(w13_bf16.shape)} and "
                              f"{tuple(w2_bf16.shape)}")
@@ -278,14 +286,28 @@ class MoEBlock:
                                  f"{tuple(w13.shape)} and {tuple(w2.shape)}")
         if not gate.keys() <= self._GATE_ARGS:
             raise TypeError(f"unexpected arguments {sorted(gate.keys() - self._GATE_ARGS)}")
+        if few_tokens and T > ops.FEW_TOKENS:
+            raise ValueError(f"few_tokens: expected T of at most {ops.FEW_TOKENS}, got {T}")
+        router, router_bias = router if isinstance(router, (tuple, list)) else (router, None)
+        if router is not None and (router.dtype != torch.bfloat16 or router.shape != (E, K)):
+            raise ValueError(f"router: expected bfloat16 weights {(E, K)}, got {router.dtype} {tuple(router.shape)}")
+        if router_bias is not None and (router_bias.dtype != torch.float32 or router_bias.shape != (E,)):
+            raise ValueError(f"router: expected a float32 bias {(E,)}, got {router_bias.dtype} "
+                             f"{tuple(router_bias.shape)}")
         # an empty batch: the gate's arguments are refused here, not at the first step
         ops.gate(torch.empty((0, E), dtype=torch.float32, device=device), kr, **gate)
-        self.T, self.K, self.I, self.kr, self.gate_args = T, K, I, kr, gate
+        self.E, self.T, self.K, self.I, self.kr, self.gate_args = E, T, K, I, kr, gate
+        self.few_tokens = few_tokens
+        if few_tokens:
+            self._few_weights(w13_bf16, w2_bf16, shared, device)
+            self.path = None
+            self.z = torch.empty((T, K), dtype=torch.bfloat16, device=device)
+            self._routing_buffers(router, router_bias, device)
+            return
         self.path = MoEPath(E, kr, T, K, 2 * I, w13_bf16, layout=layout, align_or_max_m=align_or_max_m,
                             w2_bf16=w2_bf16, device=device, expected_m=expected_m)
         self.z = self.path.z
-        self.topk_ids = torch.empty((T, kr), dtype=torch.int32, device=device)
-        self.topk_weights = torch.empty((T, kr), dtype=torch.float32, device=device)
+        self._routing_buffers(router, router_bias, device)
         self.shared = None
         if shared is not None:
             self.shared = tuple(ops.prepare_dense_weight(w.to(device)) for w in shared)
@@ -294,21 +316,58 @@ class MoEBlock:
             self.shared_q = torch.empty((T, Sp), dtype=torch.uint8, device=device)
             self.shared_sf = torch.empty((ops.sf_words(Sp), ops.sf_ld(T)), dtype=torch.int32, device=device)
 
-    def step(self, x, logits, z=None, timer=None):
-        """x bf16 [T, K], logits [T, E] (float32 or bf16) -> z bf16 [T, K].  A token all of whose logits are
-        masked gets the always-active expert alone (zero without one)."""
+    def _routing_buffers(self, router, bias, device):
+        self.topk_ids = torch.empty((self.T, self.kr), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((self.T, self.kr), dtype=torch.float32, device=device)
+        self.router = None if router is None else router.to(device).contiguous()
+        self.router_bias = None if bias is None else bias.to(device).contiguous()
+        if router is not None:
+            self.logits = torch.empty((self.T, self.E), dtype=torch.float32, device=device)
+
+    def _few_weights(self, w13, w2, shared, device):
+        """Weights as ``ops.few_token_moe`` takes them, and its workspace."""
+        def prepared(w):
+            q, sf128 = ops.quantise_weight(w.to(device))
+            return ops.tile_weights(q), ops.prepare_weight_sf(sf128, w.shape[2])
+        self.few = (*prepared(w13), *prepared(w2))
+        self.shared, S = None, 0
+        if shared is not None:
+            # gate and up rows each on a multiple of 128, so that a tile has either
+            gate_up = [torch.nn.functional.pad(w, (0, 0, 0, -w.shape[0] % 128)) for w in shared[0].to(device).chunk(2)]
+            self.shared = (*ops.prepare_dense_weight(torch.cat(gate_up)), *ops.prepare_dense_weight(shared[1].to(device)))
+            S = gate_up[0].shape[0]
+        self.workspace = ops.few_token_moe_workspace(self.T, self.kr, self.I, S, device=device)
+
+    def step(self, x, logits=None, z=None, timer=None, addend=None):
+        """x bf16 [T, K], logits [T, E] (float32 or bf16; default: the router's product of x) -> z bf16 [T, K].  A
+        token all of whose logits are masked gets the always-active expert alone (zero without one).  ``addend`` bf16
+        [T, K] (the residual stream, say) is added before z's rounding; with ``few_tokens`` only."""
         t = timer if timer is not None else _no_timer
-        p, b = self.path, self.path.bufs
         z = self.z if z is None else z
         device = self.z.device
         _expect(x, "x", torch.bfloat16, (self.T, self.K), device)
-        _expect(logits, "logits", torch.bfloat16 if logits.dtype == torch.bfloat16 else torch.float32,
-                (self.T, p.E), device)
+        if logits is None and self.router is None:
+            raise ValueError("logits: expected a tensor (the block has no router)")
+        if logits is not None:
+            _expect(logits, "logits", torch.bfloat16 if logits.dtype == torch.bfloat16 else torch.float32,
+                    (self.T, self.E if self.few_tokens else self.path.E), device)
         _expect(z, "z", torch.bfloat16, (self.T, self.K), device)
         if not z.is_contiguous():
             raise ValueError("z: expected a contiguous tensor")
+        if addend is not None:
+            if not self.few_tokens:
+                raise ValueError("addend: only a block of few_tokens adds one")
+            _expect(addend, "addend", torch.bfloat16, (self.T, self.K), device)
+        if logits is None:
+            with t("router"):
+                logits = ops.linear(x, self.router, bias=self.router_bias, out=self.logits)
         with t("gate"):
             ops.gate(logits, self.kr, topk_ids=self.topk_ids, topk_weights=self.topk_weights, **self.gate_args)
+        if self.few_tokens:
+            with t("moe"):
+                return ops.few_token_moe(x, self.topk_ids, self.topk_weights, *self.few, shared=self.shared,
+                                         addend=addend, z=z, workspace=self.workspace)
+        p, b = self.path, self.path.bufs
         p._stage_in(x, self.topk_ids, t)
         with t("gemm"):
             p.gemm(b.a_packed, b.sfa_packed, p.wq, p.sfb, p.y)
@@ -327,14 +386,14 @@ class MoEBlock:
                 ops.dense_gemm(self.shared_q, self.shared_sf, b2, sfb2, self.K, addend=z, d=z)
         return z
 
-    def capture(self, x, logits):
+    def capture(self, x, logits=None, addend=None):
         """Record one step on these (static) tensors into a CUDA graph; ``replay()`` runs it on whatever they hold."""
-        self.step(x, logits)
+        self.step(x, logits, addend=addend)
         torch.cuda.synchronize()
-        self._graph_inputs = (x, logits)             # the graph reads their memory: keep them alive with it
+        self._graph_inputs = (x, logits, addend)     # the graph reads their memory: keep them alive with it
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
-            self.step(x, logits)
+            self.step(x, logits, addend=addend)
         return self.graph
 
     def replay(self):
