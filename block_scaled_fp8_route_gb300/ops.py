@@ -7,6 +7,7 @@ kernels.  Names follow the C entry points without the ``bsf_`` prefix.
 """
 
 import ctypes
+import functools
 
 import torch
 
@@ -489,6 +490,11 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+# memory of a stream without a tensor around it, given back in stream order (a tensor costs a call 5 us)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None) or (
+    lambda size, stream: torch.cuda.caching_allocator_alloc(size, None, stream))
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None) or torch.cuda.caching_allocator_delete
+
 # index of the device that the library launches on and whose SM count and error word it uses
 _current_device = torch._C._cuda_getDevice
 
@@ -647,17 +653,22 @@ def dense_gemm(a, sfa, b, sfb, N=None, addend=None, d=None, flags=B_TILED, strea
     return d
 
 
+@functools.lru_cache(maxsize=256)
+def _few_workspace_bytes(T, kr, I, S):
+    return _lib.load().bsf_few_token_moe_workspace_bytes(T, kr, I, S)
+
+
 def few_token_moe_workspace(T, kr, I, S=0, device="cuda"):
     """Workspace of ``few_token_moe`` for these sizes (or smaller ones).  Calls that may overlap, on different
     streams or in graphs that may run at the same time, need one each."""
-    n = _lib.load().bsf_few_token_moe_workspace_bytes(T, kr, I, S)
+    n = _few_workspace_bytes(T, kr, I, S)
     if n == 0:
         raise ValueError(f"few_token_moe: expected T and kr of at most 32, got T = {T}, kr = {kr}, I = {I}, S = {S}")
     return torch.empty(n, dtype=_U8, device=device)
 
 
 def _few_weights(w, sf, E, rows, inner, kind, what):
-    """Check one weight tensor (and its scale words) of ``few_token_moe``."""
+    """Why one weight tensor (and its scale words) is none of ``few_token_moe``, if so."""
     shape = (rows, inner) if E is None else (E, rows, inner)
     if kind == _BF16 and w.dtype == _U8:         # tile_weights gives bytes
         shape = shape[:-1] + (2 * inner,)
@@ -675,31 +686,20 @@ def _few_weights(w, sf, E, rows, inner, kind, what):
         raise ValueError(f"{what}: bfloat16 weights have no scale words")
 
 
-def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, addend=None, z=None, workspace=None,
-                  flags=B_TILED, stream=None):
-    """A whole MoE layer for T <= 32 tokens in two kernels: x bf16 [T, K] (row stride a multiple of 8), topk_ids int32
-    and topk_weights float32 [T, kr] (``gate``; an id < 0 takes no expert) -> z bf16 [T, K] =
-    sum_k weight_k * W2_e (silu(gate_e x) * (up_e x)) (+ the shared expert's) (+ ``addend`` bf16 [T, K]).
-
-    Weights: w13 uint8 [E, 2 I, K] with sfb13, w2 uint8 [E, K, I] with sfb2 (``quantise_weight`` ->
-    ``prepare_weight_sf``, ``tile_weights``), or bf16 of these shapes (with ``B_TILED`` the bytes that
-    ``tile_weights`` gives) and None for both scales.  ``shared`` = (w13 [2 S, K], sfb13, w2 [K, S], sfb2) of an
-    expert that every token takes.  x is not quantised.  ``workspace`` from ``few_token_moe_workspace``, used by this
-    call alone until it is done (default: a new one)."""
+def _refuse_few(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace, need, stream):
+    """Why ``few_token_moe`` does not take these operands."""
     T, K = _two_dims(x, "x")
     if x.dtype != _BF16:
         _refuse(x, _BF16, None, "x")
-    ldx = _row_stride(x, T, K, "x")
+    _row_stride(x, T, K, "x")
     if w13.dim() != 3 or w2.dim() != 3:
         raise ValueError(f"expected w13 [E, 2 I, K] and w2 [E, K, I], got {tuple(w13.shape)} and {tuple(w2.shape)}")
     E, I = w13.shape[0], w13.shape[1] // 2
     kind = _BF16 if sfb13 is None else _U8
     _few_weights(w13, sfb13, E, 2 * I, K, kind, "w13")
     _few_weights(w2, sfb2, E, K, I, kind, "w2")
-    b13 = f13 = b2 = f2 = None
     S = 0
-    if shared is not None:
-        b13, f13, b2, f2 = shared
+    if b13 is not None:
         if b13.dim() != 2 or b2.dim() != 2:
             raise ValueError(f"shared: expected w13 [2 S, K] and w2 [K, S], got {tuple(b13.shape)} and {tuple(b2.shape)}")
         S = b13.shape[0] // 2
@@ -712,36 +712,93 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
         _refuse(topk_ids, _I32, (T, kr), "topk_ids")
     if topk_weights.dtype != _F32 or topk_weights.shape != (T, kr) or not topk_weights.is_contiguous():
         _refuse(topk_weights, _F32, (T, kr), "topk_weights")
-    out = (T, K)
-    if z is None:
-        z = _empty(out, _BF16, x, stream)
-    elif z.dtype != _BF16 or z.shape != out:
-        _refuse(z, _BF16, out, "z")
-    ldz = _row_stride(z, T, K, "z")
-    ldc = 0
-    if addend is not None:
-        if addend.dtype != _BF16 or addend.shape != out:
-            _refuse(addend, _BF16, out, "addend")
-        ldc = _row_stride(addend, T, K, "addend")
-    need = _lib.load().bsf_few_token_moe_workspace_bytes(T, kr, I, S)
-    if workspace is None:
-        workspace = _empty((max(need, 16),), _U8, x, stream)
-    elif workspace.dtype != _U8 or workspace.dim() != 1 or not workspace.is_contiguous() or workspace.numel() < need:
+    for t, what in ((z, "z"), (addend, "addend")):
+        if t is not None:
+            if t.dtype != _BF16 or t.shape != (T, K):
+                _refuse(t, _BF16, (T, K), what)
+            _row_stride(t, T, K, what)
+    if workspace is not None and (workspace.dtype != _U8 or workspace.dim() != 1 or not workspace.is_contiguous()
+                                  or workspace.numel() < need):
         raise ValueError(f"workspace: expected at least {need} contiguous bytes, got {workspace.dtype} "
                          f"{tuple(workspace.shape)}")
-    operands = (x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace)
-    device = x.get_device()
-    if (device < 0 or device != _current_device() or (stream is not None and stream.device_index != device)
-            or any(t is not None and t.get_device() != device for t in operands)):
-        _refuse_devices("x topk_ids topk_weights w13 sfb13 w2 sfb2 shared_w13 shared_sfb13 shared_w2 shared_sfb2 "
-                        "addend z workspace", operands, stream)
+    _refuse_devices("x topk_ids topk_weights w13 sfb13 w2 sfb2 shared_w13 shared_sfb13 shared_w2 shared_sfb2 "
+                    "addend z workspace", (x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z,
+                                           workspace), stream)
+
+
+def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, addend=None, z=None, workspace=None,
+                  flags=B_TILED, stream=None):
+    """A whole MoE layer for T <= 32 tokens in two kernels: x bf16 [T, K] (row stride a multiple of 8), topk_ids int32
+    and topk_weights float32 [T, kr] (``gate``; an id < 0 takes no expert) -> z bf16 [T, K] =
+    sum_k weight_k * W2_e (silu(gate_e x) * (up_e x)) (+ the shared expert's) (+ ``addend`` bf16 [T, K]).
+
+    Weights: w13 uint8 [E, 2 I, K] with sfb13, w2 uint8 [E, K, I] with sfb2 (``quantise_weight`` ->
+    ``prepare_weight_sf``, ``tile_weights``), or bf16 of these shapes (with ``B_TILED`` the bytes that
+    ``tile_weights`` gives) and None for both scales.  ``shared`` = (w13 [2 S, K], sfb13, w2 [K, S], sfb2) of an
+    expert that every token takes.  x is not quantised.  ``workspace`` from ``few_token_moe_workspace``, used by this
+    call alone until it is done (default: a new one)."""
+    b13, f13, b2, f2 = (None, None, None, None) if shared is None else shared
+    xs, ws, ids = x.shape, w13.shape, topk_ids.shape
+    fine = len(xs) == 2 and len(ws) == 3 and len(ids) == 2 and x.dtype is _BF16
+    need = 0
+    if fine:
+        T, K = xs
+        E, I, kr = ws[0], ws[1] // 2, ids[1]
+        S = 0 if b13 is None else b13.shape[0] // 2
+        device = x.get_device()
+        if K % 128 or I % 128 or S % 128 or (T > 1 and x.stride(1) != 1):
+            fine = False
+        elif sfb13 is not None:                      # E4M3: bytes, one row of scale words per 512 of the inner width
+            wk, wi = (K + 511) // 512, (I + 511) // 512
+            fine = (sfb2 is not None and w13.dtype is _U8 and w2.dtype is _U8 and sfb13.dtype is _I32 and sfb2.dtype is _I32
+                    and ws == (E, 2 * I, K) and w2.shape == (E, K, I) and sfb13.shape == (E, wk, 2 * I)
+                    and sfb2.shape == (E, wi, K) and sfb13.is_contiguous() and sfb2.is_contiguous()
+                    and sfb13.get_device() == device and sfb2.get_device() == device)
+        else:
+            fine = (sfb2 is None and (w13.dtype is _BF16 or w13.dtype is _U8) and (w2.dtype is _BF16 or w2.dtype is _U8)
+                    and ws == (E, 2 * I, K if w13.dtype is _BF16 else 2 * K)
+                    and w2.shape == (E, K, I if w2.dtype is _BF16 else 2 * I))
+        fine = (fine and w13.is_contiguous() and w2.is_contiguous() and ids == (T, kr) and topk_weights.shape == ids
+                and topk_ids.dtype is _I32 and topk_weights.dtype is _F32 and topk_ids.is_contiguous()
+                and topk_weights.is_contiguous() and device >= 0 and device == _current_device()
+                and w13.get_device() == device and w2.get_device() == device and topk_ids.get_device() == device
+                and topk_weights.get_device() == device and (stream is None or stream.device_index == device))
+        need = _few_workspace_bytes(T, kr, I, S)
+        if fine and b13 is not None:
+            kind = _U8 if sfb13 is not None else _BF16
+            _few_weights(b13, f13, None, 2 * S, K, kind, "shared w13")
+            _few_weights(b2, f2, None, K, S, kind, "shared w2")
+            fine = all(t is None or t.get_device() == device for t in (b13, f13, b2, f2))
+        if fine and z is not None:
+            fine = z.dtype is _BF16 and z.shape == xs and (T == 1 or z.stride(1) == 1) and z.get_device() == device
+        if fine and addend is not None:
+            fine = (addend.dtype is _BF16 and addend.shape == xs and (T == 1 or addend.stride(1) == 1)
+                    and addend.get_device() == device)
+        if fine and workspace is not None:
+            fine = (workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous()
+                    and workspace.numel() >= need and workspace.get_device() == device)
+    if not fine:
+        _refuse_few(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace, need, stream)
+    ldx = x.stride(0) if T > 1 else K
+    if z is None:
+        z = _empty((T, K), _BF16, x, stream)
+    ldz = z.stride(0) if T > 1 else K
+    ldc = 0 if addend is None else addend.stride(0) if T > 1 else K
     if stream is not None:
-        _used_on(stream, *operands)
-    at = [None if t is None else t.data_ptr() for t in operands]
-    status = _lib.load().bsf_few_token_moe(
-        at[0], T, K, ldx, at[1], at[2], kr, E, I, _TYPES[_BF16] if kind == _BF16 else TYPE_E4M3, at[3], at[4], at[5],
-        at[6], S, at[7], at[8], at[9], at[10], at[11], ldc, at[12], ldz, at[13], workspace.numel(), flags,
-        _current_stream(device) if stream is None else stream.cuda_stream)
+        _used_on(stream, x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace)
+    on = _current_stream(device) if stream is None else stream.cuda_stream
+    scratch = _raw_alloc(max(need, 16), on) if workspace is None else workspace.data_ptr()
+    try:
+        status = _lib.load().bsf_few_token_moe(
+            x.data_ptr(), T, K, ldx, topk_ids.data_ptr(), topk_weights.data_ptr(), kr, E, I,
+            1 if sfb13 is None else TYPE_E4M3, w13.data_ptr(), None if sfb13 is None else sfb13.data_ptr(),
+            w2.data_ptr(), None if sfb2 is None else sfb2.data_ptr(), S, None if b13 is None else b13.data_ptr(),
+            None if f13 is None else f13.data_ptr(), None if b2 is None else b2.data_ptr(),
+            None if f2 is None else f2.data_ptr(), None if addend is None else addend.data_ptr(), ldc, z.data_ptr(), ldz,
+            scratch, need, flags, on)
+    finally:
+        if workspace is None:
+            _raw_delete(scratch)                     # (reused by later work of this stream only)
     if status:
         _lib.check(status, "few_token_moe")
     return z
