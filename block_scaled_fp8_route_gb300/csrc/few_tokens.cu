@@ -40,13 +40,13 @@ constexpr int kMaxTokens = 32;
 constexpr int kMaxKr = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kBoxBytes = 16384;               // 128 weight rows x 128 bytes
-constexpr int kMaxStages = 4;                  // a stage: two boxes, the token operand that both meet, its scales
+constexpr int kMaxStages = 5;                  // a stage: two boxes, the token operand that both meet, its scales
 constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows: words 0, 1 for box 0, 2, 3 for box 1
 constexpr int kAccCol = 64;                    // tensor memory: 4 columns of ones, 4 per stage and box of scales, sums
 constexpr int kParts = 4;                      // most CTAs that share a tile of the first product
 // warps: 0 and 3 weight loads, 1 and 2 MMA issuers (one per box each), 4-7 and 8-11 as each kernel needs them
 constexpr int kThreads = 384;
-constexpr int kBarBytes = 384;                // barriers 232, two words, 32 words of groups
+constexpr int kBarBytes = 512;                // barriers, tensor memory's place, abort flag, 32 words of groups, a maximum
 constexpr int kSmem = 113 * 1024;              // two CTAs per SM
 constexpr int kMostSmem = 227 * 1024;
 constexpr int kMaxSplit = 16;
@@ -72,8 +72,7 @@ struct FewArgs {
   int nkb2, nkb2_shared;      // of the second, per expert
   int ctas1;                  // CTAs of the first kernel
   int split, nbox;            // second kernel: CTAs per cluster, 128-row tiles per CTA
-  int stages, operand_bytes;
-  int acc_stride, sets;       // columns of a sum; sets of them in the first kernel
+  int tables, stage_space;    // bytes of shared memory: tables, then stages
   uint32_t tmem_cols;
   int tiled, withhold, vec4;
   int* err;
@@ -139,11 +138,8 @@ template <int FMT, int PHASE>
 __global__ void __launch_bounds__(kThreads, 2)
     few_kernel(const __grid_constant__ CUtensorMap map_routed, const __grid_constant__ CUtensorMap map_shared,
                const FewArgs p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage_bytes = 2 * kBoxBytes + p.operand_bytes;
-  uint8_t* scales = smem + p.stages * stage_bytes;                              // [stages][kSfBytes]
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + p.stages * kSfBytes);   // per stage and box
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);                       // per stage and box
   uint64_t* empty = full + 2 * kMaxStages;                                      // per stage and box
   uint64_t* formed = empty + 2 * kMaxStages;                                    // one for each warp that forms operands
   uint64_t* acc_full = formed + 8;
@@ -152,9 +148,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* groups_of = tmem_slot + 2;                                          // per 32 experts: chosen ones, rows << 16
-  uint2* chosen = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(full) + kBarBytes);   // tokens (bits); expert, first row << 16
+  int* most_tokens = reinterpret_cast<int*>(groups_of + 32);                    // of any chosen expert
+  uint8_t* scales = smem_raw + kBarBytes;                                       // [stages][kSfBytes]
+  uint2* chosen = reinterpret_cast<uint2*>(scales + kMaxStages * kSfBytes);     // tokens (bits); expert, first row << 16
   float* share = reinterpret_cast<float*>(chosen + min(p.E, p.R) + 1);          // [R] p of each row
   uint8_t* token = reinterpret_cast<uint8_t*>(share + p.R);                     // [R] token of each row
+  uint8_t* smem = smem_raw + p.tables;                                          // stages: two boxes and the token operand
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cluster = PHASE == 2 ? static_cast<int>(blockIdx.x) / p.split : 0;
@@ -175,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(done, boxes);
     *abort_flag = 0;
+    *most_tokens = PHASE == 1 && p.S == 0 ? 1 : p.T;         // (the shared expert and the second kernel take all)
     fence_barrier_init();
     tma_prefetch_desc(&map_routed);
     if (p.S) tma_prefetch_desc(&map_shared);
@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int g = warp; g < groups; g += kThreads / 32) {
       const uint32_t m = g * 32 + lane < p.E ? mask[g * 32 + lane] : 0u;
       const int n = __reduce_add_sync(0xffffffffu, __popc(m));
+      const int most = PHASE == 1 ? static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(__popc(m)))) : 1;
       const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
+      if (PHASE == 1 && lane == 0) atomicMax(most_tokens, most);
       if (lane == 0) groups_of[g] = static_cast<uint32_t>(__popc(some)) | static_cast<uint32_t>(n) << 16;
     }
     __syncthreads();
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t everyone = p.T == 32 ? 0xffffffffu : (1u << p.T) - 1u;
   if (tid == 0) chosen[nchosen] = make_uint2(everyone, 0u);
   if (FMT == kFp8)                         // every row has a scale, whether or not it has values
-    for (int i = tid; i < p.stages * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
+    for (int i = tid; i < kMaxStages * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
   proxy_fence();                           // the tables' place is written by TMA next
   __syncthreads();
 
@@ -296,6 +298,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   // tokens padded to whole groups; the operand has so many rows for each term of a value
   auto padded = [&](int n) { return kTerms == 2 ? (n + 7) & ~7 : (n + 15) & ~15; };
+  // Stages as large as the most tokens of an expert need: 32 tokens seldom put more than 8 on one, and a larger operand
+  // would cost a stage of weights in flight.
+  const int most_rows = kTerms * padded(*most_tokens);
+  const int stage_bytes = 2 * kBoxBytes + ((most_rows * 128 + 1023) & ~1023);
+  const int stages = min(p.stage_space / stage_bytes, PHASE == 1 ? 4 : kMaxStages);      // (at most kConvWarps)
+  const int acc_stride = (most_rows + 31) & ~31;                   // columns of a sum
+  const uint32_t sets = kAccCol + 4 * acc_stride <= static_cast<int>(p.tmem_cols) ? 2u : 1u;   // of sums, first kernel
 
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
@@ -341,11 +350,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int nkb = PHASE == 1 ? p.nkb1 : shared ? p.nkb2_shared : p.nkb2;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           // (the second kernel's clock starts when the first kernel has ended)
-          if (PHASE == 2 && issued == p.stages) pdl_wait();
+          if (PHASE == 2 && issued == stages) pdl_wait();
           uint64_t* bar = &full[2 * stage + b];
           if (!mbar_wait(&empty[2 * stage + b], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
           // the stage's operand may be formed anew, too
-          if (issued >= p.stages) mbar_arrive(&formed[(issued - p.stages) & (kConvWarps - 1)]);
+          if (issued >= stages) mbar_arrive(&formed[(issued - stages) & (kConvWarps - 1)]);
           mbar_arrive_expect_tx(bar, kBoxBytes);
           uint8_t* to = smem + stage * stage_bytes + b * kBoxBytes;
           if (p.tiled)
@@ -353,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           else
             tma_load_2d_hint(to, map, bar, kb * 128, row, once);
           ++issued;
-          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+          if (++stage == static_cast<uint32_t>(stages)) { stage = 0; phase ^= 1u; }
         }
         u += w.kb1 - w.kb0;
       }
       // no TMA write may be in flight when the CTA exits or reuses its stages
-      const int outstanding = min(issued, p.stages);
+      const int outstanding = min(issued, stages);
       for (int i = 0; i < outstanding; ++i) {
-        if (stage == 0) { stage = p.stages; phase ^= 1u; }
+        if (stage == 0) { stage = stages; phase ^= 1u; }
         --stage;
         wait_quiet(&full[2 * stage + b], phase);
       }
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int u = u0; u < u1 && ok;) {
         const Unit w = unit_at(u);
         const int n = kTerms * padded(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
-        const uint32_t d = tmem_base + kAccCol + (2 * set + b) * p.acc_stride;
+        const uint32_t d = tmem_base + kAccCol + (2 * set + b) * acc_stride;
         const uint32_t idesc = FMT == kFp8 ? idesc_mxf8_e4m3(128, n, 0, 0) : idesc_bf16(128, n);
         if (PHASE == 1) {
           start = true;
@@ -400,12 +409,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           start = false;
           tc_commit(&empty[2 * stage + b]);
-          if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
+          if (++stage == static_cast<uint32_t>(stages)) { stage = 0; phase ^= 1u; }
         }
         u += w.kb1 - w.kb0;
         if (PHASE == 1 && ok) {
           tc_commit(&acc_full[set]);
-          if (++set == static_cast<uint32_t>(p.sets)) { set = 0; set_phase ^= 1u; }
+          if (++set == sets) { set = 0; set_phase ^= 1u; }
         }
       }
       if (PHASE == 2 && ok) tc_commit(&acc_full[0]);
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // anyway) on a barrier of the warp that formed it: this warp has seen the one before there complete, when it
     // formed K-block i - kConvWarps, and the one after cannot be yet (stages <= kConvWarps), so a parity says which.
     auto wait_stage = [&](int i) {
-      const int before = i - p.stages;
+      const int before = i - stages;
       return before < 0 || wait_all(&formed[before & (kConvWarps - 1)], (before / kConvWarps) & 1, abort_flag, p.err);
     };
     auto publish = [&](int stage) {
@@ -498,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = cw; u0 + i < u1; i += kConvWarps) {
         const Unit w = unit_at(u0 + i);
         const uint2 who = chosen[w.a];
-        const int n = __popc(who.x), stage = i % p.stages, rows = padded(n);
+        const int n = __popc(who.x), stage = i % stages, rows = padded(n);
         const uint8_t* list = token + (who.y >> 16);
         const bool sh = w.a == nchosen;
         const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
@@ -548,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const bool sh = w.a == nchosen;
         const uint2 who = chosen[w.a];
-        const int n = __popc(who.x), stage = i % p.stages;
+        const int n = __popc(who.x), stage = i % stages;
         const int width = sh ? p.S : p.I;
         const int64_t part_step = static_cast<int64_t>(sh ? p.T : p.R) * 2 * width;
         const int at = w.kb0 * (kLanes * 8) + sub * 8;                   // of h
@@ -626,12 +635,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       float* to = (sh ? p.part_shared : p.part) + row0 * 2 * width + w.j * 128 + 32 * q + lane;
       ok = ok && wait_all(&acc_full[set], set_phase, abort_flag, p.err);
       tc_fence_after();
-      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 2 * set * p.acc_stride;
+      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 2 * set * acc_stride;
       for (int b = 0; b < 2; ++b) {
         for (int c = 0; c < rows; c += 8) {
           uint32_t r[8], o[8];
-          tmem_ld_x8(acc + b * p.acc_stride + c, r);
-          tmem_ld_x8(acc + b * p.acc_stride + (kTerms - 1) * rows + c, o);
+          tmem_ld_x8(acc + b * acc_stride + c, r);
+          tmem_ld_x8(acc + b * acc_stride + (kTerms - 1) * rows + c, o);
           tmem_wait_ld_regs(r, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[set]);
-      if (++set == static_cast<uint32_t>(p.sets)) { set = 0; set_phase ^= 1u; }
+      if (++set == sets) { set = 0; set_phase ^= 1u; }
       u += w.kb1 - w.kb0;
     }
   }
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
     } else if (const int b = (warp - 4) >> 2; b < boxes) {
       const int q = warp & 3, rows = padded(p.T);
-      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + b * p.acc_stride;
+      const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + b * acc_stride;
       for (int c = 0; c < rows; c += 8) {
         uint32_t r[8], o[8];
         tmem_ld_x8(acc + c, r);
@@ -799,14 +808,12 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   a.nkb2_shared = a.S * kSize / 128;
   a.ctas1 = sms;
   const int rows = 2 * ((a.T + 7) / 8 * 8);      // of two terms (one term of bf16 takes no more)
-  a.operand_bytes = (rows * 128 + 1023) / 1024 * 1024;
-  a.acc_stride = (rows + 31) / 32 * 32;
-  const int tables = (((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5 + 15) / 16 * 16;
-  const int fixed = 1024 + kBarBytes + tables, stage_bytes = 2 * kBoxBytes + a.operand_bytes + kSfBytes;
-  a.stages = (kSmem - fixed) / stage_bytes;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  const size_t smem = fixed + a.stages * stage_bytes;
-  const int stages2 = std::min((kSmem - fixed) / stage_bytes, kMaxStages);
+  const int tables = kBarBytes + kMaxStages * kSfBytes + ((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5;
+  a.tables = (tables + 1023) / 1024 * 1024;
+
+  // two CTAs per SM, the kernels beside one another: two or three stages
+  a.stage_space = kSmem - a.tables;
+  const int space2 = kSmem - a.tables;
 
   // The second kernel: a CTA takes two 128-row tiles of W2 (the token operand is formed once for both), and the
   // contraction is split as far as all clusters still run at once, two CTAs per SM (the runtime's count is for one):
@@ -831,18 +838,19 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
 
   a.sf = sf13;
   a.sf_shared = sf13_shared;
-  a.sets = kAccCol + 4 * a.acc_stride <= 256 ? 2 : 1;       // (two CTAs share an SM's tensor memory)
-  a.tmem_cols = columns_of(kAccCol + 2 * a.sets * a.acc_stride);
+  // at least one set of sums for the most tokens; two CTAs share an SM's tensor memory
+  const int stride = (rows + 31) / 32 * 32;
+  a.tmem_cols = columns_of(kAccCol + (kAccCol + 4 * stride <= 256 ? 4 : 2) * stride);
   void* args1[] = {&m13, &s13, &a};
-  const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, smem, 0, s, args1);
+  const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, a.tables + a.stage_space, 0, s, args1);
   if (first != BSF_OK) return first;
   FewArgs b = a;
-  b.stages = stages2;
+  b.stage_space = space2;
   b.sf = sf2;
   b.sf_shared = sf2_shared;
-  b.tmem_cols = columns_of(kAccCol + 2 * a.acc_stride);
+  b.tmem_cols = columns_of(kAccCol + 2 * stride);
   void* args2[] = {&m2, &s2, &b};
-  return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, fixed + stages2 * stage_bytes, b.split, s, args2);
+  return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, a.tables + space2, b.split, s, args2);
 }
 
 }  // namespace
