@@ -47,7 +47,7 @@ constexpr int kParts = 4;                      // most CTAs that share a tile of
 // warps: 0 and 3 weight loads, 1 and 2 MMA issuers (one per box each), 4-7 and 8-11 as each kernel needs them
 constexpr int kThreads = 384;
 constexpr int kBarBytes = 512;                // barriers, tensor memory's place, abort flag, 32 words of groups, a maximum
-constexpr int kSmem = 113 * 1024;              // two CTAs per SM
+constexpr int kSmem = 113 * 1024;              // first kernel: 3 stages; with more in flight the SMs share HBM less evenly
 constexpr int kMostSmem = 227 * 1024;
 constexpr int kMaxSplit = 16;
 
@@ -121,6 +121,13 @@ __device__ __forceinline__ void split8(const float (&f)[8], float scale, uint2& 
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
+// x / (1 + exp(-x)); the argument of exp is rounded, an error of |x| 2**-24 of a term that matters up to |x| = 16 only.
+__device__ __forceinline__ float silu(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  return __fdividef(x, 1.f + e);
+}
+
 // A block's exponent for split8 and the factor 2**-e: NaN where the block holds an infinity (which E4M3 lacks), as a
 // NaN in the block is NaN without it.  At least `least`, so that the products' scales have an exponent.
 __device__ __forceinline__ int split_exponent(float amax, int least, float& scale) {
@@ -135,7 +142,7 @@ __device__ __forceinline__ uint8_t* operand_at(uint8_t* slot, int row, int chunk
 }
 
 template <int FMT, int PHASE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
     few_kernel(const __grid_constant__ CUtensorMap map_routed, const __grid_constant__ CUtensorMap map_shared,
                const FewArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -564,55 +571,64 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int item = w.a * tiles + (at >> 7);
         const int parts = ((item + 1) * p.nkb1 - 1) / per - item * p.nkb1 / per + 1;
         bool ok = true;
-        for (int j0 = 0; j0 < n && ok; j0 += kAtOnce) {
-          const int j = j0 + mine;
-          int t = 0;
-          float g[8] = {}, v[8] = {};
-          float weight = 1.f;
-          if (j < n) {
-            const int row = sh ? j : static_cast<int>(who.y >> 16) + j;
-            t = sh ? j : token[row];
-            weight = sh ? 1.f : share[row];
-            const float* from = (sh ? p.part_shared : p.part) + static_cast<int64_t>(row) * 2 * width + at;
+        const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
+        const float* base = (sh ? p.part_shared : p.part) + at;
+        constexpr int kRounds = 2;           // of tokens whose loads are in flight together, two parts of each
+        for (int j0 = 0; j0 < n && ok; j0 += kRounds * kAtOnce) {
+          float g[kRounds][8] = {}, v[kRounds][8] = {}, weight[kRounds];
+          int t[kRounds], row[kRounds];
 #pragma unroll
-            for (int s = 0; s < kParts; s += 2) {                        // two parts' loads at once
-              if (s >= parts) break;
-              const float* f0 = from + s * part_step;
-              const float* f1 = s + 1 < parts ? f0 + part_step : f0;
-              float4 a[4], c[4];
+          for (int k = 0; k < kRounds; ++k) {
+            const int j = j0 + k * kAtOnce + mine;
+            row[k] = -1, t[k] = 0, weight[k] = 1.f;
+            if (j < n) {
+              row[k] = sh ? j : static_cast<int>(who.y >> 16) + j;
+              t[k] = sh ? j : token[row[k]];
+              if (!sh) weight[k] = share[row[k]];
+            }
+          }
+          for (int s = 0; s < parts; s += 2) {
+            float4 a[kRounds][2][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) a[k] = __ldcg(reinterpret_cast<const float4*>(f0 + (k >> 1) * width) + (k & 1));
+            for (int k = 0; k < kRounds; ++k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) c[k] = __ldcg(reinterpret_cast<const float4*>(f1 + (k >> 1) * width) + (k & 1));
+              for (int q = 0; q < 2; ++q)
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                g[4 * k] += a[k].x, g[4 * k + 1] += a[k].y, g[4 * k + 2] += a[k].z, g[4 * k + 3] += a[k].w;
-                v[4 * k] += a[2 + k].x, v[4 * k + 1] += a[2 + k].y, v[4 * k + 2] += a[2 + k].z, v[4 * k + 3] += a[2 + k].w;
-              }
-              if (s + 1 < parts) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  g[4 * k] += c[k].x, g[4 * k + 1] += c[k].y, g[4 * k + 2] += c[k].z, g[4 * k + 3] += c[k].w;
-                  v[4 * k] += c[2 + k].x, v[4 * k + 1] += c[2 + k].y, v[4 * k + 2] += c[2 + k].z, v[4 * k + 3] += c[2 + k].w;
+                for (int i4 = 0; i4 < 4; ++i4) {
+                  a[k][q][i4] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (row[k] >= 0 && s + q < parts)
+                    a[k][q][i4] = __ldcg(reinterpret_cast<const float4*>(base + (s + q) * part_step +
+                                                                         (2 * static_cast<int64_t>(row[k]) + (i4 >> 1)) * width) + (i4 & 1));
                 }
-              }
-            }
+#pragma unroll
+            for (int k = 0; k < kRounds; ++k)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i4 = 0; i4 < 2; ++i4) {
+                  const float4 x = a[k][q][i4], y = a[k][q][2 + i4];
+                  g[k][4 * i4] += x.x, g[k][4 * i4 + 1] += x.y, g[k][4 * i4 + 2] += x.z, g[k][4 * i4 + 3] += x.w;
+                  v[k][4 * i4] += y.x, v[k][4 * i4 + 1] += y.y, v[k][4 * i4 + 2] += y.z, v[k][4 * i4 + 3] += y.w;
+                }
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) g[k] = __fdividef(g[k], 1.f + expf(-g[k])) * v[k] * weight;
-          const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
-          const Terms r = terms_of(g, e0, e1);
-          if (j0 == 0) {
-            ok = wait_stage(i);
-            if (!ok) break;
-            uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
-            for (int z = lane >> 3; z < rows; z += 4) {
-              if (who.x >> z & 1u) continue;
-              *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < kRounds; ++k) {
+            if (j0 + k * kAtOnce >= n) break;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) g[k][c] = silu(g[k][c]) * v[k][c] * weight[k];
+            const Terms r = terms_of(g[k], e0, e1);
+            if (j0 + k == 0) {
+              ok = wait_stage(i);
+              if (!ok) break;
+              uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
+              for (int z = lane >> 3; z < rows; z += 4) {
+                if (who.x >> z & 1u) continue;
+                *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
+              }
             }
+            if (row[k] >= 0) put(r, stage, t[k], rows, e0, e1);
           }
-          if (j < n) put(r, stage, t, rows, e0, e1);
         }
         if (!ok) break;
         publish(stage);
@@ -766,7 +782,7 @@ bsf_status few_limits(const FewLimits** out) {
     if (cudaFuncSetAttribute(kernels[1], cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return BSF_ERR_CUDA;
     for (int i = 1; i <= kMaxSplit; ++i) {
-      DependentLaunch launch(i, kThreads, kSmem, nullptr, i);
+      DependentLaunch launch(i, kThreads, kMostSmem, nullptr, i);
       launch.cfg.numAttrs = 1;                       // the cluster alone
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, kernels[1], &launch.cfg) != cudaSuccess) {
@@ -811,20 +827,20 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   const int tables = kBarBytes + kMaxStages * kSfBytes + ((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5;
   a.tables = (tables + 1023) / 1024 * 1024;
 
-  // two CTAs per SM, the kernels beside one another: two or three stages
   a.stage_space = kSmem - a.tables;
-  const int space2 = kSmem - a.tables;
+  const int space2 = kMostSmem - a.tables;
 
-  // The second kernel: a CTA takes two 128-row tiles of W2 (the token operand is formed once for both), and the
-  // contraction is split as far as all clusters still run at once, two CTAs per SM (the runtime's count is for one):
-  // K 4096 takes clusters of 12 (16 tokens: 202 us, of 8 209, of 16 224), K 2048 of 16 (bf16, 7 tokens: 98 us, of 8 110).
+  // The second kernel: a CTA takes two 128-row tiles of W2, for which the token operand is formed once (one where K is
+  // so small that there would be few CTAs), and an SM to itself: 5 stages in each of 96 SMs draw more from HBM than 2 or
+  // 3 in twice as many CTAs (32 tokens of 128 experts, K 4096, I 1536: 304 us against 322; 1 token 33.5 against 34.0), and
+  // one round of CTAs more than two.  So the contraction is split as far as all clusters surely run at once.
   const int tiles = a.K / 128;
-  a.nbox = 2;
+  a.nbox = (tiles + 1) / 2 * kMaxSplit >= 96 ? 2 : 1;
   const int clusters = (tiles + a.nbox - 1) / a.nbox;
   const int64_t most = static_cast<int64_t>(a.E < a.R ? a.E : a.R) * a.nkb2 + a.nkb2_shared;   // K-blocks
   a.split = 1;
   for (int i = 2; i <= kMaxSplit && i <= most; ++i)
-    if (2 * limits->clusters[i].load(std::memory_order_relaxed) >= clusters) a.split = i;
+    if (limits->clusters[i].load(std::memory_order_relaxed) > clusters) a.split = i;
 
   CUtensorMap m13, m2, s13, s2;
   if (!make_weight_map(&m13, w13, static_cast<int64_t>(a.E) * 2 * a.I, static_cast<int64_t>(a.K) * kSize, a.tiled) ||
