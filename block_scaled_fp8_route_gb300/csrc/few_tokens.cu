@@ -142,7 +142,7 @@ __device__ __forceinline__ uint8_t* operand_at(uint8_t* slot, int row, int chunk
 }
 
 template <int FMT, int PHASE>
-__global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap map_routed, const __grid_constant__ CUtensorMap map_shared,
                const FewArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
 
   const int tiles = p.I >> 7;              // 128-wide tiles of h per expert
   int u0, u1, per = 1;                     // this CTA's K-blocks
+  int first_routed = 0, mine_routed = 0, first_shared = 0;     // (second kernel)
   {
     const int routed = PHASE == 1 ? nchosen * tiles * p.nkb1 : nchosen * p.nkb2;
     const int units = routed + (PHASE == 1 ? (p.S >> 7) * p.nkb1 : p.nkb2_shared);
@@ -283,8 +284,12 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
       u0 = min(units, static_cast<int>(blockIdx.x) * per);
       u1 = min(units, u0 + per);
     } else {
-      u0 = static_cast<int>(static_cast<int64_t>(units) * rank / p.split);
-      u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / p.split);
+      // a share of the routed experts' and one of the shared expert's, whose operand takes longer to form
+      first_routed = static_cast<int>(static_cast<int64_t>(routed) * rank / p.split);
+      mine_routed = static_cast<int>(static_cast<int64_t>(routed) * (rank + 1) / p.split) - first_routed;
+      first_shared = p.nkb2_shared * rank / p.split;
+      u0 = 0;
+      u1 = mine_routed + p.nkb2_shared * (rank + 1) / p.split - first_shared;
     }
   }
   auto unit_at = [&](int u) {
@@ -296,10 +301,16 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
       w.kb0 = u - item * p.nkb1;
       w.kb1 = min(p.nkb1, w.kb0 + u1 - u);
     } else {
-      w.a = min(u / p.nkb2, nchosen);
       w.j = 0;
-      w.kb0 = u - w.a * p.nkb2;
-      w.kb1 = min(w.a < nchosen ? p.nkb2 : p.nkb2_shared, w.kb0 + u1 - u);
+      if (u < mine_routed) {
+        w.a = (first_routed + u) / p.nkb2;
+        w.kb0 = first_routed + u - w.a * p.nkb2;
+        w.kb1 = min(p.nkb2, w.kb0 + mine_routed - u);
+      } else {
+        w.a = nchosen;
+        w.kb0 = first_shared + u - mine_routed;
+        w.kb1 = w.kb0 + u1 - u;
+      }
     }
     return w;
   };
@@ -520,25 +531,39 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
         const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
         const uint16_t* from = p.x + w.kb0 * (kLanes * 8) + sub * 8;
         bool ok = true;
-        for (int j0 = 0; j0 < n && ok; j0 += kBatch * kAtOnce) {
-          uint4 v[kBatch];
+        const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
+        uint4 v[kBatch];
+        auto load = [&](int j0) {
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int j = j0 + k * kAtOnce + mine;
             v[k] = make_uint4(0, 0, 0, 0);
             if (j < n) v[k] = __ldg(reinterpret_cast<const uint4*>(from + (sh ? j : list[j]) * p.ldx));
           }
-          const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
+        };
+        load(0);
+        for (int j0 = 0; j0 < n && ok; j0 += kBatch * kAtOnce) {
+          // A batch's terms side by side, and the next one's loads, before the stage is waited for: a stage held up holds
+          // up its own next loads.
+          auto term = [&](int k) {
+            float f[8];
+            bf16x8_to_float(v[k], f);
+            return terms_of(f, e0, e1);
+          };
+          Terms r[kBatch];
+          r[0] = term(0);
+          const bool more = n - j0 > kAtOnce;
+          if (more) {
+#pragma unroll
+            for (int k = 1; k < kBatch; ++k) r[k] = term(k);
+          }
+          if (n - j0 > kBatch * kAtOnce) load(j0 + kBatch * kAtOnce);
+          if (j0 == 0) ok = wait_stage(i);
+          if (!ok) break;
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int row = j0 + k * kAtOnce + mine;
-            if (row - mine >= n) break;
-            float f[8];
-            bf16x8_to_float(v[k], f);
-            const Terms r = terms_of(f, e0, e1);
-            if (j0 + k == 0) ok = wait_stage(i);
-            if (!ok) break;
-            if (row < rows) put(r, stage, row, rows, e0, e1);
+            if ((k == 0 || more) && row < rows) put(r[k], stage, row, rows, e0, e1);
           }
         }
         if (!ok) break;
@@ -587,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
               if (!sh) weight[k] = share[row[k]];
             }
           }
-          for (int s = 0; s < parts; s += 2) {
+          // (a single round takes the other one's registers for two more parts)
+          const bool narrow = n - j0 <= kAtOnce;
+          for (int s = 0; s < parts; s += narrow ? 4 : 2) {
             float4 a[kRounds][2][4];
 #pragma unroll
             for (int k = 0; k < kRounds; ++k)
@@ -596,9 +623,10 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
 #pragma unroll
                 for (int i4 = 0; i4 < 4; ++i4) {
                   a[k][q][i4] = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (row[k] >= 0 && s + q < parts)
-                    a[k][q][i4] = __ldcg(reinterpret_cast<const float4*>(base + (s + q) * part_step +
-                                                                         (2 * static_cast<int64_t>(row[k]) + (i4 >> 1)) * width) + (i4 & 1));
+                  const int r = narrow ? row[0] : row[k], part = narrow ? s + 2 * k + q : s + q;
+                  if (r >= 0 && part < parts)
+                    a[k][q][i4] = __ldcg(reinterpret_cast<const float4*>(base + part * part_step +
+                                                                         (2 * static_cast<int64_t>(r) + (i4 >> 1)) * width) + (i4 & 1));
                 }
 #pragma unroll
             for (int k = 0; k < kRounds; ++k)
@@ -610,6 +638,11 @@ __global__ void __launch_bounds__(kThreads, PHASE == 1 ? 2 : 1)
                   g[k][4 * i4] += x.x, g[k][4 * i4 + 1] += x.y, g[k][4 * i4 + 2] += x.z, g[k][4 * i4 + 3] += x.w;
                   v[k][4 * i4] += y.x, v[k][4 * i4 + 1] += y.y, v[k][4 * i4 + 2] += y.z, v[k][4 * i4 + 3] += y.w;
                 }
+            static_assert(kRounds == 2 && kParts == 4, "a single round takes all parts");
+            if (narrow) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) g[0][c] += g[1][c], v[0][c] += v[1][c], g[1][c] = v[1][c] = 0.f;
+            }
           }
 #pragma unroll
           for (int k = 0; k < kRounds; ++k) {
