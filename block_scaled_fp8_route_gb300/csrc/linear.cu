@@ -154,22 +154,72 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
   }
 }
 
-// Tokens [j0, j1) of a tile: their S partials part[token][weight row], one in each CTA of the cluster, summed in
-// rank order, through the epilogue and stored.  A thread takes items (token, four weight rows) and has the loads of U
-// of them in flight.
+// Bias and residual of four weight rows of one token.
+struct Beside {
+  float b[4], r[4];
+};
+template <int OUT>
+__device__ __forceinline__ Beside beside(const SplitArgs& p, int64_t row, int n) {
+  const Epilogue& e = p.e;
+  Beside v = {};
+  if (n >= p.N) return v;
+  if (e.bias) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v.b[x] = load_as_float(e.bias, min(n + x, p.N - 1), e.bias_type);
+  }
+  if (e.residual) {
+    if (e.wide && n + 4 <= p.N) {
+      if (OUT == BSF_TYPE_F32) {
+        const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + row * e.ldr + n);
+        v.r[0] = r.x, v.r[1] = r.y, v.r[2] = r.z, v.r[3] = r.w;
+      } else {
+        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.residual) + row * e.ldr + n);
+        const float2 a = unpack2<OUT>(r.x), b = unpack2<OUT>(r.y);
+        v.r[0] = a.x, v.r[1] = a.y, v.r[2] = b.x, v.r[3] = b.y;
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v.r[x] = residual_at<OUT>(e, row * e.ldr + min(n + x, p.N - 1));
+    }
+  }
+  return v;
+}
+
+// The end of a CTA of a split product: once every CTA of the cluster has its partial part[token][weight row] in its
+// shared memory, tokens [j0, j1) of the tile are summed over the S partials in rank order, taken through the epilogue and
+// stored.  A thread takes items (token, four weight rows) and has the loads of U of them in flight; those of the first
+// items' bias and residual are under way before the barrier.
 template <int OUT, int S, int U>
-__device__ __forceinline__ void sum_and_store(const SplitArgs& p, uint32_t part, int n0, int tok0, int j0, int j1) {
+__device__ __forceinline__ void sum_and_store(const SplitArgs& p, uint32_t part, int n0, int tok0, int j0, int j1,
+                                              uint32_t tmem_base, volatile int* abort_flag) {
+  auto at = [&](int i0, int u) { return min(i0 + u * kThreads, j1 * 32 - 1); };   // (past the end: the last item again)
+  Beside with[U];
+  const int first = threadIdx.x + j0 * 32;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (first + u * kThreads < j1 * 32)
+      with[u] = beside<OUT>(p, tok0 + (at(first, u) >> 5), n0 + (at(first, u) & 31) * 4);
+  tc_fence_before();
+  if (S > 1) cluster_sync(); else __syncthreads();
+  if (threadIdx.x >> 5 == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+  if (*abort_flag != 0) return;
   uint32_t base[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) base[s] = map_rank(part, s);
   const Epilogue& e = p.e;
-  for (int i0 = threadIdx.x + j0 * 32; i0 < j1 * 32; i0 += U * kThreads) {
+  for (int i0 = first; i0 < j1 * 32; i0 += U * kThreads) {
     float4 v[U][S];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u * kThreads, j1 * 32 - 1);     // (past the end: the last item again, not stored)
 #pragma unroll
-      for (int s = 0; s < S; ++s) v[u][s] = ld_cluster_f4(base[s] + i * 16);
+      for (int s = 0; s < S; ++s) v[u][s] = ld_cluster_f4(base[s] + at(i0, u) * 16);
+    }
+    if (i0 != first) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) with[u] = beside<OUT>(p, tok0 + (at(i0, u) >> 5), n0 + (at(i0, u) & 31) * 4);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -188,34 +238,23 @@ __device__ __forceinline__ void sum_and_store(const SplitArgs& p, uint32_t part,
       const int64_t row = tok0 + (i >> 5);
       if (e.bias) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (n + x < p.N) f[x] += load_as_float(e.bias, n + x, e.bias_type);
+        for (int x = 0; x < 4; ++x) f[x] += with[u].b[x];
       }
       activate(f, e.act);
+      if (e.residual) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] += with[u].r[x];
+      }
       if (e.wide && n + 4 <= p.N) {
-        if (OUT == BSF_TYPE_F32) {
-          float* to = static_cast<float*>(e.y) + row * e.ldy + n;
-          if (e.residual) {
-            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + row * e.ldr + n);
-            f[0] += r.x, f[1] += r.y, f[2] += r.z, f[3] += r.w;
-          }
-          *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-        } else {
-          uint16_t* to = static_cast<uint16_t*>(e.y) + row * e.ldy + n;
-          if (e.residual) {
-            const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(e.residual) + row * e.ldr + n);
-            const float2 a = unpack2<OUT>(r.x), b = unpack2<OUT>(r.y);
-            f[0] += a.x, f[1] += a.y, f[2] += b.x, f[3] += b.y;
-          }
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]));
-        }
+        if (OUT == BSF_TYPE_F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(e.y) + row * e.ldy + n) = make_float4(f[0], f[1], f[2], f[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(e.y) + row * e.ldy + n) =
+              make_uint2(pack2<OUT>(f[0], f[1]), pack2<OUT>(f[2], f[3]));
       } else {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (n + x >= p.N) break;
-          const float r = e.residual ? residual_at<OUT>(e, row * e.ldr + n + x) : 0.f;
-          store_at<OUT>(e, row * e.ldy + n + x, f[x] + r);
-        }
+        for (int x = 0; x < 4; ++x)
+          if (n + x < p.N) store_at<OUT>(e, row * e.ldy + n + x, f[x]);
       }
     }
   }
@@ -354,25 +393,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < 32; ++j) part[(c0 + j) * kTileW] = __uint_as_float(r[j]);
     }
   }
-  tc_fence_before();
-  if (p.split > 1) cluster_sync(); else __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, p.tmem_cols);
-  }
-  if (*abort_flag == 0) {
-    const int j0 = ntok * rank / p.split, j1 = ntok * (rank + 1) / p.split, n0 = nt * kTileW;
-    const uint32_t part = smem_u32(smem);
-    switch (p.split) {
-      case 1: sum_and_store<OUT, 1, 4>(p, part, n0, tok0, j0, j1); break;
-      case 2: sum_and_store<OUT, 2, 4>(p, part, n0, tok0, j0, j1); break;
-      case 3: sum_and_store<OUT, 3, 2>(p, part, n0, tok0, j0, j1); break;
-      case 4: sum_and_store<OUT, 4, 2>(p, part, n0, tok0, j0, j1); break;
-      case 5: sum_and_store<OUT, 5, 1>(p, part, n0, tok0, j0, j1); break;
-      case 6: sum_and_store<OUT, 6, 1>(p, part, n0, tok0, j0, j1); break;
-      case 7: sum_and_store<OUT, 7, 1>(p, part, n0, tok0, j0, j1); break;
-      default: sum_and_store<OUT, 8, 1>(p, part, n0, tok0, j0, j1); break;
-    }
+  const int j0 = ntok * rank / p.split, j1 = ntok * (rank + 1) / p.split, n0 = nt * kTileW;
+  const uint32_t part = smem_u32(smem);
+  switch (p.split) {
+    case 1: sum_and_store<OUT, 1, 4>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 2: sum_and_store<OUT, 2, 4>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 3: sum_and_store<OUT, 3, 2>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 4: sum_and_store<OUT, 4, 2>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 5: sum_and_store<OUT, 5, 1>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 6: sum_and_store<OUT, 6, 1>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    case 7: sum_and_store<OUT, 7, 1>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
+    default: sum_and_store<OUT, 8, 1>(p, part, n0, tok0, j0, j1, tmem_base, abort_flag); break;
   }
   // a CTA's shared memory stays until every CTA of the cluster has read it
   if (p.split > 1) cluster_sync();
@@ -383,8 +414,8 @@ constexpr int kPairW = 256;                                // weight rows of a t
 constexpr int kPairMaxTok = 256;                           // tokens of a tile (MMA N), half staged by each CTA
 constexpr int kPairMaxStages = 8;                          // a stage is one or two K-blocks of both operands
 constexpr int kSegment = 1024;                             // values of K that a float32 output's sum takes at once
-// warps: 0 weight loads, 1 waiter, 2 and 3 token loads and MMA issuer, 4-11 epilogue, 12 second issuer
-constexpr int kPairWaiter = 1, kPairTokLoads = 2, kPairIssuer = 3, kPairIssuer2 = 12;
+// warps: 0 loads, 1 waiter, 2 second MMA issuer (narrow tiles), 3 MMA issuer, 4-11 epilogue
+constexpr int kPairWaiter = 1, kPairIssuer2 = 2, kPairIssuer = 3, kPairThreads = 384;
 constexpr int kPairBarBytes = 256;
 
 struct PairArgs {
@@ -414,20 +445,40 @@ __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, u
 // One past the last stage of segment i.
 __device__ __forceinline__ int segment_end(const PairArgs& p, int i) { return p.nst * (i + 1) / p.segments; }
 
+// The residual of 32 tokens of one weight row per lane, as finish() takes it: with 16-bit types and aligned rows 16 words
+// of two neighbouring rows, of the tokens that the lane will have then, otherwise one value a token.
+template <int OUT, bool kResidual>
+__device__ __forceinline__ void fetch(const Epilogue& e, uint32_t (&w)[32], int64_t row, int rows, int n, int N) {
+  if (!kResidual || rows <= 0 || n >= N) return;
+  if (OUT == BSF_TYPE_F32 || !e.wide) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int64_t i = (row + min(j, rows - 1)) * e.ldr + n;
+      if (OUT == BSF_TYPE_F32) w[j] = static_cast<const uint32_t*>(e.residual)[i];
+      else w[j] = static_cast<const uint16_t*>(e.residual)[i];
+    }
+    return;
+  }
+  const int odd = n & 1;
+  const uint16_t* from = static_cast<const uint16_t*>(e.residual) + row * e.ldr + (n & ~1);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = *reinterpret_cast<const uint32_t*>(from + min(2 * j + odd, rows - 1) * e.ldr);
+}
+
 // 32 tokens of one weight row per lane -> y.  Two neighbouring lanes exchange halves, so that a lane holds two
 // neighbouring rows of one token (16-bit types).
-template <int OUT>
-__device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], float bias, int64_t row, int rows, int n, int N) {
+template <int OUT, bool kResidual>
+__device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], const uint32_t (&w)[32], float bias, int64_t row,
+                                       int rows, int n, int N) {
   const int odd = n & 1;
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] += bias;
   activate(v, e.act);
   if (OUT == BSF_TYPE_F32 || !e.wide) {
     if (n >= N) return;
-    if (e.residual) {
+    if (kResidual) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < rows) v[j] += residual_at<OUT>(e, (row + j) * e.ldr + n);
+      for (int j = 0; j < 32; ++j) v[j] += OUT == BSF_TYPE_F32 ? __uint_as_float(w[j]) : unpack2<OUT>(w[j]).x;
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -435,15 +486,6 @@ __device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], float 
     return;
   }
   // (N is even, so both rows of a word exist or neither does)
-  uint32_t w[16];
-  if (e.residual) {
-    const uint16_t* from = static_cast<const uint16_t*>(e.residual) + (row + odd) * e.ldr + (n & ~1);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      w[j] = 0u;
-      if (2 * j + odd < rows && n < N) w[j] = *reinterpret_cast<const uint32_t*>(from + 2 * j * e.ldr);
-    }
-  }
   uint16_t* to = static_cast<uint16_t*>(e.y) + (row + odd) * e.ldy + (n & ~1);
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -451,7 +493,7 @@ __device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], float 
     const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
     v0 = odd ? x : v0;
     v1 = odd ? v1 : x;
-    if (e.residual) {
+    if (kResidual) {
       const float2 r = unpack2<OUT>(w[j]);
       v0 += r.x;
       v1 += r.y;
@@ -460,8 +502,8 @@ __device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], float 
   }
 }
 
-template <int OUT, int kIssuers>
-__global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
+template <int OUT, int kIssuers, bool kResidual>
+__global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                        const PairArgs p) {
   extern __shared__ uint8_t smem_raw[];
@@ -512,26 +554,28 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t set_cols = kIssuers * p.acc_cols;          // of a set of accumulators, one per issuer
 
-  if (warp == 0 || warp == kPairTokLoads) {
-    // ------------------------------------------------------------ loads (each CTA its halves), a warp per operand
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads (each CTA its halves)
     // (where a stage is two K-blocks and K has an odd number the last one's second half is zeros, and not multiplied)
     if (lane == 0) {
-      const bool weights = warp == 0;
       uint32_t stage = 0, phase = 0;
       int issued = 0;
       bool ok = !p.withhold;
       for (int t = pair; t < total && ok; t += npairs) {
         const int tm = t % p.tiles_m, tn = t / p.tiles_m;
-        const int row = weights ? (tn * 2 + static_cast<int>(rank)) * kTileW : tm * p.tok + static_cast<int>(rank) * half_tok;
-        const CUtensorMap* map = weights ? &tmap_w : &tmap_x;
-        const int offset = weights ? 0 : p.blocks * kTileW * kRowBytes, block = weights ? kTileW * kRowBytes : tok_bytes;
+        const int w_row = (tn * 2 + static_cast<int>(rank)) * kTileW, x_row = tm * p.tok + static_cast<int>(rank) * half_tok;
         for (int kb = 0; kb < p.nkb; kb += p.blocks) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err)) { ok = false; break; }
           const uint32_t bar = map_rank(smem_u32(&full[stage]), 0);
-          uint8_t* dst = smem + stage * stage_bytes + offset;
-          if (weights && rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
-          pair_load_2d(dst, map, bar, kb * kBlockK, row);
-          if (p.blocks == 2) pair_load_2d(dst + block, map, bar, (kb + 1) * kBlockK, row);
+          uint8_t* dst = smem + stage * stage_bytes;
+          uint8_t* tok_dst = dst + p.blocks * kTileW * kRowBytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);   // both CTAs, both operands
+          pair_load_2d(dst, &tmap_w, bar, kb * kBlockK, w_row);
+          pair_load_2d(tok_dst, &tmap_x, bar, kb * kBlockK, x_row);
+          if (p.blocks == 2) {
+            pair_load_2d(dst + kTileW * kRowBytes, &tmap_w, bar, (kb + 1) * kBlockK, w_row);
+            pair_load_2d(tok_dst + tok_bytes, &tmap_x, bar, (kb + 1) * kBlockK, x_row);
+          }
           ++issued;
           if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase ^= 1u; }
         }
@@ -547,7 +591,7 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
       }
     }
     __syncwarp();
-  } else if (warp == kPairIssuer || warp >= kPairIssuer2) {
+  } else if (warp == kPairIssuer || (kIssuers == 2 && warp == kPairIssuer2)) {
     // ------------------------------------------------------------ MMA issuers (rank 0)
     // An issuing thread reads no shared memory between stages: the waiter warp does every wait and hands each stage
     // over through a named barrier whose OR-reduced predicate carries an abort.  With two issuers the stages of
@@ -626,7 +670,7 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
         if (kIssuers == 2 && (st + 1 < p.nst || t + npairs < total)) named_barrier_or(2 - me, 64, true);
       }
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue: lane = weight row, 32 tokens at a time
     // two warps share a quadrant's tokens
     const int q = warp & 3, ew = warp - 4;
@@ -638,6 +682,8 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
       const int64_t tok0 = static_cast<int64_t>(tm) * p.tok;
       const int rows = min(p.tok, p.M - static_cast<int>(tok0));
       const float bias = p.e.bias && n < p.N ? load_as_float(p.e.bias, n, p.e.bias_type) : 0.f;
+      uint32_t w[32];                       // the residual, in flight while the products run
+      fetch<OUT, kResidual>(p.e, w, tok0 + 32 * c_first, rows - 32 * c_first, n, p.N);
       bool ok = wait_all(&acc_full[acc], acc_phase, abort_flag, p.err);
       if (!ok) break;
       tc_fence_after();
@@ -671,7 +717,9 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int c = 32 * (c_first + i);
-          if (c_first + i < c_last && c < rows) finish<OUT>(p.e, v[i], bias, tok0 + c, min(32, rows - c), n, p.N);
+          if (c_first + i >= c_last || c >= rows) break;
+          if (i > 0) fetch<OUT, kResidual>(p.e, w, tok0 + c, rows - c, n, p.N);
+          finish<OUT, kResidual>(p.e, v[i], w, bias, tok0 + c, min(32, rows - c), n, p.N);
         }
       } else {
         const uint32_t taddr = quad + acc * set_cols;
@@ -693,7 +741,13 @@ __global__ void __launch_bounds__(32 * (11 + kIssuers), 1)
             __syncwarp();
             if (lane == 0) arrive_cluster(map_rank(smem_u32(&acc_empty[acc]), 0));
           }
-          if (32 * c < rows) finish<OUT>(p.e, v, bias, tok0 + 32 * c, min(32, rows - 32 * c), n, p.N);
+          if (32 * c < rows) {
+            uint32_t now[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) now[j] = w[j];
+            if (c + 1 < c_last) fetch<OUT, kResidual>(p.e, w, tok0 + 32 * (c + 1), rows - 32 * (c + 1), n, p.N);
+            finish<OUT, kResidual>(p.e, v, now, bias, tok0 + 32 * c, min(32, rows - 32 * c), n, p.N);
+          }
         }
         if ((acc ^= 1u) == 0u) acc_phase ^= 1u;
       }
@@ -732,10 +786,14 @@ uint32_t idesc_16(bool bf16, int m, int n) {
 }
 
 template <int OUT>
-const void* kernel_of(int form) {                  // 0 split, 1 and 2 pairs with so many issuers
-  return form == 0   ? reinterpret_cast<const void*>(linear_split_kernel<OUT>)
-         : form == 1 ? reinterpret_cast<const void*>(linear_pair_kernel<OUT, 1>)
-                     : reinterpret_cast<const void*>(linear_pair_kernel<OUT, 2>);
+const void* kernel_of(int form) {                  // 0 split; 1 and 2 pairs with so many issuers, 3 and 4 with a residual
+  switch (form) {
+    case 0: return reinterpret_cast<const void*>(linear_split_kernel<OUT>);
+    case 1: return reinterpret_cast<const void*>(linear_pair_kernel<OUT, 1, false>);
+    case 2: return reinterpret_cast<const void*>(linear_pair_kernel<OUT, 2, false>);
+    case 3: return reinterpret_cast<const void*>(linear_pair_kernel<OUT, 1, true>);
+    default: return reinterpret_cast<const void*>(linear_pair_kernel<OUT, 2, true>);
+  }
 }
 const void* kernel_of(int out, int form) {
   return out == BSF_TYPE_F32    ? kernel_of<BSF_TYPE_F32>(form)
@@ -757,7 +815,7 @@ bsf_status linear_limits(const LinearLimits** out) {
   LinearLimits& l = limits[dev];
   if (!l.ready.load(std::memory_order_acquire)) {      // (racing first calls store the same values)
     for (int type : {BSF_TYPE_F32, BSF_TYPE_BF16, BSF_TYPE_F16})
-      for (int form = 0; form < 3; ++form) {
+      for (int form = 0; form < 5; ++form) {
         const void* k = kernel_of(type, form);
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess ||
             cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
@@ -909,7 +967,7 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
     if (!make_map_16(&map_x, x, T, K, ldx, tok / 2)) return BSF_ERR_CUDA;
     const int64_t pairs = sm_count() / 2, used = tiles < pairs ? tiles : pairs;
     void* args[] = {&map_w, &map_x, &p};
-    return launch_cluster(kernel_of(y_type, issuers), static_cast<unsigned>(2 * used), 32 * (11 + issuers), kSmemBytes, 2, s,
+    return launch_cluster(kernel_of(y_type, issuers + (residual ? 2 : 0)), static_cast<unsigned>(2 * used), kPairThreads, kSmemBytes, 2, s,
                           args);
   }
 
