@@ -9,11 +9,17 @@
 // As in the dense FP8 product, weights are the MMA's M = 128 rows (256 in a CTA pair) and tokens its N, and the
 // forms are chosen by the time each would take (choose_plan):
 //
-// * Split (few tokens, or few tiles).  A tile's K is split over a cluster of CTAs, which exchange their
+// * Split (few tokens, or few tiles).  A tile's K is split over a cluster of 1 .. 8 CTAs, which exchange their
 //   FP32 partials through distributed shared memory and add them in rank order: no atomics, no workspace, the same
-//   bits every run.  Bias, activation and residual are applied to the sum, once per element.
+//   bits every run.  Bias, activation and residual are applied to the sum, once per element; bias and residual
+//   are under way before the cluster's barrier.  Bound by latency (1 x 256 x 7168 6.3 us, of which its 3.7 MB need 0.5;
+//   3 x 130 x 264 takes 4.3) or, with weights from HBM, by their stream plus those 4 (37 x 7168 x 4096 15.4 us: 60 MB, 8.8).
 // * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 256 tokens with one cta_group::2 MMA per 16 K;
-//   two accumulators let a tile's epilogue run under the next tile's MMAs.
+//   two accumulators let a tile's epilogue run under the next tile's MMAs.  What an SM takes in from L2, 53 bytes a cycle
+//   (the same from its own loads and by multicast), binds these tiles: 256 x 256 x 64 brings each SM 32 KB, 610
+//   cycles of loads for 512 of MMAs.  8192 x 7168 x 4096 with bias and residual takes 275-285 us in short runs, 1.69-1.75
+//   PFLOP/s, 89-92 % of the measured burst, and 290-320 where the power cap holds; 8192 x 256 x 7168 (tiles of 112 tokens in
+//   one round of CTAs) 32 us, 939 TFLOP/s; 777 x 4100 x 1416 with gelu 18.6 us, a quarter of it the epilogue.
 #include "cluster.cuh"
 #include "common.cuh"
 #include "host_utils.h"
@@ -443,7 +449,9 @@ __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, u
 }
 
 // One past the last stage of segment i.
-__device__ __forceinline__ int segment_end(const PairArgs& p, int i) { return p.nst * (i + 1) / p.segments; }
+__device__ __forceinline__ int segment_end(const PairArgs& p, int i) {
+  return static_cast<int>(static_cast<int64_t>(p.nst) * (i + 1) / p.segments);
+}
 
 // The residual of 32 tokens of one weight row per lane, as finish() takes it: with 16-bit types and aligned rows 16 words
 // of two neighbouring rows, of the tokens that the lane will have then, otherwise one value a token.
@@ -838,20 +846,20 @@ bsf_status linear_limits(const LinearLimits** out) {
   return BSF_OK;
 }
 
-// Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 1800 products
+// Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 2200 products
 // of 1 .. 8192 tokens, 16 .. 8192 weight rows and K of 64 .. 8192, drawn by their logarithms, with weights that come from
-// HBM, each timed in every form that could win (20000 in all).  The choice is 0.8 % above the best form on average, at
-// worst 38 % (2694 x 23 x 1528, in tiles of 64 tokens over 6 CTAs instead of 128 over 5); with K over 1, 2, 4 or
-// 8 CTAs alone it would be 2.8 %.  Both sides: 256 x 4096 x 4096 takes 17.3 us split and 18.5 in pairs, 1024 x 256 x
-// 7168 11.3 and 21, 777 x 4100 x 1416 34 and 15.7.
+// HBM, each timed in every form that could win (26000 in all).  The choice is 1.0 % above the best form on average, at
+// worst 25 % (141 x 5097 x 64: split 6.1 us, in pairs 4.9); with K over 1, 2, 4 or 8 CTAs alone it would be 3.0 %.
+// Both sides: 256 x 4096 x 4096 takes 17.3 us split and 18.5 in pairs, 1024 x 256 x 7168 11.3 and 21, 777 x 4100 x 1416
+// 34 and 15.7.
 struct Plan {
   bool pair;
   int tok;                  // pairs: tokens per tile; split: most tokens per tile
   int split;
 };
-Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, const LinearLimits& limits) {
+Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const LinearLimits& limits) {
   const int64_t nkb = (K + kBlockK - 1) / kBlockK, ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
-  const double read = 2.0 * K * (M + N) / 7221;        // of both operands from HBM
+  const double read = 2.0 * K * (M + N) / 6767;        // of both operands from HBM
   Plan best = {false, 64, 1};
   double least = 1e300;
   for (int tok = 64; tok <= kMaxTok; tok += 64) {
@@ -862,11 +870,11 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, const LinearLimits& 
       if (split > 1 && (nkb < 2 * split || ctas > 2 * sms)) break;
       const int64_t at_once = limits.ctas[split].load(std::memory_order_relaxed);
       const int64_t load = (ctas + at_once - 1) / at_once;            // CTAs of the busiest SM
-      const double once = 89 * per / sqrt(double(split)) + (split > 1 ? 513 + 53 * split : 0);
+      const double once = (residual ? 97.5 : 87.6) * per / sqrt(double(split)) + (split > 1 ? 547 + 52.6 * split : 0);
       // tiles of more than 64 tokens have an SM to themselves, others share one two at a time
-      const double busy = per > 64 ? load * (once + kbs * (206 + 0.55 * per))
-                                   : load / 2 * (once + 702.0 * kbs) + load % 2 * (once + 282.0 * kbs);
-      const double ns = 2558 + (busy > read ? busy : read);
+      const double busy = per > 64 ? load * (once + kbs * (209 + 0.43 * per))
+                                   : load / 2 * (once + 691.0 * kbs) + load % 2 * (once + 282.0 * kbs);
+      const double ns = 2638 + (busy > read ? busy : read);
       if (ns < least) {
         least = ns;
         best = {false, tok, split};
@@ -875,12 +883,11 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, const LinearLimits& 
   }
   for (int tok = f32 ? kMaxTok : kPairMaxTok; tok >= 64; tok -= 16) {      // (float32 sums live in registers)
     const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
-    const bool narrow = tok <= kMaxTok;
-    // a K-block: by the issuing threads, or by the tensor cores and L2
-    const double issue = narrow ? 143 : 261, multiply = narrow ? 105 + 1.5 * tok : 317 + 0.25 * tok;
-    const double loop = (narrow ? (nkb + 1) / 2 * 2 : nkb) * (issue > multiply ? issue : multiply);
-    const double store = tok * (f32 ? 15.0 : 10.4), busy = waves * (loop > 1456 + store ? loop : 1456 + store);
-    const double ns = 3920 + (busy > read ? busy : read) + store;
+    // a K-block: what an SM takes from L2, 53 bytes a cycle, binds every tile (wide ones nearly the tensor cores, too)
+    const double loop = tok <= kMaxTok ? (nkb + 1) / 2 * 2 * (140 + 1.27 * tok) : 380.0 * nkb;
+    const double store = tok * (8.65 + (f32 ? 3.15 : 0) + (residual ? 2.83 : 0));
+    const double busy = waves * (loop > 2299 + store ? loop : 2299 + store);
+    const double ns = 3930 + (busy > read ? busy : read) + store;
     if (ns < least) {
       least = ns;
       best = {true, tok, 1};
@@ -923,7 +930,7 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   const LinearLimits* limits;
   const bsf_status st = linear_limits(&limits);
   if (st != BSF_OK) return st;
-  const Plan plan = choose_plan(T, N, K, y_type == BSF_TYPE_F32, *limits);
+  const Plan plan = choose_plan(T, N, K, y_type == BSF_TYPE_F32, residual != nullptr, *limits);
   Epilogue e;
   e.bias = bias;
   e.residual = residual;

@@ -657,8 +657,9 @@ bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, 
  * terms, exact for values within 2^-14 of the largest of their 128 and off by
  * at most 2^-21 of that largest below (h: also 2^-9 of its own size; bf16
  * weights: h is rounded to bf16).  The weight topk_weights enters before that.  The order
- * of all sums is fixed: results are bit-identical from run to run.  An infinity
- * or NaN in x gives NaN in that token's z.
+ * of all sums is fixed: results are bit-identical from run to run.  A token
+ * whose x holds an infinity or NaN gets a z that is not finite; others are
+ * not affected.
  * T <= 32, kr <= 32, E <= 1024 (else BSF_ERR_UNSUPPORTED); K, I and S
  * multiples of 128; 16-byte aligned x and weights; z and addend need only their element
  * alignment (8 bytes and row strides of 4 elements are faster).  flags:
