@@ -36,6 +36,7 @@ constexpr int kBlockK = 64;                     // K per block: rows of 128 byte
 constexpr int kRowBytes = 128;
 constexpr int kMaxTok = 128;                    // split: tokens per tile
 constexpr int kMaxIssuers = 2;
+constexpr int kSegment = 1024;                  // values of K that a float32 output's sum takes at once (pairs: two halves)
 constexpr int kThreads = 32 * (1 + kMaxIssuers + 4);   // split: loads, issuers, four warps for the accumulators
 constexpr int kMaxStages = 12;
 constexpr int kBarBytes = 512;
@@ -57,7 +58,8 @@ struct SplitArgs {
   int M, N, nkb;
   int chunks, per;           // token chunks per weight tile, tokens of a full chunk (multiple of 16)
   int split, stages;
-  int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between their accumulators
+  int issuers, acc_stride;   // MMA-issuing warps (a power of two), columns between accumulators
+  int runs;                  // accumulators of an issuer, one after the other: its sum's parts
   uint32_t tmem_cols, idesc;
   int withhold;              // BSF_DEBUG_WITHHOLD_LOADS, in the last CTA of each cluster
   int* err;
@@ -343,13 +345,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else if (warp <= kMaxIssuers) {
     // ------------------------------------------------------------ MMA issuers
     // Issuer i takes the K-blocks (kb - kb0) % issuers == i into an accumulator of its own: four narrow MMAs with
-    // their wait and commit keep a thread busy longer than the loads of a block take.
+    // their wait and commit keep a thread busy longer than the loads of a block take.  The tensor cores cut each sum
+    // off, so a long one drifts towards zero; for a float32 output it is taken in runs (issuer_runs), each in
+    // columns of its own, which the epilogue adds: 2000 x 256 x 16384 is off by 2.1e-6 in one run and 9.9e-7 in these.
     const int me = warp - 1;
     if (me < p.issuers && lane == 0) {
-      const uint32_t d_tmem = tmem_base + me * p.acc_stride;
+      uint32_t d_tmem = tmem_base + me * p.runs * p.acc_stride;
       uint32_t stage = me, phase = 0;      // (stages are a multiple of issuers: a stage keeps its issuer)
       bool first = true;
+      const int count = (kb1 - kb0 - me + p.issuers - 1) / p.issuers;
+      int run = 0, left = count / p.runs;  // K-blocks of the run
       for (int kb = kb0 + me; kb < kb1; kb += p.issuers) {
+        if (left == 0) {
+          ++run;
+          left = static_cast<int>(static_cast<int64_t>(count) * (run + 1) / p.runs) -
+                 static_cast<int>(static_cast<int64_t>(count) * run / p.runs);
+          d_tmem += p.acc_stride;
+          first = true;
+        }
+        --left;
         if (!mbar_wait(&full[stage], phase, abort_flag, p.err)) break;
         tc_fence_after();
         const uint8_t* src = smem + stage * stage_bytes;
@@ -385,12 +399,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int q = warp & 3;
     const uint32_t quad = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     float* part = reinterpret_cast<float*>(smem) + 32 * q + lane;
+    const int accumulators = p.issuers * p.runs;
     for (int c0 = 0; c0 < ntok; c0 += 32) {      // (whole chunks: the rows past ntok are not read)
       uint32_t r[32], o[32];
       tmem_ld_x32(quad + c0, r);
-      if (p.issuers == 2) tmem_ld_x32(quad + p.acc_stride + c0, o);
+      if (accumulators > 1) tmem_ld_x32(quad + p.acc_stride + c0, o);
       tmem_wait_ld_regs(r);
-      if (p.issuers == 2) {
+      for (int a = 1; a < accumulators; ++a) {
+        if (a > 1) tmem_ld_x32(quad + a * p.acc_stride + c0, o);
         tmem_wait_ld_regs(o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(o[j]));
@@ -419,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 constexpr int kPairW = 256;                                // weight rows of a tile (MMA M), 128 per CTA
 constexpr int kPairMaxTok = 256;                           // tokens of a tile (MMA N), half staged by each CTA
 constexpr int kPairMaxStages = 8;                          // a stage is one or two K-blocks of both operands
-constexpr int kSegment = 1024;                             // values of K that a float32 output's sum takes at once
 // warps: 0 loads, 1 waiter, 2 second MMA issuer (narrow tiles), 3 MMA issuer, 4-11 epilogue
 constexpr int kPairWaiter = 1, kPairIssuer2 = 2, kPairIssuer = 3, kPairThreads = 384;
 constexpr int kPairBarBytes = 256;
@@ -846,6 +861,19 @@ bsf_status linear_limits(const LinearLimits** out) {
   return BSF_OK;
 }
 
+// Split: the issuers of a CTA, and the accumulators that each needs for runs of kSegment values of a float32 output's
+// sum.  TMEM holds 256 columns for each of two CTAs of an SM, 512 for one alone.
+int split_issuers(int64_t nkb, int split) { return nkb / split >= kMaxIssuers ? kMaxIssuers : 1; }
+int issuer_runs(int64_t nkb, int split, bool f32) {
+  const int64_t count = ((nkb + split - 1) / split + split_issuers(nkb, split) - 1) / split_issuers(nkb, split);
+  const int64_t runs = f32 ? (count * kBlockK + kSegment - 1) / kSegment : 1;
+  return static_cast<int>(runs < 1024 ? runs : 1024);
+}
+int acc_columns(int64_t per) { return static_cast<int>((per + 31) / 32 * 32); }
+bool runs_fit(int64_t nkb, int split, int64_t per, bool f32) {
+  return split_issuers(nkb, split) * issuer_runs(nkb, split, f32) * acc_columns(per) <= (per <= 64 ? 256 : 512);
+}
+
 // Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 2200 products
 // of 1 .. 8192 tokens, 16 .. 8192 weight rows and K of 64 .. 8192, drawn by their logarithms, with weights that come from
 // HBM, each timed in every form that could win (26000 in all).  The choice is 1.0 % above the best form on average, at
@@ -868,6 +896,7 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const
     for (int split = 1; split <= kMaxSplit; ++split) {
       const int64_t ctas = ntn * chunks * split, kbs = (nkb + split - 1) / split;
       if (split > 1 && (nkb < 2 * split || ctas > 2 * sms)) break;
+      if (!runs_fit(nkb, split, per, f32)) continue;                  // (pairs add runs of any number)
       const int64_t at_once = limits.ctas[split].load(std::memory_order_relaxed);
       const int64_t load = (ctas + at_once - 1) / at_once;            // CTAs of the busiest SM
       const double once = (residual ? 97.5 : 87.6) * per / sqrt(double(split)) + (split > 1 ? 547 + 52.6 * split : 0);
@@ -993,12 +1022,13 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   const size_t smem = p.per <= 64 ? kHalfSmemBytes : kSmemBytes;
   p.stages = (static_cast<int>(smem) - 1024 - kBarBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.acc_stride = (p.per + 31) / 32 * 32;
-  // (an issuer without a K-block would leave its accumulator unwritten)
-  p.issuers = nkb / p.split >= kMaxIssuers ? kMaxIssuers : 1;
+  p.acc_stride = acc_columns(p.per);
+  // (an issuer or a run without a K-block would leave its accumulator unwritten: every run has 15 or more, or is alone)
+  p.issuers = split_issuers(nkb, p.split);
+  p.runs = issuer_runs(nkb, p.split, y_type == BSF_TYPE_F32);
   p.stages = p.stages / p.issuers * p.issuers;
-  const int cols = p.issuers * p.acc_stride;
-  p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+  p.tmem_cols = 32;
+  while (static_cast<int>(p.tmem_cols) < p.issuers * p.runs * p.acc_stride) p.tmem_cols *= 2;
   p.idesc = idesc_16(type == BSF_TYPE_BF16, kTileW, p.per);
   p.withhold = withhold;
   p.err = err;

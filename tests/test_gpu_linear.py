@@ -191,3 +191,22 @@ def test_a_wait_that_runs_out(dev, T, N, K):
     assert torch.all(y == 3.0)
     assert torch.equal(p.run(), want)
     assert ops.device_error() == 0
+
+
+def test_no_tokens(dev):
+    w = torch.zeros(40, 64, dtype=BF16, device=dev)
+    assert ops.linear(torch.zeros(0, 64, dtype=BF16, device=dev), w).shape == (0, 40)
+    assert ops.device_error() == 0
+
+
+# (split over a cluster, in one run of K a CTA or more; the last two in pairs)
+@pytest.mark.parametrize("T,K", [(40, 16384), (2000, 16384), (3, 40000), (16, 11200), (100, 9000), (1, 140000), (100, 70000)])
+def test_long_sums_in_float32(dev, T, K):
+    """An error that grows with the number of terms would show.  The tensor core cuts its sum off every 16 products, by
+    half of 2**-23 of it on average, 0.72 of that over the mantissas; the sum grows as a root, which leaves 2/3: a run
+    of 1024 products drifts by 64 * 2/3 * 0.72 * 2**-24 = 1.8e-6 of itself, and runs do not drift together."""
+    p = Problem(dev, T, 256, K, BF16, F32)
+    y = p.run()
+    p.check(y)
+    ref = oracle.linear.linear(wide(p.x), wide(p.w))
+    assert np.linalg.norm(wide(y) - ref) <= 2e-6 * np.linalg.norm(ref)
