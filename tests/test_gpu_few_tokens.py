@@ -240,3 +240,50 @@ def test_a_wait_that_runs_out(dev):
     assert torch.all(torch.isnan(z) | (z == 3.0))
     assert torch.equal(layer.call(x, ids, p), want)
     assert ops.device_error() == 0
+
+
+def test_no_tokens(dev):
+    layer = Layer(dev, 4, 256, 128, 128)
+    x, ids, p = inputs(dev, 3, 256, 4, 2)
+    z = layer.call(x[:0], ids[:0], p[:0])
+    assert z.shape == (0, 256) and ops.device_error() == 0
+
+
+def test_graph_and_eager_calls_that_allocate_their_own_workspace(dev):
+    """Two captured calls and eager ones in between, none with a workspace of the caller's."""
+    layer = Layer(dev, 16, 512, 256, 128)
+    cases = [inputs(dev, T, 512, 16, 3, seed=T) for T in (4, 29)]
+    want = [layer.call(*c).clone() for c in cases]
+    graphs = []
+    for c in cases:
+        z = torch.empty_like(c[0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.call(*c, z=z)
+            layer.call(*c, z=z)
+        graphs.append((g, z))
+    for _ in range(5):
+        for (g, z), c, w in zip(graphs, cases, want):
+            z.zero_()
+            g.replay()
+            other = [torch.empty(1 << 16, dtype=torch.uint8, device=dev).fill_(255) for _ in range(4)]
+            assert torch.equal(layer.call(*c), w)
+            torch.cuda.synchronize()
+            assert torch.equal(z, w) and len(other) == 4
+
+
+def test_more_experts_than_a_table_of_one_warp(dev):
+    """1024 experts, as many as there may be, most of them chosen by nobody or by one token."""
+    layer = Layer(dev, 1024, 128, 128, seed=1)
+    x, ids, p = inputs(dev, 32, 128, 1024, 32, 7)
+    ids[0, 0], ids[31, 31] = 0, 1023
+    layer.check(layer.call(x, ids, p), x, ids, p)
+
+
+@pytest.mark.parametrize("K,I,S", [(2176, 128, 0), (2048, 1408, 2816)])
+def test_second_products_in_pairs_of_tiles(dev, K, I, S):
+    """Wide enough for two tiles of W2 a CTA, also where their number is odd, with a heavy shared expert."""
+    layer = Layer(dev, 6, K, I, S)
+    for T in (2, 16):
+        x, ids, p = inputs(dev, T, K, 6, 2, T)
+        layer.check(layer.call(x, ids, p), x, ids, p)
