@@ -746,7 +746,7 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
         E, I, kr = ws[0], ws[1] // 2, ids[1]
         S = 0 if b13 is None else b13.shape[0] // 2
         device = x.get_device()
-        if K % 128 or I % 128 or S % 128 or (T > 1 and x.stride(1) != 1):
+        if K % 128 or I % 128 or S % 128 or x.stride(1) != 1:
             fine = False
         elif sfb13 is not None:                      # E4M3: bytes, one row of scale words per 512 of the inner width
             wk, wi = (K + 511) // 512, (I + 511) // 512
@@ -770,9 +770,9 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
             _few_weights(b2, f2, None, K, S, kind, "shared w2")
             fine = all(t is None or t.get_device() == device for t in (b13, f13, b2, f2))
         if fine and z is not None:
-            fine = z.dtype is _BF16 and z.shape == xs and (T == 1 or z.stride(1) == 1) and z.get_device() == device
+            fine = z.dtype is _BF16 and z.shape == xs and z.stride(1) == 1 and z.get_device() == device
         if fine and addend is not None:
-            fine = (addend.dtype is _BF16 and addend.shape == xs and (T == 1 or addend.stride(1) == 1)
+            fine = (addend.dtype is _BF16 and addend.shape == xs and addend.stride(1) == 1
                     and addend.get_device() == device)
         if fine and workspace is not None:
             fine = (workspace.dtype is _U8 and workspace.dim() == 1 and workspace.is_contiguous()
@@ -808,7 +808,7 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, out_dtype=
     """act(x w^T + bias) + residual: x [T, K] and w [N, K] both bf16 or both fp16 (row strides multiples of 8) -> out
     [T, N] of ``out_dtype`` float32, bf16 or fp16 (default: that of ``out``, else x's).  ``bias`` [N] of any of the
     three types, ``activation`` None, "relu", "silu", "gelu", "gelu_tanh" or "sigmoid", ``residual`` [T, N] of the
-    output's type (it may be ``out``).  One rounding, of the float32 result."""
+    output's type (it may be ``out``, which may not overlap x or w).  One rounding, of the float32 result."""
     T, K = _two_dims(x, "x")
     N, Kw = _two_dims(w, "w")
     kind = x.dtype

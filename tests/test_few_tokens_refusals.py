@@ -201,6 +201,19 @@ def test_few_token_moe_refuses_other_operands(library, other):
         moe(moe_operands(**other))
 
 
+@pytest.mark.parametrize("name", ["x", "z", "addend"])
+def test_few_token_moe_refuses_a_single_row_whose_values_are_apart(library, name):
+    one = dict(x=Tensor(1, 256, dtype=BF16), topk_ids=Tensor(1, 2, dtype=I32), topk_weights=Tensor(1, 2, dtype=F32),
+               addend=Tensor(1, 256, dtype=BF16), z=Tensor(1, 256, dtype=BF16))
+    with pytest.raises(Reached):
+        moe(moe_operands(**one))
+    for stride in ((512, 2), (0, 0), (1, 1024)):
+        with pytest.raises(ValueError, match=name):
+            moe(moe_operands(**{**one, name: Tensor(1, 256, dtype=BF16, stride=stride)}))
+    with pytest.raises(Reached):                     # (the stride between rows of a single row is not looked at)
+        moe(moe_operands(**{**one, name: Tensor(1, 256, dtype=BF16, stride=(3, 1))}))
+
+
 def test_few_token_moe_refuses_scales_of_bf16_weights_and_odd_sizes(library):
     with pytest.raises(ValueError, match="no scale words"):
         moe(moe_operands(BF16, sfb2=Tensor(8, 1, 256, dtype=I32)))
