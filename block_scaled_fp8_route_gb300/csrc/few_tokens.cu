@@ -11,19 +11,28 @@
 // Such a layer is bound by the chosen experts' weights, which are read once; everything else has to hide
 // behind that stream.
 // * Work is cut into units of K-blocks, not of experts: every CTA takes the same number of boxes (128
-//   weight rows x 128 bytes, 16 KB, a contiguous run of tiled weights) whatever the routing is.  Each CTA derives
-//   routing, units and places from topk_ids itself.
+//   weight rows x 128 bytes, 16 KB, a contiguous run of tiled weights) whatever the routing is, fewer where an expert has
+//   more than 8 tokens, whose operand then takes longer than its weights.  Each CTA derives routing, units and places
+//   from topk_ids itself.
 // * The first kernel multiplies gate and up rows of one 128-wide tile by the expert's tokens.  A tile whose
 //   K is shared by two or more CTAs leaves that many partial sums; nobody waits for anybody, because
 //   the second kernel adds them (in a fixed order) while it forms h.
-// * The second kernel, a programmatic dependent, is resident beside the first (half the shared memory each) and has
-//   its first weights in flight before the first one ends.  Contraction runs over (expert, i), so a cluster
+// * The second kernel, a programmatic dependent, takes whole SMs with up to five stages as the first one's CTAs leave
+//   them, does its routing and starts its loads before it waits for the partial sums.  (Half the shared memory for each
+//   kernel, so that both are resident and the weights are under way sooner, is no faster with one token and slower with
+//   a batch, whose second product then has too little in flight.)  Contraction runs over (expert, i), so a cluster
 //   splits one long K and its CTAs exchange one partial of z through distributed shared memory, in rank order.
 // * FP8 weights meet unquantised activations on the FP8 tensor cores: a value scaled to its block of 128 is split
 //   into E4M3 terms, v = hi + lo / 16, which take two columns of the MMA.  A bf16 value has 8 significant bits and
 //   each term holds 4, so the split is exact down to 2**-14 of the block's largest value and off by at most
 //   2**-21 of that below; a float32 h is off by at most 2**-9 of its size or 2**-21 of the block's largest.  The weights
 //   go from HBM to the tensor core without passing a register.
+//
+// Measured with FP8 weights.  128 experts of which a token chooses 8, K 4096, I 1536: 32 tokens read the 2.11 GB of 111
+// experts in 298 us, 7.1 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236 us, 7.2 TB/s; both are
+// bound by HBM.  One token of the first layer reads 152 MB in 34 us: its first kernel streams at 7.7 TB/s, and some 6 us
+// are the exit, launch and routing between the two kernels, the first operand, and the exchange at the end.
+// Multiplying less gains next to nothing there (3 of 4 MMAs left out: 1 us).
 #include <algorithm>
 #include <cfloat>
 
@@ -47,7 +56,8 @@ constexpr int kParts = 4;                      // most CTAs that share a tile of
 // warps: 0 and 3 weight loads, 1 and 2 MMA issuers (one per box each), 4-7 and 8-11 as each kernel needs them
 constexpr int kThreads = 384;
 constexpr int kBarBytes = 512;                // barriers, tensor memory's place, abort flag, 32 words of groups, a maximum
-constexpr int kSmem = 113 * 1024;              // first kernel: 3 stages; with more in flight the SMs share HBM less evenly
+constexpr int kStages1 = 3;                    // first kernel; with more in flight the SMs share HBM less evenly
+constexpr int kUnitTokens = 8;                 // FP8: tokens whose operand the first kernel forms in the time of a load
 constexpr int kMostSmem = 227 * 1024;
 constexpr int kMaxSplit = 16;
 
@@ -154,10 +164,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* groups_of = tmem_slot + 2;                                          // per 32 experts: chosen ones, rows << 16
+  uint32_t* groups_of = tmem_slot + 2;              // per 32 experts: chosen ones, further costs << 8, rows << 16
   int* most_tokens = reinterpret_cast<int*>(groups_of + 32);                    // of any chosen expert
   uint8_t* scales = smem_raw + kBarBytes;                                       // [stages][kSfBytes]
-  uint2* chosen = reinterpret_cast<uint2*>(scales + kMaxStages * kSfBytes);     // tokens (bits); expert, first row << 16
+  // of each chosen expert: its tokens (bits); expert, first row << 10, further costs of those before it << 21
+  uint2* chosen = reinterpret_cast<uint2*>(scales + kMaxStages * kSfBytes);
   float* share = reinterpret_cast<float*>(chosen + min(p.E, p.R) + 1);          // [R] p of each row
   uint8_t* token = reinterpret_cast<uint8_t*>(share + p.R);                     // [R] token of each row
   uint8_t* smem = smem_raw + p.tables;                                          // stages: two boxes and the token operand
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(done, boxes);
     *abort_flag = 0;
-    *most_tokens = PHASE == 1 && p.S == 0 ? 1 : p.T;         // (the shared expert and the second kernel take all)
+    *most_tokens = p.S == 0 ? 1 : p.T;     // (all take the shared expert)
     fence_barrier_init();
     tma_prefetch_desc(&map_routed);
     if (p.S) tma_prefetch_desc(&map_shared);
@@ -191,6 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int e = tid; e < p.E; e += kThreads) reinterpret_cast<uint32_t*>(smem)[e] = 0u;      // (the masks below)
   if (PHASE == 1) pdl_wait();
   pdl_launch_dependents();
+
+  // What a K-block of the first product costs with n tokens.  Forming an FP8 operand (two terms of each value, a
+  // maximum of each block) takes longer than loading its weights beyond 8 tokens: 32 tokens of which all choose one
+  // of 64 experts (K 4096, I 1536) take 435 us in CTAs of equal K-blocks and 210 in these, with a shared expert of 1536
+  // 435 and 203; the 435 with two stages for such operands, too.  bf16 values are copied (343 either way).  At most
+  // 113 further costs in all (9 tokens each of 1024 assignments).
+  auto cost = [](uint32_t n) -> uint32_t { return FMT == kFp8 ? (n + kUnitTokens - 1) / kUnitTokens : 1u; };
 
   // ---------------------------------------------------------------- routing, in every CTA
   // The stages, not yet in use, hold the tables: tokens and first row of every expert, ids and weights.
@@ -214,32 +232,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int groups = (p.E + 31) >> 5;
     for (int g = warp; g < groups; g += kThreads / 32) {
       const uint32_t m = g * 32 + lane < p.E ? mask[g * 32 + lane] : 0u;
-      const int n = __reduce_add_sync(0xffffffffu, __popc(m));
-      const int most = PHASE == 1 ? static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(__popc(m)))) : 1;
-      const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
-      if (PHASE == 1 && lane == 0) atomicMax(most_tokens, most);
-      if (lane == 0) groups_of[g] = static_cast<uint32_t>(__popc(some)) | static_cast<uint32_t>(n) << 16;
+      const uint32_t n = __popc(m);
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, n << 16 | (n ? (cost(n) - 1) << 8 | 1u : 0u));
+      const uint32_t most = __reduce_max_sync(0xffffffffu, n);
+      if (lane == 0) {
+        if (PHASE == 1 || (sum & 0xFF00u)) atomicMax(most_tokens, static_cast<int>(most));
+        groups_of[g] = sum;
+      }
     }
     __syncthreads();
     for (int g = warp; g < groups; g += kThreads / 32) {
       const int e = g * 32 + lane;
       const uint32_t m = e < p.E ? mask[e] : 0u;
       const uint32_t some = __ballot_sync(0xffffffffu, m != 0u);
-      int rows = __popc(m);
+      const uint32_t mine = m ? static_cast<uint32_t>(__popc(m)) << 16 | (cost(__popc(m)) - 1) << 8 : 0u;
+      uint32_t before = mine;                // rows << 16, further costs << 8, chosen experts
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int below = __shfl_up_sync(0xffffffffu, rows, o);
-        if (lane >= o) rows += below;
+        const uint32_t below = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += below;
       }
-      rows -= __popc(m);
-      int at = __popc(some & ((1u << lane) - 1u));
+      before += __popc(some & ((1u << lane) - 1u)) - mine;
+      uint32_t at = before & 0xFFu, further = before >> 8 & 0xFFu, rows = before >> 16;
       for (int k = 0; k < g; ++k) {
-        rows += static_cast<int>(groups_of[k] >> 16);
-        at += static_cast<int>(groups_of[k] & 0xFFFFu);
+        at += groups_of[k] & 0xFFu;
+        further += groups_of[k] >> 8 & 0xFFu;
+        rows += groups_of[k] >> 16;
       }
       if (m) {
-        chosen[at] = make_uint2(m, static_cast<uint32_t>(e) | static_cast<uint32_t>(rows) << 16);
-        first[e] = rows;
+        chosen[at] = make_uint2(m, static_cast<uint32_t>(e) | rows << 10 | further << 21);
+        first[e] = static_cast<int>(rows);
       }
     }
     __syncthreads();
@@ -262,10 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  int nchosen = 0;
-  for (int g = 0; g < (p.E + 31) >> 5; ++g) nchosen += static_cast<int>(groups_of[g] & 0xFFFFu);
+  int nchosen = 0, further = 0;
+  for (int g = 0; g < (p.E + 31) >> 5; ++g) {
+    nchosen += static_cast<int>(groups_of[g] & 0xFFu);
+    further += static_cast<int>(groups_of[g] >> 8 & 0xFFu);
+  }
   const uint32_t everyone = p.T == 32 ? 0xffffffffu : (1u << p.T) - 1u;
-  if (tid == 0) chosen[nchosen] = make_uint2(everyone, 0u);
+  if (tid == 0) chosen[nchosen] = make_uint2(everyone, static_cast<uint32_t>(further) << 21);
   if (FMT == kFp8)                         // every row has a scale, whether or not it has values
     for (int i = tid; i < kMaxStages * kSfBytes / 4; i += kThreads) reinterpret_cast<uint32_t*>(scales)[i] = 0x7F7F7F7Fu;
   proxy_fence();                           // the tables' place is written by TMA next
@@ -277,12 +302,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int routed = PHASE == 1 ? nchosen * tiles * p.nkb1 : nchosen * p.nkb2;
     const int units = routed + (PHASE == 1 ? (p.S >> 7) * p.nkb1 : p.nkb2_shared);
-    const int units1 = PHASE == 1 ? units : (nchosen * tiles + (p.S >> 7)) * p.nkb1;
-    // (at least a third of a tile's K, so that at most kParts CTAs share one)
-    per = max((units1 + p.ctas1 - 1) / p.ctas1, (p.nkb1 + 2) / 3);
+    const int whole = tiles * p.nkb1;      // K-blocks of an expert
+    const int all = (nchosen + further) * whole + (p.S >> 7) * p.nkb1 * static_cast<int>(cost(p.T));   // costs
+    // (at least a third of a tile's, so that at most kParts CTAs share one)
+    per = max((all + p.ctas1 - 1) / p.ctas1, static_cast<int>(cost(*most_tokens)) * ((p.nkb1 + 2) / 3));
     if (PHASE == 1) {
-      u0 = min(units, static_cast<int>(blockIdx.x) * per);
-      u1 = min(units, u0 + per);
+      // a CTA takes the K-blocks that begin within its `per` costs
+      auto cut = [&](int cta) {
+        const int at = cta * per;
+        if (at >= all) return units;
+        int a = min(at / whole, nchosen);
+        if (further) {                     // the last expert that begins at or before it
+          a = 0;
+          for (int hi = nchosen; a < hi;) {
+            const int mid = (a + hi + 1) >> 1;
+            if ((mid + static_cast<int>(chosen[mid].y >> 21)) * whole <= at) a = mid;
+            else hi = mid - 1;
+          }
+        }
+        const int c = static_cast<int>(cost(__popc(chosen[a].x)));
+        return a * whole + (at - (a + static_cast<int>(chosen[a].y >> 21)) * whole + c - 1) / c;
+      };
+      if (all == units) {                  // (one cost each: found without the search, 0.6 us of one token's 33)
+        u0 = min(units, static_cast<int>(blockIdx.x) * per);
+        u1 = min(units, u0 + per);
+      } else {
+        u0 = u1 = 0;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          u0 = u1;
+          u1 = cut(blockIdx.x + k);
+        }
+      }
     } else {
       // a share of the routed experts' and one of the shared expert's, whose operand takes longer to form
       first_routed = static_cast<int>(static_cast<int64_t>(routed) * rank / p.split);
@@ -292,6 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       u1 = mine_routed + p.nkb2_shared * (rank + 1) / p.split - first_shared;
     }
   }
+  // the costs before a tile, and those of its K-blocks: CTA c of the first kernel has those of c * per and above
+  auto costs_before = [&](int a, int j) {
+    return ((a + static_cast<int>(chosen[a].y >> 21)) * tiles + j * static_cast<int>(cost(__popc(chosen[a].x)))) * p.nkb1;
+  };
   auto unit_at = [&](int u) {
     Unit w;
     if (PHASE == 1) {
@@ -318,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto padded = [&](int n) { return kTerms == 2 ? (n + 7) & ~7 : (n + 15) & ~15; };
   // Stages as large as the most tokens of an expert need: 32 tokens seldom put more than 8 on one, and a larger operand
   // would cost a stage of weights in flight.
-  const int most_rows = kTerms * padded(*most_tokens);
+  const int most_rows = kTerms * padded(PHASE == 1 ? *most_tokens : p.T);
   const int stage_bytes = 2 * kBoxBytes + ((most_rows * 128 + 1023) & ~1023);
-  const int stages = min(p.stage_space / stage_bytes, PHASE == 1 ? 4 : kMaxStages);      // (at most kConvWarps)
+  const int stages = min(p.stage_space / stage_bytes, PHASE == 1 ? kStages1 : kMaxStages);      // (at most kConvWarps)
   const int acc_stride = (most_rows + 31) & ~31;                   // columns of a sum
   const uint32_t sets = kAccCol + 4 * acc_stride <= static_cast<int>(p.tmem_cols) ? 2u : 1u;   // of sums, first kernel
 
@@ -362,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit w = unit_at(u);
         const bool shared = w.a == nchosen;
         const CUtensorMap* map = shared ? &map_shared : &map_routed;
-        const int e = shared ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
+        const int e = shared ? 0 : static_cast<int>(chosen[w.a].y & 0x3FFu);
         const int width = shared ? p.S : p.I;                            // of h
         const int row = PHASE == 1 ? (2 * e + b) * width + w.j * 128 : e * p.K + (cluster * p.nbox + b) * 128;
         const int nkb = PHASE == 1 ? p.nkb1 : shared ? p.nkb2_shared : p.nkb2;
@@ -441,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_quiet(done, 0);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 4 + kConvWarps) {
+  } else if (warp < 4 + kConvWarps) {
     // ------------------------------------------------------------ token operands and scales
     // One warp per K-block: what forms an operand is a chain of latencies (values, a maximum, codes, fences) several
     // times as long as a unit's share of HBM, so as many of them as there are warps are under way at once.
@@ -452,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto scale_word = [&](const Unit& w, int b) -> uint32_t {
       if (FMT != kFp8 || b >= boxes) return 0x7F7F7F7Fu;
       const bool sh = w.a == nchosen;
-      const int width = sh ? p.S : p.I, e = sh ? 0 : static_cast<int>(chosen[w.a].y & 0xFFFFu);
+      const int width = sh ? p.S : p.I, e = sh ? 0 : static_cast<int>(chosen[w.a].y & 0x3FFu);
       const int rows = PHASE == 1 ? 2 * width : p.K, inner = PHASE == 1 ? p.K : width;
       const int row = PHASE == 1 ? b * width + w.j * 128 : (cluster * p.nbox + b) * 128;
       const int64_t at = (static_cast<int64_t>(e) * ((inner + 511) >> 9) + (w.kb0 >> 2)) * rows + row;
@@ -522,11 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PHASE == 1) {
       // x: the loads of up to kBatch rounds are in flight at once, and while the warp waits for its stage
       constexpr int kBatch = 4;
+      constexpr int kStep = kBatch * kAtOnce;
       for (int i = cw; u0 + i < u1; i += kConvWarps) {
         const Unit w = unit_at(u0 + i);
         const uint2 who = chosen[w.a];
         const int n = __popc(who.x), stage = i % stages, rows = padded(n);
-        const uint8_t* list = token + (who.y >> 16);
+        const uint8_t* list = token + (who.y >> 10 & 0x7FFu);
         const bool sh = w.a == nchosen;
         const uint32_t word0 = scale_word(w, 0), word1 = scale_word(w, 1);
         const uint16_t* from = p.x + w.kb0 * (kLanes * 8) + sub * 8;
@@ -542,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         load(0);
-        for (int j0 = 0; j0 < n && ok; j0 += kBatch * kAtOnce) {
+        for (int j0 = 0; j0 < n; j0 += kStep) {
           // A batch's terms side by side, and the next one's loads, before the stage is waited for: a stage held up holds
           // up its own next loads.
           auto term = [&](int k) {
@@ -557,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 1; k < kBatch; ++k) r[k] = term(k);
           }
-          if (n - j0 > kBatch * kAtOnce) load(j0 + kBatch * kAtOnce);
+          if (n - j0 > kStep) load(j0 + kStep);
           if (j0 == 0) ok = wait_stage(i);
           if (!ok) break;
 #pragma unroll
@@ -594,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t part_step = static_cast<int64_t>(sh ? p.T : p.R) * 2 * width;
         const int at = w.kb0 * (kLanes * 8) + sub * 8;                   // of h
         const int item = w.a * tiles + (at >> 7);
-        const int parts = ((item + 1) * p.nkb1 - 1) / per - item * p.nkb1 / per + 1;
+        const int costs = costs_before(w.a, item - w.a * tiles), more = (p.nkb1 - 1) * static_cast<int>(cost(n));
+        const int parts = (costs + more) / per - costs / per + 1;
         bool ok = true;
         const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
         const float* base = (sh ? p.part_shared : p.part) + at;
@@ -607,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j = j0 + k * kAtOnce + mine;
             row[k] = -1, t[k] = 0, weight[k] = 1.f;
             if (j < n) {
-              row[k] = sh ? j : static_cast<int>(who.y >> 16) + j;
+              row[k] = sh ? j : static_cast<int>(who.y >> 10 & 0x7FFu) + j;
               t[k] = sh ? j : token[row[k]];
               if (!sh) weight[k] = share[row[k]];
             }
@@ -667,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish(stage);
       }
     }
-  } else if (PHASE == 1 && warp >= 8) {
+  } else if (PHASE == 1) {
     // ------------------------------------------------------------ first kernel's sums: lane = row of the tile
     const int q = warp & 3;
     const uint32_t tmem_base = *tmem_at;
@@ -679,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint2 who = chosen[w.a];
       const int n = __popc(who.x), rows = padded(n);
       const int width = sh ? p.S : p.I;
-      const int part = static_cast<int>(blockIdx.x) - (w.a * tiles + w.j) * p.nkb1 / per;
-      const int64_t row0 = static_cast<int64_t>(part) * (sh ? p.T : p.R) + (who.y >> 16);
+      const int part = static_cast<int>(blockIdx.x) - costs_before(w.a, w.j) / per;
+      const int64_t row0 = static_cast<int64_t>(part) * (sh ? p.T : p.R) + (who.y >> 10 & 0x7FFu);
       float* to = (sh ? p.part_shared : p.part) + row0 * 2 * width + w.j * 128 + 32 * q + lane;
       ok = ok && wait_all(&acc_full[set], set_phase, abort_flag, p.err);
       tc_fence_after();
@@ -860,7 +917,7 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   const int tables = kBarBytes + kMaxStages * kSfBytes + ((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5;
   a.tables = (tables + 1023) / 1024 * 1024;
 
-  a.stage_space = kSmem - a.tables;
+  a.stage_space = kStages1 * (2 * kBoxBytes + ((FMT == kFp8 ? rows : (a.T + 15) / 16 * 16) * 128 + 1023) / 1024 * 1024);
   const int space2 = kMostSmem - a.tables;
 
   // The second kernel: a CTA takes two 128-row tiles of W2, for which the token operand is formed once (one where K is

@@ -287,3 +287,30 @@ def test_second_products_in_pairs_of_tiles(dev, K, I, S):
     for T in (2, 16):
         x, ids, p = inputs(dev, T, K, 6, 2, T)
         layer.check(layer.call(x, ids, p), x, ids, p)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("T", [9, 17, 25, 32])
+def test_a_heavy_expert_among_light_ones(dev, fmt, T):
+    """Experts of 9 tokens and more cost the first kernel more than one unit: one that all choose, first, in the middle or
+    last, some of about half the tokens, and a shared one."""
+    for heavy, S in ((0, 0), (9, 256), (19, 128)):
+        layer = Layer(dev, 20, 640, 256, S, fmt=fmt, seed=heavy)
+        x, ids, p = inputs(dev, T, 640, 20, 3, seed=T + heavy)
+        ids[:, 1] = heavy
+        ids[:T // 2 + 1, 2] = (heavy + 7) % 20
+        layer.check(layer.call(x, ids, p), x, ids, p)
+
+
+def test_many_heavy_experts(dev):
+    """1024 assignments in groups of nine tokens an expert, as many costs beyond one as there can be, on 1024 experts."""
+    layer = Layer(dev, 1024, 128, 128, seed=3)
+    x, ids, p = inputs(dev, 32, 128, 1024, 32, 3)
+    free = [0] * 32
+    for e in range(113):
+        order = sorted(range(32), key=lambda t: (free[t], t))[:9]
+        for t in order:
+            if free[t] < 32:
+                ids[t, free[t]] = 9 * e + 3
+                free[t] += 1
+    layer.check(layer.call(x, ids, p), x, ids, p)
