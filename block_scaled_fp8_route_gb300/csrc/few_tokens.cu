@@ -29,7 +29,7 @@
 //   go from HBM to the tensor core without passing a register.
 //
 // Measured with FP8 weights.  128 experts of which a token chooses 8, K 4096, I 1536: 32 tokens read the 2.11 GB of 111
-// experts in 298 us, 7.1 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236 us, 7.2 TB/s; both are
+// experts in 298-302 us, 7.0 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236-239 us, 7.1 TB/s; both are
 // bound by HBM.  One token of the first layer reads 152 MB in 34 us: its first kernel streams at 7.7 TB/s, and some 6 us
 // are the exit, launch and routing between the two kernels, the first operand, and the exchange at the end.
 // Multiplying less gains next to nothing there (3 of 4 MMAs left out: 1 us).
