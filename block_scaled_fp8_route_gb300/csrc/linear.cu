@@ -484,18 +484,28 @@ __device__ __forceinline__ void fetch(const Epilogue& e, uint32_t (&w)[32], int6
   }
   const int odd = n & 1;
   const uint16_t* from = static_cast<const uint16_t*>(e.residual) + row * e.ldr + (n & ~1);
+  if (rows >= 32) {
+    from += odd * e.ldr;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, from += 2 * e.ldr) w[j] = *reinterpret_cast<const uint32_t*>(from);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 16; ++j) w[j] = *reinterpret_cast<const uint32_t*>(from + min(2 * j + odd, rows - 1) * e.ldr);
 }
 
-// 32 tokens of one weight row per lane -> y.  Two neighbouring lanes exchange halves, so that a lane holds two
-// neighbouring rows of one token (16-bit types).
+// 32 tokens of one weight row per lane -> y.  With 16-bit types two tokens are packed in a word and neighbouring lanes
+// exchange words, so that a lane holds two neighbouring rows of one token (one exchange and one byte permutation for two
+// values; the residual's words go the other way).  The epilogue's warps are few, two a scheduler, so their instructions
+// count: full chunks have no predicates, and rows are stepped through, not multiplied out.
 template <int OUT, bool kResidual>
 __device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], const uint32_t (&w)[32], float bias, int64_t row,
                                        int rows, int n, int N) {
   const int odd = n & 1;
+  if (e.bias) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] += bias;
+    for (int j = 0; j < 32; ++j) v[j] += bias;
+  }
   activate(v, e.act);
   if (OUT == BSF_TYPE_F32 || !e.wide) {
     if (n >= N) return;
@@ -503,26 +513,49 @@ __device__ __forceinline__ void finish(const Epilogue& e, float (&v)[32], const 
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] += OUT == BSF_TYPE_F32 ? __uint_as_float(w[j]) : unpack2<OUT>(w[j]).x;
     }
+    Epilogue at = e;
+    if (OUT == BSF_TYPE_F32) at.y = static_cast<float*>(e.y) + row * e.ldy + n;
+    else at.y = static_cast<uint16_t*>(e.y) + row * e.ldy + n;
+    if (rows >= 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        store_at<OUT>(at, 0, v[j]);
+        if (OUT == BSF_TYPE_F32) at.y = static_cast<float*>(at.y) + e.ldy;
+        else at.y = static_cast<uint16_t*>(at.y) + e.ldy;
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (j < rows) store_at<OUT>(e, (row + j) * e.ldy + n, v[j]);
+      if (j < rows) store_at<OUT>(at, j * e.ldy, v[j]);
     return;
   }
   // (N is even, so both rows of a word exist or neither does)
-  uint16_t* to = static_cast<uint16_t*>(e.y) + (row + odd) * e.ldy + (n & ~1);
+  const uint32_t pick = odd ? 0x3276u : 0x5410u;
+  uint32_t u[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     float v0 = v[2 * j], v1 = v[2 * j + 1];
-    const float x = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-    v0 = odd ? x : v0;
-    v1 = odd ? v1 : x;
     if (kResidual) {
-      const float2 r = unpack2<OUT>(w[j]);
+      const float2 r = unpack2<OUT>(__byte_perm(w[j], __shfl_xor_sync(0xffffffffu, w[j], 1), pick));
       v0 += r.x;
       v1 += r.y;
     }
-    if (2 * j + odd < rows && n < N) *reinterpret_cast<uint32_t*>(to + 2 * j * e.ldy) = pack2<OUT>(v0, v1);
+    u[j] = pack2<OUT>(v0, v1);
   }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) u[j] = __byte_perm(u[j], __shfl_xor_sync(0xffffffffu, u[j], 1), pick);
+  if (n >= N) return;
+  uint16_t* to = static_cast<uint16_t*>(e.y) + (row + odd) * e.ldy + (n & ~1);
+  const int64_t step = 2 * e.ldy;
+  if (rows >= 32) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j, to += step) *reinterpret_cast<uint32_t*>(to) = u[j];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j, to += step)
+    if (2 * j + odd < rows) *reinterpret_cast<uint32_t*>(to) = u[j];
 }
 
 template <int OUT, int kIssuers, bool kResidual>
