@@ -17,9 +17,10 @@
 // * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 256 tokens with one cta_group::2 MMA per 16 K;
 //   two accumulators let a tile's epilogue run under the next tile's MMAs.  What an SM takes in from L2, 53 bytes a cycle
 //   (the same from its own loads and by multicast), binds these tiles: 256 x 256 x 64 brings each SM 32 KB, 610
-//   cycles of loads for 512 of MMAs.  8192 x 7168 x 4096 with bias and residual takes 275-285 us in short runs, 1.69-1.75
-//   PFLOP/s, 89-92 % of the measured burst, and 290-320 where the power cap holds; 8192 x 256 x 7168 (tiles of 112 tokens in
-//   one round of CTAs) 32 us, 939 TFLOP/s; 777 x 4100 x 1416 with gelu 18.6 us, a quarter of it the epilogue.
+//   cycles of loads for 512 of MMAs.  8192 x 7168 x 4096 with bias and residual takes 266-275 us in short runs, 1.75-1.81
+//   PFLOP/s, 92-95 % of the measured burst, and 300-330 where the power cap holds; 8192 x 256 x 7168 (tiles of 112 tokens in
+//   one round of CTAs) 30.5 us, 986 TFLOP/s; 777 x 4100 x 1416 with gelu 16.0-16.5 us.  With few K-blocks a tile is bound by
+//   its epilogue: 8192 x 2048 x 512 21 us, with a residual, whose loads two warps a scheduler do not hide, 31.
 #include "cluster.cuh"
 #include "common.cuh"
 #include "host_utils.h"
@@ -909,10 +910,9 @@ bool runs_fit(int64_t nkb, int split, int64_t per, bool f32) {
 
 // Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 2200 products
 // of 1 .. 8192 tokens, 16 .. 8192 weight rows and K of 64 .. 8192, drawn by their logarithms, with weights that come from
-// HBM, each timed in every form that could win (26000 in all).  The choice is 1.0 % above the best form on average, at
-// worst 25 % (141 x 5097 x 64: split 6.1 us, in pairs 4.9); with K over 1, 2, 4 or 8 CTAs alone it would be 3.0 %.
-// Both sides: 256 x 4096 x 4096 takes 17.3 us split and 18.5 in pairs, 1024 x 256 x 7168 11.3 and 21, 777 x 4100 x 1416
-// 34 and 15.7.
+// HBM, each timed in every form that could win (25000 in all).  On 1500 others the choice is 1.0 % above the best
+// form on average, at worst 18 %.  Both sides: 64 x 4096 x 4096 takes 12.2 us split and 14.7 in pairs, 256 x 4096 x 4096
+// 16.6 and 14.3, 1024 x 256 x 7168 10.9 and 21.0, 777 x 4100 x 1416 33.5 and 13.0.
 struct Plan {
   bool pair;
   int tok;                  // pairs: tokens per tile; split: most tokens per tile
@@ -920,7 +920,7 @@ struct Plan {
 };
 Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const LinearLimits& limits) {
   const int64_t nkb = (K + kBlockK - 1) / kBlockK, ntn = (N + kTileW - 1) / kTileW, sms = sm_count(), pairs = sms / 2;
-  const double read = 2.0 * K * (M + N) / 6767;        // of both operands from HBM
+  const double read = 2.0 * K * (M + N) / 8895;        // of both operands from HBM
   Plan best = {false, 64, 1};
   double least = 1e300;
   for (int tok = 64; tok <= kMaxTok; tok += 64) {
@@ -932,11 +932,11 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const
       if (!runs_fit(nkb, split, per, f32)) continue;                  // (pairs add runs of any number)
       const int64_t at_once = limits.ctas[split].load(std::memory_order_relaxed);
       const int64_t load = (ctas + at_once - 1) / at_once;            // CTAs of the busiest SM
-      const double once = (residual ? 97.5 : 87.6) * per / sqrt(double(split)) + (split > 1 ? 547 + 52.6 * split : 0);
+      const double once = (residual ? 88.4 : 76.4) * per / sqrt(double(split)) + (split > 1 ? 734 + 138 * split : 0);
       // tiles of more than 64 tokens have an SM to themselves, others share one two at a time
-      const double busy = per > 64 ? load * (once + kbs * (209 + 0.43 * per))
-                                   : load / 2 * (once + 691.0 * kbs) + load % 2 * (once + 282.0 * kbs);
-      const double ns = 2638 + (busy > read ? busy : read);
+      const double busy = per > 64 ? load * (once + 270.0 * kbs)
+                                   : load / 2 * (once + 730.0 * kbs) + load % 2 * (once + 293.0 * kbs);
+      const double ns = 1498 + (busy > read ? busy : read);
       if (ns < least) {
         least = ns;
         best = {false, tok, split};
@@ -946,10 +946,10 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const
   for (int tok = f32 ? kMaxTok : kPairMaxTok; tok >= 64; tok -= 16) {      // (float32 sums live in registers)
     const int64_t tiles = (M + tok - 1) / tok * ((ntn + 1) / 2), waves = (tiles + pairs - 1) / pairs;
     // a K-block: what an SM takes from L2, 53 bytes a cycle, binds every tile (wide ones nearly the tensor cores, too)
-    const double loop = tok <= kMaxTok ? (nkb + 1) / 2 * 2 * (140 + 1.27 * tok) : 380.0 * nkb;
-    const double store = tok * (8.65 + (f32 ? 3.15 : 0) + (residual ? 2.83 : 0));
-    const double busy = waves * (loop > 2299 + store ? loop : 2299 + store);
-    const double ns = 3930 + (busy > read ? busy : read) + store;
+    const double loop = tok <= kMaxTok ? (nkb + 1) / 2 * 2 * (152 + 0.682 * tok) : 290.0 * nkb;
+    const double store = tok * (2.53 + (f32 ? 4.8 : 0) + (residual ? 4.17 : 0));
+    const double busy = waves * (loop > 891 + store ? loop : 891 + store);
+    const double ns = 3301 + (busy > read ? busy : read) + store;
     if (ns < least) {
       least = ns;
       best = {true, tok, 1};
