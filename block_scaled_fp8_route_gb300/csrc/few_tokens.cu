@@ -114,6 +114,9 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem_addr) 
   d |= static_cast<uint64_t>(1u) << 46;                             // descriptor version (tcgen05)
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
+__device__ __forceinline__ void arrive_with(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Eight values f * scale -> E4M3 codes of their leading four bits and of 16 times what is left (exact in float32).
@@ -178,11 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = PHASE == 2 ? static_cast<int>(blockIdx.x) - cluster * p.split : 0;
   const int boxes = PHASE == 1 ? 2 : min(p.nbox, p.K / 128 - cluster * p.nbox);
   constexpr int kConvWarps = PHASE == 1 ? 4 : 8;
+  constexpr int kShares = PHASE == 1 ? 1 : kConvWarps;       // of forming an operand
   constexpr int kTerms = FMT == kFp8 || PHASE == 2 ? 2 : 1;
 
   if (tid == 0) {
     for (int s = 0; s < 2 * kMaxStages; ++s) {
-      mbar_init(&full[s], 2);              // its load, and the warp that formed the operand
+      mbar_init(&full[s], 1 + kShares);    // its load, and all shares of the operand's forming
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kConvWarps; ++s) mbar_init(&formed[s], boxes);
@@ -379,6 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int acc_stride = (most_rows + 31) & ~31;                   // columns of a sum
   const uint32_t sets = kAccCol + 4 * acc_stride <= static_cast<int>(p.tmem_cols) ? 2u : 1u;   // of sums, first kernel
 
+  // A CTA of the second kernel with at most half as many K-blocks as warps (and fewer than stages, so that none is used
+  // twice) has several warps form each of them, some tokens each: 10 tokens that all choose 4 experts, K and I 384, 16.2 ->
+  // 13.0 us, 32 tokens x 2 of 8 experts, K 2048, I 512, 25.1 -> 23.6.  What a warp's arrival counts makes up for it.
+  const int helpers = PHASE == 1 || u1 - u0 > 4 ? 1 : u1 - u0 > 2 ? 2 : u1 - u0 > 1 ? 4 : 8;
+
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto publish = [&](int stage) {
       proxy_fence();
       __syncwarp();
-      if (lane < boxes) mbar_arrive(&full[2 * stage + lane]);
+      if (lane < boxes) arrive_with(&full[2 * stage + lane], kShares / helpers);
     };
 
     if (PHASE == 1) {
@@ -630,15 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that did not choose the expert get zeros
       Unit w = {};
       uint32_t word0 = 0, word1 = 0;
-      if (u0 + cw < u1) {                  // (there may be no K-block at all, nor scales)
-        w = unit_at(u0 + cw);
+      const int first = cw / helpers, helper = cw - first * helpers;
+      if (u0 + first < u1) {               // (there may be no K-block at all, nor scales)
+        w = unit_at(u0 + first);
         word0 = scale_word(w, 0);
         word1 = scale_word(w, 1);
       }
       pdl_wait();
       const int rows = padded(p.T);
-      for (int i = cw; u0 + i < u1; i += kConvWarps) {
-        if (i != cw) {
+      for (int i = first; u0 + i < u1; i += kConvWarps) {
+        if (i != first) {
           w = unit_at(u0 + i);
           word0 = scale_word(w, 0);
           word1 = scale_word(w, 1);
@@ -656,21 +666,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e0 = exponent(word0, w.kb0), e1 = exponent(word1, w.kb0);
         const float* base = (sh ? p.part_shared : p.part) + at;
         constexpr int kRounds = 2;           // of tokens whose loads are in flight together, two parts of each
-        for (int j0 = 0; j0 < n && ok; j0 += kRounds * kAtOnce) {
+        // tokens that did not choose the expert, when the stage is free
+        auto zeros = [&]() {
+          uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
+          for (int z = 4 * helper + (lane >> 3); z < rows; z += 4 * helpers) {
+            if (who.x >> z & 1u) continue;
+            *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        };
+        const int j_first = helper * kAtOnce;          // (several warps: a round at a time each)
+        if (j_first >= n) zeros();                     // (there are several, so the stage is new)
+        for (int j0 = j_first; j0 < n && ok; j0 += helpers > 1 ? helpers * kAtOnce : kRounds * kAtOnce) {
           float g[kRounds][8] = {}, v[kRounds][8] = {}, weight[kRounds];
           int t[kRounds], row[kRounds];
 #pragma unroll
           for (int k = 0; k < kRounds; ++k) {
             const int j = j0 + k * kAtOnce + mine;
             row[k] = -1, t[k] = 0, weight[k] = 1.f;
-            if (j < n) {
+            if (j < n && (k == 0 || helpers == 1)) {
               row[k] = sh ? j : static_cast<int>(who.y >> 10 & 0x7FFu) + j;
               t[k] = sh ? j : token[row[k]];
               if (!sh) weight[k] = share[row[k]];
             }
           }
           // (a single round takes the other one's registers for two more parts)
-          const bool narrow = n - j0 <= kAtOnce;
+          const bool narrow = helpers > 1 || n - j0 <= kAtOnce;
           for (int s = 0; s < parts; s += narrow ? 4 : 2) {
             float4 a[kRounds][2][4];
 #pragma unroll
@@ -703,19 +724,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int k = 0; k < kRounds; ++k) {
-            if (j0 + k * kAtOnce >= n) break;
+            if (j0 + k * kAtOnce >= n || (k > 0 && helpers > 1)) break;
 #pragma unroll
             for (int c = 0; c < 8; ++c) g[k][c] = silu(g[k][c]) * v[k][c] * weight[k];
             const Terms r = terms_of(g[k], e0, e1);
-            if (j0 + k == 0) {
+            if (j0 == j_first && k == 0) {
               ok = wait_stage(i);
               if (!ok) break;
-              uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
-              for (int z = lane >> 3; z < rows; z += 4) {
-                if (who.x >> z & 1u) continue;
-                *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
-              }
+              zeros();
             }
             if (row[k] >= 0) put(r, stage, t[k], rows, e0, e1);
           }

@@ -314,3 +314,16 @@ def test_many_heavy_experts(dev):
                 ids[t, free[t]] = 9 * e + 3
                 free[t] += 1
     layer.check(layer.call(x, ids, p), x, ids, p)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 5, 10, 17, 32])
+@pytest.mark.parametrize("E,I,S", [(1, 128, 0), (1, 256, 0), (1, 512, 0), (3, 128, 128), (4, 384, 0)])
+def test_few_blocks_and_many_tokens(dev, fmt, T, E, I, S):
+    """One to a few K-blocks a CTA of the second kernel, so that 8, 4 or 2 warps form one; some tokens choose nothing."""
+    layer = Layer(dev, E, 384, I, S, fmt=fmt, seed=I)
+    x, ids, p = inputs(dev, T, 384, E, min(2, E), seed=T)
+    if T > 4:
+        ids[1] = -1
+        ids[T - 1] = -1
+    layer.check(layer.call(x, ids, p), x, ids, p)
