@@ -23,10 +23,11 @@
 //   a batch, whose second product then has too little in flight.)  Contraction runs over (expert, i), so a cluster
 //   splits one long K and its CTAs exchange one partial of z through distributed shared memory, in rank order.
 // * FP8 weights meet unquantised activations on the FP8 tensor cores: a value scaled to its block of 128 is split
-//   into E4M3 terms, v = hi + lo / 16, which take two columns of the MMA.  A bf16 value has 8 significant bits and
-//   each term holds 4, so the split is exact down to 2**-14 of the block's largest value and off by at most
-//   2**-21 of that below; a float32 h is off by at most 2**-9 of its size or 2**-21 of the block's largest.  The weights
-//   go from HBM to the tensor core without passing a register.
+//   into E4M3 terms, v = t0 + t1 / 16 (+ t2 / 256), which take two (three) columns of the MMA.  A bf16 value has 8
+//   significant bits and each term holds 4, so two terms of x are exact down to 2**-14 of the block's largest value and
+//   off by at most 2**-21 of that below.  A float32 h takes three: off by at most 2**-14 of its size or 2**-25 of the
+//   block's largest (two would leave 2**-9 and 2**-21, which z's rounding to bf16 does not hide).  bf16 weights meet h as
+//   two bf16 terms (2**-17 of it).  The weights go from HBM to the tensor core without passing a register.
 //
 // Measured with FP8 weights.  128 experts of which a token chooses 8, K 4096, I 1536: 32 tokens read the 2.11 GB of 111
 // experts in 298-302 us, 7.0 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236-239 us, 7.1 TB/s; both are
@@ -50,7 +51,7 @@ constexpr int kMaxKr = 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kBoxBytes = 16384;               // 128 weight rows x 128 bytes
 constexpr int kMaxStages = 5;                  // a stage: two boxes, the token operand that both meet, its scales
-constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows: words 0, 1 for box 0, 2, 3 for box 1
+constexpr int kSfBytes = 512;                  // scale bytes of an operand's rows: word r / 32 of row r, byte b for box b
 constexpr int kAccCol = 64;                    // tensor memory: 4 columns of ones, 4 per stage and box of scales, sums
 constexpr int kParts = 4;                      // most CTAs that share a tile of the first product
 // warps: 0 and 3 weight loads, 1 and 2 MMA issuers (one per box each), 4-7 and 8-11 as each kernel needs them
@@ -98,13 +99,27 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr)
                : "memory");
 }
-// (names the registers of the loads that it completes, see tmem_wait_ld_regs)
-__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[8], uint32_t (&o)[8]) {
+// (names the registers of the load that it completes, see tmem_wait_ld_regs)
+__device__ __forceinline__ void tmem_wait_ld_regs(uint32_t (&r)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]), "+r"(o[6]), "+r"(o[7])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
                :
                : "memory");
+}
+// Eight tokens' sums of this lane's weight row: the columns of their terms, `rows` apart, all in flight at once.
+template <int TERMS>
+__device__ __forceinline__ void sum_of_terms(uint32_t taddr, int rows, float (&v)[8]) {
+  uint32_t r[TERMS][8];
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) tmem_ld_x8(taddr + t * rows, r[t]);
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) tmem_wait_ld_regs(r[t]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = __uint_as_float(r[0][k]);
+#pragma unroll
+    for (int t = 1; t < TERMS; ++t) v[k] += __uint_as_float(r[t][k]);
+  }
 }
 // 32 rows of 16 bytes in shared memory -> four columns of tensor memory, the same in each of the four lane quadrants:
 // scale bytes, row r + 32 c of the operand in word c of row r.  The MMAs that the same thread issues next see them.
@@ -119,19 +134,24 @@ __device__ __forceinline__ void arrive_with(uint64_t* bar, uint32_t count) {
 }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Eight values f * scale -> E4M3 codes of their leading four bits and of 16 times what is left (exact in float32).
-__device__ __forceinline__ void split8(const float (&f)[8], float scale, uint2& hi, uint2& lo) {
-  uint32_t h[4], l[4];
+// Eight values f * scale -> E4M3 codes of their leading four bits, and term by term of 16 times what is left (exact in
+// float32).
+template <int TERMS>
+__device__ __forceinline__ void split8(const float (&f)[8], float scale, uint32_t (&code)[TERMS][2]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = f[2 * i] * scale, b = f[2 * i + 1] * scale;
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[i]), __NV_E4M3);
-    const float2 back = __half22float2(__half2(raw));
-    l[i] = __nv_cvt_float2_to_fp8x2(make_float2((a - back.x) * 16.f, (b - back.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+    float a = f[2 * i] * scale, b = f[2 * i + 1] * scale;
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+      code[t][i >> 1] = i & 1 ? code[t][i >> 1] | static_cast<uint32_t>(c) << 16 : c;
+      if (t + 1 < TERMS) {
+        const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        a = (a - back.x) * 16.f;
+        b = (b - back.y) * 16.f;
+      }
+    }
   }
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
 // x / (1 + exp(-x)); the argument of exp is rounded, an error of |x| 2**-24 of a term that matters up to |x| = 16 only.
@@ -182,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int boxes = PHASE == 1 ? 2 : min(p.nbox, p.K / 128 - cluster * p.nbox);
   constexpr int kConvWarps = PHASE == 1 ? 4 : 8;
   constexpr int kShares = PHASE == 1 ? 1 : kConvWarps;       // of forming an operand
-  constexpr int kTerms = FMT == kFp8 || PHASE == 2 ? 2 : 1;
+  constexpr int kTerms = (FMT == kFp8 ? 1 : 0) + PHASE;      // of a value in the operand
 
   if (tid == 0) {
     for (int s = 0; s < 2 * kMaxStages; ++s) {
@@ -373,17 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return w;
   };
-  // tokens padded to whole groups; the operand has so many rows for each term of a value
-  auto padded = [&](int n) { return kTerms == 2 ? (n + 7) & ~7 : (n + 15) & ~15; };
+  // tokens padded to whole groups; the operand has so many rows for each term of a value, 16 k in all
+  auto padded = [&](int n) { return kTerms >= 2 ? (n + 7) & ~7 : (n + 15) & ~15; };
+  auto operand_rows = [&](int n) { return (kTerms * padded(n) + 15) & ~15; };
   // Stages as large as the most tokens of an expert need: 32 tokens seldom put more than 8 on one, and a larger operand
   // would cost a stage of weights in flight.
-  const int most_rows = kTerms * padded(PHASE == 1 ? *most_tokens : p.T);
+  const int most_rows = operand_rows(PHASE == 1 ? *most_tokens : p.T);
   const int stage_bytes = 2 * kBoxBytes + ((most_rows * 128 + 1023) & ~1023);
   const int stages = min(p.stage_space / stage_bytes, PHASE == 1 ? kStages1 : kMaxStages);      // (at most kConvWarps)
   const int acc_stride = (most_rows + 31) & ~31;                   // columns of a sum
   const uint32_t sets = kAccCol + 4 * acc_stride <= static_cast<int>(p.tmem_cols) ? 2u : 1u;   // of sums, first kernel
 
-  // A CTA of the second kernel with at most half as many K-blocks as warps (and fewer than stages, so that none is used
+  // A CTA of the second kernel with at most half as many K-blocks as warps (and no more than stages, so that none is used
   // twice) has several warps form each of them, some tokens each: 10 tokens that all choose 4 experts, K and I 384, 16.2 ->
   // 13.0 us, 32 tokens x 2 of 8 experts, K 2048, I 512, 25.1 -> 23.6.  What a warp's arrival counts makes up for it.
   const int helpers = PHASE == 1 || u1 - u0 > 4 ? 1 : u1 - u0 > 2 ? 2 : u1 - u0 > 1 ? 4 : 8;
@@ -467,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true, start = true;
       for (int u = u0; u < u1 && ok;) {
         const Unit w = unit_at(u);
-        const int n = kTerms * padded(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
+        const int n = operand_rows(PHASE == 1 ? __popc(chosen[w.a].x) : p.T);
         const uint32_t d = tmem_base + kAccCol + (2 * set + b) * acc_stride;
-        const uint32_t idesc = FMT == kFp8 ? idesc_mxf8_e4m3(128, n, 0, 0) : idesc_bf16(128, n);
+        const uint32_t idesc = FMT == kFp8 ? idesc_mxf8_e4m3(128, n, 0, b) : idesc_bf16(128, n);
         if (PHASE == 1) {
           start = true;
           if (!mbar_wait(&acc_empty[set], set_phase ^ 1u, abort_flag, p.err)) break;
@@ -485,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (FMT == kFp8)
-              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem_base, sf + 2 * b, !start || k != 0);
+              mma_mxf8(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem_base, sf, !start || k != 0);
             else
               mma_bf16(d, adesc + 2 * k, bdesc + 2 * k, idesc, !start || k != 0);
           }
@@ -525,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // This lane's eight values of a token as they go into an operand: the terms' codes (or bf16 values), and the
     // exponent of their block.
     struct Terms {
-      uint32_t hi[4], lo[4];
+      uint32_t code[kTerms][FMT == kFp8 ? 2 : 4];
       int e;
     };
     auto terms_of = [&](const float (&f)[8], int e0, int e1) {
@@ -538,16 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale;
-        r.e = split_exponent(amax, -122 - min(0, min(e0, e1)), scale);
-        uint2 hi, lo;
-        split8(f, scale, hi, lo);
-        r.hi[0] = hi.x, r.hi[1] = hi.y, r.lo[0] = lo.x, r.lo[1] = lo.y;
-      } else {
+        r.e = split_exponent(amax, 4 * kTerms - 130 - min(0, min(e0, e1)), scale);      // (the last term's is -126)
+        if constexpr (FMT == kFp8) split8(f, scale, r.code);
+      } else if constexpr (FMT == kBf16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          r.hi[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-          if (kTerms == 2)
-            r.lo[i] = pack_bf16x2(f[2 * i] - __uint_as_float(r.hi[i] << 16), f[2 * i + 1] - __uint_as_float(r.hi[i] & 0xFFFF0000u));
+          const uint32_t hi = r.code[0][i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+          if constexpr (kTerms == 2)
+            r.code[1][i] = pack_bf16x2(f[2 * i] - __uint_as_float(hi << 16), f[2 * i + 1] - __uint_as_float(hi & 0xFFFF0000u));
         }
       }
       return r;
@@ -555,18 +574,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ... as row `row` of a stage's operand whose terms are `rows` apart
     auto put = [&](const Terms& r, int stage, int row, int rows, int e0, int e1) {
       uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
-      if (FMT == kFp8) {
-        *reinterpret_cast<uint2*>(operand_at(to, row, sub >> 1) + (sub & 1) * 8) = make_uint2(r.hi[0], r.hi[1]);
-        *reinterpret_cast<uint2*>(operand_at(to, rows + row, sub >> 1) + (sub & 1) * 8) = make_uint2(r.lo[0], r.lo[1]);
-        if (sub < 4) {                     // lane 0: hi for box 0, 1: hi for box 1, 2 and 3: lo, 2**-4 of it
-          const int at = sub & 2 ? rows + row : row;
-          const int byte = min(r.e + (sub & 1 ? e1 : e0) + 127 - (sub & 2 ? 4 : 0), 254);
-          *reinterpret_cast<uint32_t*>(scales + stage * kSfBytes + (at & 31) * 16 + (sub & 1) * 8 + (at >> 5) * 4) =
-              static_cast<uint32_t>(byte);
+      if constexpr (FMT == kFp8) {
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+          *reinterpret_cast<uint2*>(operand_at(to, t * rows + row, sub >> 1) + (sub & 1) * 8) = make_uint2(r.code[t][0], r.code[t][1]);
+        if (sub < kTerms) {                // a term's scales, for box 0 and box 1
+          const int at = sub * rows + row, e = r.e + 127 - 4 * sub;
+          *reinterpret_cast<uint32_t*>(scales + stage * kSfBytes + (at & 31) * 16 + (at >> 5) * 4) =
+              static_cast<uint32_t>(min(e + e0, 254) | min(e + e1, 254) << 8);
         }
       } else {
-        *reinterpret_cast<uint4*>(operand_at(to, row, sub)) = make_uint4(r.hi[0], r.hi[1], r.hi[2], r.hi[3]);
-        if (kTerms == 2) *reinterpret_cast<uint4*>(operand_at(to, rows + row, sub)) = make_uint4(r.lo[0], r.lo[1], r.lo[2], r.lo[3]);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+          *reinterpret_cast<uint4*>(operand_at(to, t * rows + row, sub)) = make_uint4(r.code[t][0], r.code[t][1], r.code[t][2], r.code[t][3]);
       }
     };
     auto exponent = [](uint32_t word, int kb) { return static_cast<int>((word >> (8 * (kb & 3))) & 255u) - 127; };
@@ -671,8 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* to = smem + stage * stage_bytes + 2 * kBoxBytes;
           for (int z = 4 * helper + (lane >> 3); z < rows; z += 4 * helpers) {
             if (who.x >> z & 1u) continue;
-            *reinterpret_cast<uint4*>(operand_at(to, z, lane & 7)) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(operand_at(to, rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t)
+              *reinterpret_cast<uint4*>(operand_at(to, t * rows + z, lane & 7)) = make_uint4(0, 0, 0, 0);
           }
         };
         const int j_first = helper * kAtOnce;          // (several warps: a round at a time each)
@@ -760,17 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + 2 * set * acc_stride;
       for (int b = 0; b < 2; ++b) {
         for (int c = 0; c < rows; c += 8) {
-          uint32_t r[8], o[8];
-          tmem_ld_x8(acc + b * acc_stride + c, r);
-          tmem_ld_x8(acc + b * acc_stride + (kTerms - 1) * rows + c, o);
-          tmem_wait_ld_regs(r, o);
+          float v[8];
+          sum_of_terms<kTerms>(acc + b * acc_stride + c, rows, v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float v = __uint_as_float(r[k]);
-            if (kTerms == 2) v += __uint_as_float(o[k]);
+          for (int k = 0; k < 8; ++k)
             // (where a wait ran out the sums are marked, so that z cannot look like an answer)
-            if (c + k < n) to[(static_cast<int64_t>(c + k) * 2 + b) * width] = ok ? v : __uint_as_float(0x7FC00000u);
-          }
+            if (c + k < n) to[(static_cast<int64_t>(c + k) * 2 + b) * width] = ok ? v[k] : __uint_as_float(0x7FC00000u);
         }
       }
       tc_fence_before();
@@ -809,15 +825,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q = warp & 3, rows = padded(p.T);
       const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kAccCol + b * acc_stride;
       for (int c = 0; c < rows; c += 8) {
-        uint32_t r[8], o[8];
-        tmem_ld_x8(acc + c, r);
-        tmem_ld_x8(acc + rows + c, o);
-        tmem_wait_ld_regs(r, o);
+        float v[8];
+        sum_of_terms<kTerms>(acc + c, rows, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float v = __uint_as_float(r[k]) + __uint_as_float(o[k]);
-          if (c + k < p.T) sums[((c + k) * boxes + b) * 128 + 32 * q + lane] = u0 < u1 ? v : 0.f;
-        }
+        for (int k = 0; k < 8; ++k)
+          if (c + k < p.T) sums[((c + k) * boxes + b) * 128 + 32 * q + lane] = u0 < u1 ? v[k] : 0.f;
       }
     }
   }
@@ -929,11 +941,13 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   a.nkb2 = a.I * kSize / 128;
   a.nkb2_shared = a.S * kSize / 128;
   a.ctas1 = sms;
-  const int rows = 2 * ((a.T + 7) / 8 * 8);      // of two terms (one term of bf16 takes no more)
+  // operand rows of either kernel's terms (one term of bf16 takes whole groups of 16 tokens)
+  const int groups = (a.T + 7) / 8 * 8;
+  const int rows1 = FMT == kFp8 ? 2 * groups : (a.T + 15) / 16 * 16, rows2 = ((FMT == kFp8 ? 3 : 2) * groups + 15) / 16 * 16;
   const int tables = kBarBytes + kMaxStages * kSfBytes + ((a.E < a.R ? a.E : a.R) + 1) * 8 + a.R * 5;
   a.tables = (tables + 1023) / 1024 * 1024;
 
-  a.stage_space = kStages1 * (2 * kBoxBytes + ((FMT == kFp8 ? rows : (a.T + 15) / 16 * 16) * 128 + 1023) / 1024 * 1024);
+  a.stage_space = kStages1 * (2 * kBoxBytes + (rows1 * 128 + 1023) / 1024 * 1024);
   const int space2 = kMostSmem - a.tables;
 
   // The second kernel: a CTA takes two 128-row tiles of W2, for which the token operand is formed once (one where K is
@@ -961,7 +975,7 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   a.sf = sf13;
   a.sf_shared = sf13_shared;
   // at least one set of sums for the most tokens; two CTAs share an SM's tensor memory
-  const int stride = (rows + 31) / 32 * 32;
+  const int stride = (rows1 + 31) / 32 * 32;
   a.tmem_cols = columns_of(kAccCol + (kAccCol + 4 * stride <= 256 ? 4 : 2) * stride);
   void* args1[] = {&m13, &s13, &a};
   const bsf_status first = launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 1>), a.ctas1, kThreads, a.tables + a.stage_space, 0, s, args1);
@@ -970,7 +984,7 @@ bsf_status launch_few(FewArgs a, const void* w13, const int32_t* sf13, const voi
   b.stage_space = space2;
   b.sf = sf2;
   b.sf_shared = sf2_shared;
-  b.tmem_cols = columns_of(kAccCol + 2 * stride);
+  b.tmem_cols = columns_of(kAccCol + 2 * ((rows2 + 31) / 32 * 32));
   void* args2[] = {&m2, &s2, &b};
   return launch_cluster(reinterpret_cast<const void*>(few_kernel<FMT, 2>), clusters * b.split, kThreads, a.tables + space2, b.split, s, args2);
 }

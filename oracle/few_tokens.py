@@ -31,22 +31,27 @@ def few_token_moe(x, ids, weights, w13, w2, shared=None, addend=None):
     return z if addend is None else z + addend
 
 
-def bound(x, ids, weights, w13, w2, shared=None, addend=None, fp8=True):
+def bound(x, ids, weights, w13, w2, shared=None, addend=None, fp8=True, terms=2):
     """Largest error of z before its rounding to bf16 (half a step, 2**-8 |z|, comes on top).
 
     First product: the tensor core rounds the running sum at most four times per instruction (32 values of E4M3, 16 of
     bf16), each by 2**-24 of the sum of magnitudes; E4M3 weights meet x as two terms (two such sums), off by 2**-21
     of the largest of the 128 values.  Then |d silu| <= 1.1 |dg|, a few float32 roundings, the split of
-    p h (2**-9 of it, 2**-21 of the largest of its 128; or the rounding to bf16, 2**-8) and the second product's sum
-    over all experts of the token.  Values of h and z below the normal range, 2**-126, may count as 0."""
+    p h into ``terms`` terms and the second product's sum over all experts of the token.  An E4M3 term is off by half a
+    step of its 4 significant bits, and what is left is at most half a step of the leading one: 2**-9 of a value with two terms,
+    2**-14 with three, or, where the last term is subnormal, half of 2**-9 / 16**(terms - 1) of a block whose largest
+    is above 224: 2**-21 and 2**-25 of that.  bf16 terms hold 8 bits: 2**-8 of a value with one, 2**-17 with two.
+    Values of h and z below the normal range, 2**-126, may count as 0."""
     T, K = x.shape
     steps = 4 / (32 if fp8 else 16) * 2.0 ** -24 * (2 if fp8 else 1)
 
-    def tail(v):
+    split = {1: 2.0 ** -4, 2: 2.0 ** -9, 3: 2.0 ** -14}[terms] if fp8 else {1: 2.0 ** -8, 2: 2.0 ** -17}[terms]
+
+    def tail(v, n=2):
         if not fp8:
             return np.zeros_like(v)
         blocks = np.abs(v).reshape(v.shape[0], -1, 128)
-        return np.repeat(blocks.max(2) * 2.0 ** -21, 128, axis=1)
+        return np.repeat(blocks.max(2) * 2.0 ** (-13 - 4 * n), 128, axis=1)
 
     def expert(rows, a13, a2, p):
         """(error of p W2 h, its sum of magnitudes) for rows of x."""
@@ -55,7 +60,7 @@ def bound(x, ids, weights, w13, w2, shared=None, addend=None, fp8=True):
         dg, du = np.split(m, 2, axis=1)
         dh = 1.1 * dg * (np.abs(u) + du) + np.abs(_silu(g)) * du + 2.0 ** -20 * np.abs(h)
         ph, dh = p * np.abs(h), p * dh
-        dh += (2.0 ** -9 if fp8 else 2.0 ** -8) * (ph + dh) + tail(ph + dh) + 2.0 ** -126
+        dh += split * (ph + dh) + tail(ph + dh, terms) + 2.0 ** -126
         return dh @ np.abs(a2).T, ph @ np.abs(a2).T
 
     err, mag = np.zeros((T, K)), np.zeros((T, K))
