@@ -733,9 +733,9 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
     sum_k weight_k * W2_e (silu(gate_e x) * (up_e x)) (+ the shared expert's) (+ ``addend`` bf16 [T, K]).
 
     Weights: w13 uint8 [E, 2 I, K] with sfb13, w2 uint8 [E, K, I] with sfb2 (``quantise_weight`` ->
-    ``prepare_weight_sf``, ``tile_weights``), or bf16 of these shapes (with ``B_TILED`` the bytes that
-    ``tile_weights`` gives) and None for both scales.  ``shared`` = (w13 [2 S, K], sfb13, w2 [K, S], sfb2) of an
-    expert that every token takes.  x is not quantised.  ``workspace`` from ``few_token_moe_workspace``, used by this
+    ``prepare_weight_sf``, ``tile_weights``), or bf16 of these shapes and None for both scales.  ``B_TILED`` says that
+    the bytes (uint8) are those of ``tile_weights``; tensors of dtype bfloat16 are rows, whatever it says, and do not mix with
+    tiled bytes.  ``shared`` = (w13 [2 S, K], sfb13, w2 [K, S], sfb2) of an expert that every token takes.  x is not quantised.  ``workspace`` from ``few_token_moe_workspace``, used by this
     call alone until it is done (default: a new one)."""
     b13, f13, b2, f2 = (None, None, None, None) if shared is None else shared
     xs, ws, ids = x.shape, w13.shape, topk_ids.shape
@@ -779,6 +779,12 @@ def few_token_moe(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, shared=None, 
                     and workspace.numel() >= need and workspace.get_device() == device)
     if not fine:
         _refuse_few(x, topk_ids, topk_weights, w13, sfb13, w2, sfb2, b13, f13, b2, f2, addend, z, workspace, need, stream)
+    if sfb13 is None and flags & B_TILED:            # (tile_weights gives bytes)
+        rows = [w.dtype is _BF16 for w in (w13, w2, b13, b2) if w is not None]
+        if all(rows):
+            flags &= ~B_TILED
+        elif any(rows):
+            raise ValueError("few_token_moe: expected all weights as tile_weights gives them, or all as bfloat16 rows")
     ldx = x.stride(0) if T > 1 else K
     if z is None:
         z = _empty((T, K), _BF16, x, stream)
