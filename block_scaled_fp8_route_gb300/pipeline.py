@@ -259,8 +259,9 @@ class MoEBlock:
 
     ``router`` = its weights bf16 [E, K], or (weights, bias float32 [E]): the logits are then a product of the block's
     own (``ops.linear``, float32).  ``few_tokens=True`` (T <= 32) runs everything after the gate as
-    ``ops.few_token_moe``, two kernels that leave x and the hidden values unquantised: closer to the weights' own
-    result than the chain, not bit-equal to it.
+    ``ops.few_token_moe`` on the same FP8 weights, two kernels that leave x and the hidden values unquantised: closer to
+    the weights' own result than the chain, not bit-equal to it.  Nothing is packed then, so ``layout``,
+    ``align_or_max_m`` and ``expected_m`` are refused with it.
 
     Every step is a ``libbsfroute.so`` call on one stream without synchronisation or allocation, so it can be
     captured.  Steps of one object share its buffers and must not overlap."""
@@ -288,6 +289,9 @@ class MoEBlock:
             raise TypeError(f"unexpected arguments {sorted(gate.keys() - self._GATE_ARGS)}")
         if few_tokens and T > ops.FEW_TOKENS:
             raise ValueError(f"few_tokens: expected T of at most {ops.FEW_TOKENS}, got {T}")
+        if few_tokens and (layout, align_or_max_m, expected_m) != (ops.CONTIGUOUS, 128, 0):
+            raise ValueError("few_tokens: layout, align_or_max_m and expected_m are those of packed rows, which a block of "
+                             "few_tokens does not have")
         router, router_bias = router if isinstance(router, (tuple, list)) else (router, None)
         if router is not None and (router.dtype != torch.bfloat16 or router.shape != (E, K)):
             raise ValueError(f"router: expected bfloat16 weights {(E, K)}, got {router.dtype} {tuple(router.shape)}")
