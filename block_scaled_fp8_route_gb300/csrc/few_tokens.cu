@@ -230,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // What a K-block of the first product costs with n tokens.  Forming an FP8 operand (two terms of each value, a
   // maximum of each block) takes longer than loading its weights beyond 8 tokens: 32 tokens of which all choose one
   // of 64 experts (K 4096, I 1536) take 435 us in CTAs of equal K-blocks and 210 in these, with a shared expert of 1536
-  // 435 and 203; the 435 with two stages for such operands, too.  bf16 values are copied (343 either way).  At most
-  // 113 further costs in all (9 tokens each of 1024 assignments).
+  // 435 and 203; the 435 with two stages for such operands, too.  bf16 values are copied (343 either way).  Costs
+  // beyond one: at most 3 of an expert, 96 of 32 experts (a byte) and 122 of 1024 assignments (40 experts of 25 tokens, one
+  // of 24).
   auto cost = [](uint32_t n) -> uint32_t { return FMT == kFp8 ? (n + kUnitTokens - 1) / kUnitTokens : 1u; };
 
   // ---------------------------------------------------------------- routing, in every CTA
