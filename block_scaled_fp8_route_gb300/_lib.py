@@ -68,6 +68,7 @@ SIGNATURES = {
                                    _p, _p, _p, _i64, _p, _i64, _p, _size, _c_int, _p]),
     "bsf_linear": (_c_int, [_p, _c_int, _i64, _i64, _i64, _p, _i64, _i64, _p, _c_int, _c_int, _p, _i64, _p, _c_int,
                             _i64, _c_int, _p]),
+    "bsf_linear_form": (_c_int, [_i64, _i64, _i64, _c_int, _c_int, _p]),
     "bsf_dense_gemm": (_c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p]),
 }
 

@@ -958,6 +958,9 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, bool f32, bool residual, const
   return best;
 }
 
+// Tokens of a split tile: equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * tok < T).
+int64_t tokens_per_chunk(int64_t T, int64_t chunks) { return ((T + chunks - 1) / chunks + 15) / 16 * 16; }
+
 size_t size_of(int type) { return type == BSF_TYPE_F32 ? 4 : 2; }
 bool known(int type) { return type == BSF_TYPE_F32 || type == BSF_TYPE_BF16 || type == BSF_TYPE_F16; }
 
@@ -965,6 +968,21 @@ bool known(int type) { return type == BSF_TYPE_F32 || type == BSF_TYPE_BF16 || t
 }  // namespace bsf
 
 using namespace bsf;
+
+extern "C" bsf_status bsf_linear_form(int64_t T, int64_t N, int64_t K, int y_type, int residual, int64_t* form) {
+  if (T <= 0 || N <= 0 || K <= 0 || !known(y_type) || !form) return BSF_ERR_INVALID_ARGUMENT;
+  if (!fits_rows(T, N) || K > kMaxRowWidth || T > kMaxRows - 256) return BSF_ERR_UNSUPPORTED;
+  const LinearLimits* limits;
+  const bsf_status st = linear_limits(&limits);
+  if (st != BSF_OK) return st;
+  const Plan plan = choose_plan(T, N, K, y_type == BSF_TYPE_F32, residual != 0, *limits);
+  const int64_t ntn = (N + kTileW - 1) / kTileW, chunks = (T + plan.tok - 1) / plan.tok;
+  form[0] = plan.pair;
+  form[1] = plan.pair ? plan.tok : tokens_per_chunk(T, chunks);
+  form[2] = plan.split;
+  form[3] = chunks * (plan.pair ? (ntn + 1) / 2 : ntn);
+  return BSF_OK;
+}
 
 extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, int64_t ldx, const void* w, int64_t N,
                                  int64_t ldw, const void* bias, int bias_type, int activation, const void* residual,
@@ -1048,8 +1066,7 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   p.N = static_cast<int>(N);
   p.nkb = static_cast<int>(nkb);
   p.chunks = static_cast<int>(chunks);
-  // equal chunks (the last may be shorter, never empty: (chunks - 1) * per <= (chunks - 1) * tok < T)
-  p.per = static_cast<int>(((T + chunks - 1) / chunks + 15) / 16 * 16);
+  p.per = static_cast<int>(tokens_per_chunk(T, chunks));
   p.split = plan.split;
   const int stage_bytes = (kTileW + p.per) * kRowBytes;
   const size_t smem = p.per <= 64 ? kHalfSmemBytes : kSmemBytes;

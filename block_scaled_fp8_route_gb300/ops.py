@@ -863,3 +863,11 @@ def linear(x, w, bias=None, activation=None, residual=None, out=None, out_dtype=
     if status:
         _lib.check(status, "linear")
     return out
+
+
+def linear_form(T, N, K, out_dtype=torch.bfloat16, residual=False):
+    """How ``linear`` multiplies [T, K] by [N, K] on the current device: (pairs, tokens, split, tiles), that is whether CTA
+    pairs take tiles of 256 weight rows, the most tokens of a tile, the CTAs that share a tile's K otherwise, and the tiles."""
+    form = (ctypes.c_int64 * 4)()
+    _lib.check(_lib.load().bsf_linear_form(T, N, K, _LINEAR_TYPES.get(out_dtype, -1), int(bool(residual)), form), "linear_form")
+    return bool(form[0]), form[1], form[2], form[3]

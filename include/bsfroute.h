@@ -710,6 +710,15 @@ bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, int64_t ldx
                       int64_t ldw, const void* bias, int bias_type, int activation, const void* residual, int64_t ldr,
                       void* y, int y_type, int64_t ldy, int flags, bsf_stream_t stream);
 
+/*
+ * bsf_linear_form — how bsf_linear multiplies T x K by N x K on the current
+ * device, for tests and tuning: form[0] 1 where CTA pairs take tiles of 256
+ * weight rows, 0 where a cluster of form[2] CTAs splits the K of a tile of 128;
+ * form[1] the most tokens of a tile; form[3] the number of tiles.  `residual`:
+ * whether there is one.  No launch; host arithmetic after a first query.
+ */
+bsf_status bsf_linear_form(int64_t T, int64_t N, int64_t K, int y_type, int residual, int64_t* form);
+
 #ifdef __cplusplus
 }
 #endif
