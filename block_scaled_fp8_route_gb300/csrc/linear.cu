@@ -1073,7 +1073,9 @@ extern "C" bsf_status bsf_linear(const void* x, int type, int64_t T, int64_t K, 
   p.stages = (static_cast<int>(smem) - 1024 - kBarBytes) / stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.acc_stride = acc_columns(p.per);
-  // (an issuer or a run without a K-block would leave its accumulator unwritten: every run has 15 or more, or is alone)
+  // (an issuer or a run without a K-block would leave its accumulator unwritten.  The K-blocks of two issuers, of one CTA or
+  // of two, differ by at most 1, and runs = ceil(most / 16), so where there are several runs an issuer has at least
+  // 16 (runs - 1) K-blocks and each of its runs 8 or more)
   p.issuers = split_issuers(nkb, p.split);
   p.runs = issuer_runs(nkb, p.split, y_type == BSF_TYPE_F32);
   p.stages = p.stages / p.issuers * p.issuers;
