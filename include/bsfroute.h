@@ -649,7 +649,7 @@ bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, 
  *                 with E = 1 and S in place of I; S == 0: none.
  *   addend        bf16 [T, K], row stride ldc >= K, or NULL: added before the
  *                 one rounding (for instance the residual stream).  It may be z.
- *   z             bf16 [T, K], row stride ldz >= K (output).
+ *   z             bf16 [T, K], row stride ldz >= K (output).  It may be x.
  *   workspace     bsf_few_token_moe_workspace_bytes() bytes, 16-byte aligned,
  *                 any contents; used from the call's start on its stream to its
  *                 end there, so calls that may overlap need one each.
@@ -659,8 +659,11 @@ bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, 
  * its own size or 2^-25 of the largest of its 128; bf16 weights meet h as two bf16
  * terms, off by at most 2^-17 of its own size.  The weight topk_weights enters before that.  The order
  * of all sums is fixed: results are bit-identical from run to run.  A token
- * whose x holds an infinity or NaN gets a z that is not finite; others are
- * not affected.
+ * that chooses an expert and whose x holds an infinity or NaN gets a z that is
+ * not finite; others are not affected, and x and weights of what chooses none are
+ * not looked at.  Weights are finite: the second product runs over all chosen
+ * experts with zeros for the tokens that did not choose one, so an infinity or
+ * NaN in a chosen expert's w2 reaches every token.
  * T <= 32, kr <= 32, E <= 1024 (else BSF_ERR_UNSUPPORTED); K, I and S
  * multiples of 128; 16-byte aligned x and weights; z and addend need only their element
  * alignment (8 bytes and row strides of 4 elements are faster).  flags:
