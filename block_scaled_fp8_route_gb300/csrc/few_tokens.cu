@@ -30,10 +30,12 @@
 //   two bf16 terms (2**-17 of it).  The weights go from HBM to the tensor core without passing a register.
 //
 // Measured with FP8 weights.  128 experts of which a token chooses 8, K 4096, I 1536: 32 tokens read the 2.11 GB of 111
-// experts in 298-302 us, 7.0 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236-239 us, 7.1 TB/s; both are
-// bound by HBM.  One token of the first layer reads 152 MB in 34 us: its first kernel streams at 7.7 TB/s, and some 6 us
-// are the exit, launch and routing between the two kernels, the first operand, and the exchange at the end.
-// Multiplying less gains next to nothing there (3 of 4 MMAs left out: 1 us).
+// experts in 300-304 us, 7.0 TB/s; 256 experts, K 7168, I 2048 and a shared one, 5 tokens: 1.69 GB in 236-239 us, 7.1 TB/s; both are
+// bound by HBM.  One token of the first layer reads 152 MB in 34 us.  Time stamps of its CTAs (medians): the first kernel's
+// routing 1.7, first load and operand 3.1, products 13.2, sums 0.6; the second's start 1.1, routing 2.0, wait for the last
+// partial sums 1.1, first operand 2.1, products 7.0, exchange 1.5: 20 us of products in a chain of 13 us of latencies.
+// Multiplying less gains next to nothing there (3 of 4 MMAs left out: 1 us).  The third term of h costs 0.1-0.3 us of a
+// small layer, 0.6 % of one token, 0.8 % of 32 and 2.2 % where 32 tokens all choose 8 experts (112 -> 114.5 us).
 #include <algorithm>
 #include <cfloat>
 

@@ -17,8 +17,8 @@
 // * Pairs (many tokens).  Two CTAs multiply 256 weight rows x up to 256 tokens with one cta_group::2 MMA per 16 K;
 //   two accumulators let a tile's epilogue run under the next tile's MMAs.  What an SM takes in from L2, 53 bytes a cycle
 //   (the same from its own loads and by multicast), binds these tiles: 256 x 256 x 64 brings each SM 32 KB, 610
-//   cycles of loads for 512 of MMAs.  8192 x 7168 x 4096 with bias and residual takes 266-275 us in short runs, 1.75-1.81
-//   PFLOP/s, 92-95 % of the measured burst, and 300-330 where the power cap holds; 8192 x 256 x 7168 (tiles of 112 tokens in
+//   cycles of loads for 512 of MMAs.  8192 x 7168 x 4096 with bias and residual takes 261-275 us in short runs, 1.75-1.84
+//   PFLOP/s, 90-95 % of the measured burst, and 300-330 where the power cap holds; 8192 x 256 x 7168 (tiles of 112 tokens in
 //   one round of CTAs) 30.5 us, 986 TFLOP/s; 777 x 4100 x 1416 with gelu 16.0-16.5 us.  With few K-blocks a tile is bound by
 //   its epilogue: 8192 x 2048 x 512 21 us, with a residual, whose loads two warps a scheduler do not hide, 31.
 #include "cluster.cuh"
@@ -779,6 +779,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           finish<OUT, kResidual>(p.e, v[i], w, bias, tok0 + c, min(32, rows - c), n, p.N);
         }
       } else {
+        // (16-bit outputs take all of K in the accumulators of the issuers: what they cut off is far below the rounding.
+        // 1024 x 2048 x 4096 in bf16: 0.12 % of the outputs are not the one nearest to the exact result, 0.22 % with a
+        // library bf16 product, 0.035 % with a rounded float32 one; runs would take 128 registers for their sums)
         const uint32_t taddr = quad + acc * set_cols;
         for (int c = c_first; c < c_last; ++c) {
           uint32_t r[32];
@@ -910,8 +913,11 @@ bool runs_fit(int64_t nkb, int split, int64_t per, bool f32) {
 
 // Which kernel a product takes, by the time each would need (nanoseconds).  The constants are fitted to 2200 products
 // of 1 .. 8192 tokens, 16 .. 8192 weight rows and K of 64 .. 8192, drawn by their logarithms, with weights that come from
-// HBM, each timed in every form that could win (25000 in all).  On 1500 others the choice is 1.0 % above the best
-// form on average, at worst 18 %.  Both sides: 64 x 4096 x 4096 takes 12.2 us split and 14.7 in pairs, 256 x 4096 x 4096
+// HBM, each timed in every form that could win (25000 in all), none of them with an activation.  On 1500 others the choice is
+// 1.0 % above the best form on average, at worst 18 %; on 9700 with gelu, silu or gelu_tanh 0.9 %, at worst 33 %
+// (7592 x 812 x 72 with residual, float32, gelu: 30.1 us in tiles of 80 tokens, 22.7 of 64).  It ranks forms; it is not
+// a clock: where the epilogue binds, all forms take up to twice what it says (777 x 4100 x 1416 with gelu 16 us, not
+// 10.5; 8192 x 2048 x 512 with residual 31, not 14.4).  Both sides: 64 x 4096 x 4096 takes 12.2 us split and 14.7 in pairs, 256 x 4096 x 4096
 // 16.6 and 14.3, 1024 x 256 x 7168 10.9 and 21.0, 777 x 4100 x 1416 33.5 and 13.0.
 struct Plan {
   bool pair;

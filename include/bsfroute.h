@@ -699,7 +699,8 @@ bsf_status bsf_few_token_moe(const void* x, int64_t T, int64_t K, int64_t ldx, c
  *   y         [T, N] (output) of y_type BSF_TYPE_F32, BF16 or F16, row stride
  *             ldy >= N; nothing else is written.  It may not overlap x or w.
  * FP32 accumulation on the tensor cores (float32 y: in runs of at most 1024
- * values, added in float32, as the cores cut a long sum off); bias, activation and residual in
+ * values, added in float32, as the cores cut a long sum off; 16-bit y: in one or
+ * two runs, which moves some results by a step of y's type); bias, activation and residual in
  * float32 on the sum, then one rounding (to nearest even) to y's type.  The order
  * of sums is fixed: results are bit-identical from run to run.  Infinities
  * and NaN go through the arithmetic as they are.  x and w 16-byte aligned, ldx
