@@ -80,3 +80,32 @@ def test_values_far_apart_in_a_block(dev):
     x[4] = torch.finfo(torch.bfloat16).tiny
     x[5] *= 2.0 ** 20
     layer.check(layer.call(x, ids, p), x, ids, p)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("T", [1, 9, 16, 17, 32])
+def test_every_block_of_weights_has_an_exponent_of_its_own(dev, fmt, T):
+    """Neighbouring tiles of a CTA (gate and up rows; two tiles of w2) meet one operand with different scales."""
+    E, K, I, S = 5, 1536, 384, 256
+    layer = TermsLayer(dev, E, K, I, S, fmt=fmt)
+    g = torch.Generator().manual_seed(T)
+
+    def made(n, rows, inner):
+        w = torch.randn(n, rows // 128, 128, inner // 128, 128, generator=g) * 0.05
+        w *= torch.exp2(torch.randint(-4, 5, (n, rows // 128, 1, inner // 128, 1), generator=g).float())
+        w = w.view(n, rows, inner).to(torch.bfloat16).to(dev)
+        if fmt == "bf16":
+            return ops.tile_weights(w), None, f64(w)
+        q, sf128 = ops.quantise_weight(w)
+        bq, bsf = oracle.quantise.quantise_weight(w.cpu().view(torch.int16).numpy().view(np.uint16))
+        assert len(np.unique(bsf)) > 4
+        return ops.tile_weights(q), ops.prepare_weight_sf(sf128, inner), np.stack(
+            [oracle.gemm.dequant_weight(bq[e], bsf[e]) for e in range(n)])
+
+    layer.w13, layer.sf13, layer.wide13 = made(E, 2 * I, K)
+    layer.w2, layer.sf2, layer.wide2 = made(E, K, I)
+    a, b = made(1, 2 * S, K), made(1, K, S)
+    layer.shared = tuple(None if t is None else t[0] for t in (a[0], a[1], b[0], b[1]))
+    layer.wide_shared = (a[2][0], b[2][0])
+    x, ids, p = inputs(dev, T, K, E, 2, T)
+    layer.check(layer.call(x, ids, p), x, ids, p)
