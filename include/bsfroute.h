@@ -656,7 +656,8 @@ bsf_status bsf_dense_gemm(const uint8_t* a, const int32_t* sfa, int64_t sfa_ld, 
  * FP32 accumulation on the tensor cores; an E4M3 weight meets x as two E4M3
  * terms, exact for values within 2^-14 of the largest of their 128 and off by
  * at most 2^-21 of that largest below, and h as three, off by at most 2^-14 of
- * its own size or 2^-25 of the largest of its 128; bf16 weights meet h as two bf16
+ * its own size or 2^-25 of the largest of its 128 (a scale of those 128 times that
+ * of their weights beyond 2^127 counts as 2^127); bf16 weights meet h as two bf16
  * terms, off by at most 2^-17 of its own size.  The weight topk_weights enters before that.  The order
  * of all sums is fixed: results are bit-identical from run to run.  A token
  * that chooses an expert and whose x holds an infinity or NaN gets a z that is
